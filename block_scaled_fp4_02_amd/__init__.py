@@ -25,7 +25,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe_nvfp4.so")
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(6)
 MOE_DTYPE_BF16, MOE_DTYPE_F32 = 0, 1
 MOE_GS_STATIC, MOE_GS_DYNAMIC = 0, 1
-MOE_EPI_NONE, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_NVFP4 = 0, 1, 2
+MOE_EPI_NONE, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_NVFP4, MOE_EPI_SWIGLU_FP8 = 0, 1, 2, 3
 MOE_LAYOUT_ROWMAJOR, MOE_LAYOUT_PACKED = 0, 1
 
 EXPORTED = [
@@ -36,6 +36,10 @@ EXPORTED = [
     "moe_grouped_gemm_nvfp4_can_implement", "moe_grouped_gemm_nvfp4", "moe_grouped_gemm_nvfp4_noalloc",
     "moe_pack_weights_nvfp4_bytes", "moe_pack_weights_nvfp4",
     "moe_finalize",
+    "moe_quantize_fp8", "moe_quantize_fp8_weights", "moe_fp8_token_blocks", "moe_quantize_fp8_tokens",
+    "moe_grouped_gemm_fp8_can_implement", "moe_grouped_gemm_fp8",
+    "moe_grouped_wgrad_fp8_can_implement", "moe_grouped_wgrad_fp8",
+    "moe_balance_loss_workspace", "moe_balance_loss", "moe_balance_loss_backward",
 ]
 
 
@@ -60,6 +64,23 @@ class moe_gemm_args(C.Structure):
     ]
 
 
+class moe_gemm_fp8_args(C.Structure):
+    _fields_ = [
+        ("A", C.c_void_p), ("A_sf", C.c_void_p), ("A_rows", C.c_void_p), ("rows_A", C.c_int64),
+        ("B", C.c_void_p), ("B_sf", C.c_void_p), ("expert_offsets", C.c_void_p),
+        ("E", C.c_int32), ("N", C.c_int32), ("K", C.c_int32), ("epilogue", C.c_int32),
+        ("R", C.c_int64), ("D", C.c_void_p), ("D_sf", C.c_void_p),
+    ]
+
+
+class moe_wgrad_fp8_args(C.Structure):
+    _fields_ = [
+        ("Y", C.c_void_p), ("Y_sf", C.c_void_p), ("X", C.c_void_p), ("X_sf", C.c_void_p),
+        ("expert_offsets", C.c_void_p), ("E", C.c_int32), ("N", C.c_int32), ("K", C.c_int32),
+        ("D_dtype", C.c_int32), ("R", C.c_int64), ("D", C.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -73,6 +94,7 @@ def lib():
         L = C.CDLL(LIB_PATH)
         P, i32, i64, sz = C.c_void_p, C.c_int, C.c_int64, C.c_size_t
         args_p = C.POINTER(moe_gemm_args)
+        fp8_p, wgrad_p = C.POINTER(moe_gemm_fp8_args), C.POINTER(moe_wgrad_fp8_args)
         sig = {
             "moe_status_string": (C.c_char_p, [i32]),
             "moe_last_hip_error": (i32, []),
@@ -88,6 +110,17 @@ def lib():
             "moe_pack_weights_nvfp4_bytes": (sz, [i64, i32]),
             "moe_pack_weights_nvfp4": (i32, [P, P, i64, i32, P, P]),
             "moe_finalize": (i32, [P, i64, P, P, i32, i32, i32, P, P]),
+            "moe_quantize_fp8": (i32, [P, i32, i64, i64, P, P, P]),
+            "moe_quantize_fp8_weights": (i32, [P, i32, i32, i32, i32, P, P, P, P, P]),
+            "moe_fp8_token_blocks": (i64, [i64, i32]),
+            "moe_quantize_fp8_tokens": (i32, [P, i32, i64, P, P, i32, i64, i64, P, P, P]),
+            "moe_grouped_gemm_fp8_can_implement": (i32, [fp8_p]),
+            "moe_grouped_gemm_fp8": (i32, [fp8_p, P]),
+            "moe_grouped_wgrad_fp8_can_implement": (i32, [wgrad_p]),
+            "moe_grouped_wgrad_fp8": (i32, [wgrad_p, P]),
+            "moe_balance_loss_workspace": (sz, [i32, i32, i32, i32]),
+            "moe_balance_loss": (i32, [P, P, i32, i32, i32, P, i32, P, P, P, P, P, sz, P]),
+            "moe_balance_loss_backward": (i32, [P, i32, i32, P, i32, P, P, P, P, P, P, i32, P, P]),
         }
         for name, (res, argt) in sig.items():
             fn = getattr(L, name)
@@ -199,6 +232,172 @@ def moe_finalize(Y, topk_w, token_slot_row, out, stream=None):
     H = out.shape[1]
     _check("moe_finalize", lib().moe_finalize(
         _p(Y), Y.shape[0], _p(topk_w), _p(token_slot_row), T, k, H, _p(out), _stream(stream)))
+
+
+_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+
+
+def _fp8_blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def _dense(fn: str, **tensors):
+    """The library reads raw pointers: every tensor given has to be dense, of the named dtype and on
+    one device, and what is read 16 bytes at a time (codes and bf16 or f32 data) aligned to that."""
+    device = None
+    for name, (t, dtypes) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype not in dtypes or not t.is_contiguous() or (device is not None and t.device != device) or (
+                dtypes in (_U8, _REAL, _BF16) and t.data_ptr() % 16):
+            raise MoeError(fn, MOE_ERR_UNSUPPORTED, f"{name}: a dense, aligned tensor of {dtypes} on one device is needed, got "
+                           f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+        device = t.device
+
+
+def _current(fn: str, t):
+    """Kernels are launched on the current device: its tensors only."""
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise MoeError(fn, MOE_ERR_UNSUPPORTED, f"tensors of the current device are needed, got {t.device}")
+
+
+_U8, _MASK, _I32, _F32 = (torch.uint8,), (torch.uint8, torch.bool), (torch.int32,), (torch.float32,)
+_BF16, _REAL = (torch.bfloat16,), (torch.bfloat16, torch.float32)
+
+
+def _sized(fn: str, ok: bool, what: str):
+    if not ok:
+        raise MoeError(fn, MOE_ERR_SHAPE, what)
+
+
+def moe_quantize_fp8(x, q, sf, stream=None):
+    """x [rows, C] bf16 or f32 -> q [rows, C] u8 E4M3 codes, sf [rows, ceil(C/128)] f32 scales."""
+    _dense("moe_quantize_fp8", x=(x, _REAL), q=(q, _U8), sf=(sf, _F32))
+    rows, cols = x.shape
+    _sized("moe_quantize_fp8", q.numel() == rows * cols and sf.numel() == rows * _fp8_blocks(cols), "q or sf size")
+    _current("moe_quantize_fp8", x)
+    _check("moe_quantize_fp8", lib().moe_quantize_fp8(_p(x), _DTYPES[x.dtype], rows, cols, _p(q), _p(sf), _stream(stream)))
+
+
+def moe_quantize_fp8_weights(w, q, sf, qt=None, sft=None, stream=None):
+    """w [E, N, K] bf16 or f32 -> q, sf with one scale per 128 x 128 tile; qt [E, K, N] and sft
+    receive the transposed copy."""
+    _dense("moe_quantize_fp8_weights", w=(w, _REAL), q=(q, _U8), sf=(sf, _F32), qt=(qt, _U8), sft=(sft, _F32))
+    E, N, K = w.shape
+    tiles = E * _fp8_blocks(N) * _fp8_blocks(K)
+    _sized("moe_quantize_fp8_weights", all(t is None or t.numel() == n for t, n in (
+        (q, w.numel()), (sf, tiles), (qt, w.numel()), (sft, tiles))), "an output's size")
+    _current("moe_quantize_fp8_weights", w)
+    _check("moe_quantize_fp8_weights", lib().moe_quantize_fp8_weights(
+        _p(w), _DTYPES[w.dtype], E, N, K, _p(q), _p(sf), _p(qt), _p(sft), _stream(stream)))
+
+
+def moe_fp8_token_blocks(R: int, E: int) -> int:
+    return lib().moe_fp8_token_blocks(int(R), E)
+
+
+def moe_quantize_fp8_tokens(x, expert_offsets, R, q, sf, rows=None, stream=None):
+    """x [rows_x, C] -> q [blocks, C, 128], sf [blocks, C]: blocks of 128 permuted rows of a group,
+    one scale per column (blocks = moe_fp8_token_blocks(R, E))."""
+    _dense("moe_quantize_fp8_tokens", x=(x, _REAL), expert_offsets=(expert_offsets, _I32), q=(q, _U8), sf=(sf, _F32), rows=(rows, _I32))
+    rows_x, cols = x.shape
+    E = expert_offsets.numel() - 1
+    blocks = moe_fp8_token_blocks(R, E)
+    _sized("moe_quantize_fp8_tokens", q.numel() >= blocks * cols * 128 and sf.numel() >= blocks * cols
+           and (rows is None or rows.numel() >= R), "q, sf or rows size")
+    _current("moe_quantize_fp8_tokens", x)
+    _check("moe_quantize_fp8_tokens", lib().moe_quantize_fp8_tokens(
+        _p(x), _DTYPES[x.dtype], rows_x, _p(rows), _p(expert_offsets), E, int(R), cols, _p(q), _p(sf), _stream(stream)))
+
+
+def make_gemm_fp8_args(A, A_sf, B, B_sf, expert_offsets, R, epilogue, D=None, D_sf=None, A_rows=None) -> moe_gemm_fp8_args:
+    """A [rows_A, K] / A_sf from moe_quantize_fp8, B [E, N, K] / B_sf from moe_quantize_fp8_weights;
+    D bf16 [R, N] (NONE), or u8 [R, N/2] with D_sf f32 [R, N/256] (SWIGLU_FP8).  The tensors must
+    outlive the arguments' use."""
+    fp8_act = epilogue == MOE_EPI_SWIGLU_FP8
+    _dense("make_gemm_fp8_args", A=(A, _U8), A_sf=(A_sf, _F32), B=(B, _U8), B_sf=(B_sf, _F32), expert_offsets=(expert_offsets, _I32),
+           D=(D, _U8 if fp8_act else _BF16), D_sf=(D_sf, _F32), A_rows=(A_rows, _I32))
+    E, N, K = B.shape
+    rows_A, R, kb = A.shape[0], int(R), _fp8_blocks(K)
+    _sized("make_gemm_fp8_args", A.shape[1] == K and A_sf.numel() == rows_A * kb and B_sf.numel() == E * _fp8_blocks(N) * kb
+           and expert_offsets.numel() == E + 1 and (A_rows is None or A_rows.numel() >= R)
+           and (D is None or D.numel() >= R * (N // 2 if fp8_act else N))
+           and (D_sf is None or D_sf.numel() >= R * (N // 256)), "operand sizes do not agree")
+    _current("make_gemm_fp8_args", A)
+    return moe_gemm_fp8_args(A.data_ptr(), A_sf.data_ptr(), A_rows.data_ptr() if A_rows is not None else None, rows_A,
+                             B.data_ptr(), B_sf.data_ptr(), expert_offsets.data_ptr(), E, N, K, epilogue, R,
+                             D.data_ptr() if D is not None else None, D_sf.data_ptr() if D_sf is not None else None)
+
+
+def moe_grouped_gemm_fp8_can_implement(args: moe_gemm_fp8_args) -> int:
+    return lib().moe_grouped_gemm_fp8_can_implement(C.byref(args))
+
+
+def moe_grouped_gemm_fp8(args: moe_gemm_fp8_args, stream=None):
+    _check("moe_grouped_gemm_fp8", lib().moe_grouped_gemm_fp8(C.byref(args), _stream(stream)))
+
+
+def make_wgrad_fp8_args(Y, Y_sf, X, X_sf, expert_offsets, R, D) -> moe_wgrad_fp8_args:
+    """Y [blocks, N, 128] / Y_sf and X [blocks, K, 128] / X_sf from moe_quantize_fp8_tokens over the
+    same expert_offsets and R; D [E, N, K] f32 or bf16."""
+    _dense("make_wgrad_fp8_args", Y=(Y, _U8), Y_sf=(Y_sf, _F32), X=(X, _U8), X_sf=(X_sf, _F32), expert_offsets=(expert_offsets, _I32), D=(D, _REAL))
+    E, N, K = D.shape
+    blocks = moe_fp8_token_blocks(R, E)
+    _sized("make_wgrad_fp8_args", expert_offsets.numel() == E + 1 and Y.numel() >= blocks * N * 128
+           and Y_sf.numel() >= blocks * N and X.numel() >= blocks * K * 128 and X_sf.numel() >= blocks * K,
+           "operand sizes do not agree")
+    _current("make_wgrad_fp8_args", D)
+    return moe_wgrad_fp8_args(Y.data_ptr(), Y_sf.data_ptr(), X.data_ptr(), X_sf.data_ptr(), expert_offsets.data_ptr(),
+                              E, N, K, _DTYPES[D.dtype], int(R), D.data_ptr())
+
+
+def moe_grouped_wgrad_fp8_can_implement(args: moe_wgrad_fp8_args) -> int:
+    return lib().moe_grouped_wgrad_fp8_can_implement(C.byref(args))
+
+
+def moe_grouped_wgrad_fp8(args: moe_wgrad_fp8_args, stream=None):
+    _check("moe_grouped_wgrad_fp8", lib().moe_grouped_wgrad_fp8(C.byref(args), _stream(stream)))
+
+
+def moe_balance_loss_workspace(T: int, E: int, k: int, S: int) -> int:
+    return lib().moe_balance_loss_workspace(T, E, k, S)
+
+
+def moe_balance_loss(logits, topk_ids, counts, coef, loss, seq_offsets=None, token_mask=None, ws=None, stream=None):
+    """logits [T, E] f32, topk_ids [T, k] i32, seq_offsets [S+1] i32 or None (S = 1), token_mask [T] u8
+    or None -> counts [S, E] i32, coef [S, E] f32 (for the backward pass), loss [1] f32."""
+    _dense("moe_balance_loss", logits=(logits, _F32), topk_ids=(topk_ids, _I32), counts=(counts, _I32), coef=(coef, _F32), loss=(loss, _F32),
+           seq_offsets=(seq_offsets, _I32), token_mask=(token_mask, _MASK))
+    (T, E), k = logits.shape, topk_ids.shape[1]
+    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    _sized("moe_balance_loss", topk_ids.shape[0] == T and counts.numel() == S * E and coef.numel() == S * E
+           and loss.numel() >= 1 and (token_mask is None or token_mask.numel() == T), "operand sizes do not agree")
+    _current("moe_balance_loss", logits)
+    if ws is None:
+        ws = _ws(moe_balance_loss_workspace(T, E, k, S), logits.device)
+    _check("moe_balance_loss", lib().moe_balance_loss(
+        _p(logits), _p(topk_ids), T, E, k, _p(seq_offsets), S, _p(token_mask), _p(counts), _p(coef), _p(loss),
+        _p(ws), ws.numel(), _stream(stream)))
+
+
+def moe_balance_loss_backward(logits, coef, grad_loss, dlogits, seq_offsets=None, token_mask=None,
+                              topk_ids=None, topk_w=None, d_topk_w=None, stream=None):
+    """dlogits [T, E] from grad_loss [1] and coef (moe_balance_loss); with topk_ids, topk_w and
+    d_topk_w [T, k] the gradient of the routing weights is added in the same pass."""
+    _dense("moe_balance_loss_backward", logits=(logits, _F32), coef=(coef, _F32), grad_loss=(grad_loss, _F32), dlogits=(dlogits, _F32),
+           seq_offsets=(seq_offsets, _I32), token_mask=(token_mask, _MASK), topk_ids=(topk_ids, _I32), topk_w=(topk_w, _F32),
+           d_topk_w=(d_topk_w, _F32))
+    T, E = logits.shape
+    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    k = 1 if d_topk_w is None else d_topk_w.shape[1]
+    _sized("moe_balance_loss_backward", coef.numel() == S * E and grad_loss.numel() >= 1 and dlogits.shape == logits.shape
+           and (token_mask is None or token_mask.numel() == T)
+           and (d_topk_w is None or all(t is not None and t.shape == (T, k) for t in (topk_ids, topk_w, d_topk_w))),
+           "operand sizes do not agree")
+    _current("moe_balance_loss_backward", logits)
+    _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
+        _p(logits), T, E, _p(seq_offsets), S, _p(token_mask), _p(coef), _p(grad_loss), _p(topk_ids), _p(topk_w),
+        _p(d_topk_w), k, _p(dlogits), _stream(stream)))
 
 
 # ---- allocating helpers ------------------------------------------------------------
@@ -373,6 +572,120 @@ class MoELayerPlan:
         allocates nothing and records no memory-set node: every buffer is cleared or written
         by the library's own kernels."""
         self.forward(logits, x)              # one eager pass first (lazy initialisation)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            self.forward(logits, x)
+        torch.cuda.synchronize()
+        return g
+
+
+@dataclass
+class FP8Tensor:
+    """Device FP8 tensor: E4M3 codes u8 and f32 scales, one per 128 elements of the contraction (rows
+    [rows, C] / [rows, ceil(C/128)], weights [E, N, K] / one per 128 x 128 tile, or token blocks
+    [blocks, C, 128] / [blocks, C])."""
+    q: torch.Tensor
+    sf: torch.Tensor
+
+
+def quantize_fp8_alloc(x: torch.Tensor, stream=None) -> FP8Tensor:
+    rows, cols = x.shape
+    out = FP8Tensor(torch.empty(rows, cols, dtype=torch.uint8, device=x.device),
+                    torch.empty(rows, _fp8_blocks(cols), dtype=torch.float32, device=x.device))
+    moe_quantize_fp8(x, out.q, out.sf, stream)
+    return out
+
+
+def quantize_fp8_weights_alloc(w: torch.Tensor, transposed=False, stream=None):
+    """FP8Tensor of w [E, N, K]; with `transposed` the pair (W, W^T) from one pass over w."""
+    E, N, K = w.shape
+    z = lambda a, b: FP8Tensor(torch.empty(E, a, b, dtype=torch.uint8, device=w.device),
+                               torch.empty(E, _fp8_blocks(a), _fp8_blocks(b), dtype=torch.float32, device=w.device))
+    out = z(N, K)
+    if not transposed:
+        moe_quantize_fp8_weights(w, out.q, out.sf, stream=stream)
+        return out
+    t = z(K, N)
+    moe_quantize_fp8_weights(w, out.q, out.sf, t.q, t.sf, stream)
+    return out, t
+
+
+def quantize_fp8_tokens_alloc(x: torch.Tensor, expert_offsets, R, rows=None, stream=None) -> FP8Tensor:
+    blocks = moe_fp8_token_blocks(R, expert_offsets.numel() - 1)
+    out = FP8Tensor(torch.empty(blocks, x.shape[1], 128, dtype=torch.uint8, device=x.device),
+                    torch.empty(blocks, x.shape[1], dtype=torch.float32, device=x.device))
+    moe_quantize_fp8_tokens(x, expert_offsets, R, out.q, out.sf, rows, stream)
+    return out
+
+
+def grouped_gemm_fp8_alloc(A: FP8Tensor, B: FP8Tensor, expert_offsets, R, epilogue=MOE_EPI_NONE, A_rows=None, stream=None):
+    """D bf16 [R, N] (NONE) or the FP8Tensor act [R, N/2] (SWIGLU_FP8)."""
+    N, R, dev = B.q.shape[1], int(R), A.q.device
+    if epilogue == MOE_EPI_SWIGLU_FP8:
+        out = FP8Tensor(torch.empty(R, N // 2, dtype=torch.uint8, device=dev),
+                        torch.empty(R, N // 256, dtype=torch.float32, device=dev))
+        D, D_sf = out.q, out.sf
+    else:
+        out = D = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
+        D_sf = None
+    moe_grouped_gemm_fp8(make_gemm_fp8_args(A.q, A.sf, B.q, B.sf, expert_offsets, R, epilogue, D, D_sf, A_rows), stream)
+    return out
+
+
+def grouped_wgrad_fp8_alloc(dY: FP8Tensor, X: FP8Tensor, expert_offsets, R, dtype=torch.float32, stream=None):
+    """dW [E, N, K] from quantize_fp8_tokens_alloc of the output gradients and of the rows."""
+    E, N, K = expert_offsets.numel() - 1, dY.q.shape[1], X.q.shape[1]
+    D = torch.empty(E, N, K, dtype=dtype, device=dY.q.device)
+    moe_grouped_wgrad_fp8(make_wgrad_fp8_args(dY.q, dY.sf, X.q, X.sf, expert_offsets, R, D), stream)
+    return D
+
+
+def balance_loss_alloc(logits: torch.Tensor, topk_ids: torch.Tensor, seq_offsets=None, token_mask=None, stream=None):
+    """(loss [1], counts [S, E], coef [S, E]); coef goes to moe_balance_loss_backward."""
+    S, E = 1 if seq_offsets is None else seq_offsets.numel() - 1, logits.shape[1]
+    counts = torch.empty(S, E, dtype=torch.int32, device=logits.device)
+    coef = torch.empty(S, E, dtype=torch.float32, device=logits.device)
+    loss = torch.empty(1, dtype=torch.float32, device=logits.device)
+    moe_balance_loss(logits, topk_ids, counts, coef, loss, seq_offsets, token_mask, stream=stream)
+    return loss, counts, coef
+
+
+class MoEFP8LayerPlan:
+    """The layer of MoELayerPlan with FP8 experts: W1 [E, 2I, H] and W2 [E, H, I] as FP8Tensor of
+    quantize_fp8_weights_alloc (I % 128 == 0).  Buffers and argument blocks are allocated once; the
+    gate/up product quantises its SwiGLU output itself."""
+
+    def __init__(self, T: int, E: int, k: int, H: int, I: int, W1: FP8Tensor, W2: FP8Tensor, device="cuda"):
+        self.T, self.E, self.k, self.H, self.I = T, E, k, H, I
+        R = self.R = T * k
+        dev = torch.device(device)
+        z = lambda *s, dt: torch.empty(*s, dtype=dt, device=dev)
+        self.ids, self.w = z(T, k, dt=torch.int32), z(T, k, dt=torch.float32)
+        self.off, self.row_src, self.tsr = z(E + 1, dt=torch.int32), z(R, dt=torch.int32), z(R, dt=torch.int32)
+        self.xq = FP8Tensor(z(T, H, dt=torch.uint8), z(T, _fp8_blocks(H), dt=torch.float32))
+        self.actq = FP8Tensor(z(R, I, dt=torch.uint8), z(R, _fp8_blocks(I), dt=torch.float32))
+        self.Y, self.out = z(R, H, dt=torch.bfloat16), z(T, H, dt=torch.bfloat16)
+        self.W1, self.W2 = W1, W2
+        self.args1 = make_gemm_fp8_args(self.xq.q, self.xq.sf, W1.q, W1.sf, self.off, R, MOE_EPI_SWIGLU_FP8,
+                                        self.actq.q, self.actq.sf, self.row_src)
+        self.args2 = make_gemm_fp8_args(self.actq.q, self.actq.sf, W2.q, W2.sf, self.off, R, MOE_EPI_NONE, self.Y)
+        for a in (self.args1, self.args2):
+            _check("moe_grouped_gemm_fp8_can_implement", moe_grouped_gemm_fp8_can_implement(a))
+        self.ws_route = _ws(lib().moe_route_permute_workspace(T, E, k), dev)
+
+    def forward(self, logits, x, stream=None):
+        main = stream if stream is not None else torch.cuda.current_stream()
+        moe_route_permute(logits, self.k, self.ids, self.w, self.off, self.row_src, self.tsr, self.ws_route, main)
+        moe_quantize_fp8(x, self.xq.q, self.xq.sf, main)
+        moe_grouped_gemm_fp8(self.args1, main)
+        moe_grouped_gemm_fp8(self.args2, main)
+        moe_finalize(self.Y, self.w, self.tsr, self.out, main)
+        return self.out
+
+    def graph(self, logits, x) -> "torch.cuda.CUDAGraph":
+        """As MoELayerPlan.graph: one forward pass over these input buffers, captured."""
+        self.forward(logits, x)
         torch.cuda.synchronize()
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):

@@ -17,14 +17,16 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build", "moe_nvfp4")
 LIB_PATH = os.path.join(PKG, "libmoe_nvfp4.so")
 SOURCES = ["route_permute.hip", "quantize.hip", "grouped_gemm.hip", "gemm_lds.hip", "gemm_ksplit.hip",
-           "gemm_rowmajor.hip", "finalize.hip", "moe_api.hip"]
+           "gemm_rowmajor.hip", "finalize.hip", "moe_api.hip", "fp8_quantize.hip", "fp8_gemm.hip",
+           "balance_loss.hip", "fp8_api.hip"]
 # the benchmark's measurement kernels (streaming read, MFMA throughput), a library of their own
 # (not the MoE ABI)
 PROBE_SOURCES = ["stream_probe.hip", "mfma_probe.hip"]
 PROBE_LIB_PATH = os.path.join(PKG, "libmoe_probes.so")
 # per-source extra flags: the MFMA probe's loop keeps its accumulators in VGPRs only in the
-# VGPR form of MFMA
-EXTRA_FLAGS = {"mfma_probe.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# VGPR form of MFMA; the FP8 GEMM's MFMA results are read by the next vector instructions
+EXTRA_FLAGS = {"mfma_probe.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "fp8_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH_FLAGS = ["--offload-arch=gfx950"]

@@ -272,6 +272,150 @@ moe_status moe_finalize(const uint16_t *Y, int64_t R, const float *topk_w,
                         const int32_t *token_slot_row, int T, int k, int H, uint16_t *out,
                         hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * 5. FP8 operands: E4M3FN elements (bias 7, max 448) with one binary32 scale per 128
+ * elements of the contraction.
+ *
+ * Defined by: this library.  The pages hold their weights in FP4 and use E4M3 only for the
+ * block scales of it ("Cracking the SM120 Shared Memory Ceiling", section "The Shared
+ * Memory Calculation"); checkpoints and training runs with 8-bit experts use the layout
+ * below, which takes the place of section 2's and 3's operands in the same layer.
+ *
+ * Steps of every quantiser, per block: s = amax / 448, code = e4m3(min(|x| / s, 448)) with
+ * the sign of x, both quotients correctly rounded binary32, the code round to nearest
+ * even; the output is bit-exact.  A block whose maximum is 0, or whose s underflows to 0,
+ * holds signed zeros.  A block with an infinity or a NaN gets scale NaN and codes 0: all
+ * its values are NaN, so an overflow stays visible in every product that reads it.
+ * value = e4m3(code) * s.  x_dtype: MOE_DTYPE_BF16 or MOE_DTYPE_F32.
+ *
+ * 5a. moe_quantize_fp8: rows.  x [rows, C] -> q [rows, C] u8, sf [rows, ceil(C / 128)] f32;
+ *     blocks of 128 along a row, the last one short if C % 128 != 0.
+ * 5b. moe_quantize_fp8_weights: tiles.  w [E, N, K] -> q [E, N, K], sf [E, ceil(N / 128),
+ *     ceil(K / 128)]: one scale per 128 x 128 tile, short at the edges.  With qt and sft
+ *     (both or neither) also the transposed copy qt [E, K, N], sft [E, ceil(K / 128),
+ *     ceil(N / 128)]: the same codes and scales, which the input gradient contracts over N.
+ * 5c. moe_quantize_fp8_tokens: columns of groups.  Permuted row p of group e is row
+ *     rows[p] (NULL: p) of x [rows_x, C]; each group is cut into blocks of 128 rows, the
+ *     blocks of all groups numbered in order: q [blocks, C, 128], sf [blocks, C] with one
+ *     scale per column of a block, zero codes behind a group's last row.  blocks =
+ *     moe_fp8_token_blocks(R, E) is the most there can be; blocks past the last one in use
+ *     are not written.
+ * Limits: rows, R >= 0; C, N, K multiples of 16 (of x in 5a and 5c: C >= 16) up to 2^20;
+ * 1 <= E <= 1024; R < 2^31; fewer than 2^31 blocks.
+ * ------------------------------------------------------------------------- */
+moe_status moe_quantize_fp8(const void *x, int x_dtype, int64_t rows, int64_t C, uint8_t *q, float *sf,
+                            hipStream_t stream);
+moe_status moe_quantize_fp8_weights(const void *w, int w_dtype, int E, int N, int K, uint8_t *q, float *sf,
+                                    uint8_t *qt, float *sft, hipStream_t stream);
+int64_t moe_fp8_token_blocks(int64_t R, int E);
+moe_status moe_quantize_fp8_tokens(const void *x, int x_dtype, int64_t rows_x, const int32_t *rows,
+                                   const int32_t *expert_offsets, int E, int64_t R, int64_t C, uint8_t *q,
+                                   float *sf, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 6. Grouped FP8 GEMM.  For expert e and permuted row p in [expert_offsets[e],
+ * expert_offsets[e+1]):
+ *   y[p, n] = sum_b sA[r, b] sB[e, n / 128, b] sum_{i<128} a[r, 128b+i] b[e, n, 128b+i]
+ * with r = A_rows ? A_rows[p] : p; within a block the FP8 matrix core adds 8 products at
+ * a time, each cut off at 2^-13 of the largest one's power of two, and those sums in binary32;
+ * the blocks are summed in binary32.  A / A_sf from 5a, B / B_sf from 5b.
+ * Epilogues:
+ *   MOE_EPI_NONE        D bf16 [R, N]: D[p, n] = bf16(y[p, n]).
+ *   MOE_EPI_SWIGLU_FP8  N = 2I; columns [0, I) are gate, [I, 2I) are up; act = silu(gate) up
+ *                       in binary32 (hardware exp2 and reciprocal, a few ulp), quantised by
+ *                       the steps of 5a: D u8 [R, I], D_sf f32 [R, I / 128], the A operand
+ *                       of the down projection.
+ * Rows p >= expert_offsets[E] of D are not written.  A single token, a decode batch and a
+ * prompt take the same call.  The gradient with respect to the rows, dX[p, k] = sum_n
+ * dY[p, n] W[e, n, k], is the same product: A = dY quantised by 5a, B = qt, B_sf = sft of
+ * 5b, with N and K exchanged (moe_finalize with unit weights sums a token's rows).
+ * Supported: N % 16 == 0, K % 16 == 0, N, K <= 2^20, N * K <= 2^31 - 4096, 1 <= E <= 1024,
+ * 0 <= R < 2^31; SWIGLU_FP8: N % 256 == 0; with A_rows: rows_A * K <= 2^31 - 4096;
+ * MOE_ERR_UNSUPPORTED otherwise.  Without A_rows, rows_A >= R.  No workspace: every
+ * workgroup derives its work item from the offsets.
+ * moe_grouped_gemm_fp8_can_implement() returns MOE_OK exactly when the launch is supported.
+ * ------------------------------------------------------------------------- */
+enum { MOE_EPI_SWIGLU_FP8 = 3 };
+
+typedef struct moe_gemm_fp8_args {
+  const uint8_t *A;               /* [rows_A, K] */
+  const float *A_sf;              /* [rows_A, ceil(K/128)] */
+  const int32_t *A_rows;          /* [R] gather map, or NULL for the identity */
+  int64_t rows_A;                 /* rows of A */
+  const uint8_t *B;               /* [E, N, K] */
+  const float *B_sf;              /* [E, ceil(N/128), ceil(K/128)] */
+  const int32_t *expert_offsets;  /* [E+1] */
+  int32_t E, N, K;
+  int32_t epilogue;               /* MOE_EPI_NONE or MOE_EPI_SWIGLU_FP8 */
+  int64_t R;
+  void *D;                        /* bf16 [R, N] (NONE), u8 codes [R, N/2] (SWIGLU_FP8) */
+  float *D_sf;                    /* SWIGLU_FP8 only: [R, N/256] */
+} moe_gemm_fp8_args;
+
+moe_status moe_grouped_gemm_fp8_can_implement(const moe_gemm_fp8_args *args);
+moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args *args, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 7. Grouped FP8 weight gradient: dW[e, n, k] = sum over the rows p of group e of
+ * dY[p, n] x[p, k], from operands quantised by 5c (Y from the output gradients, X from the
+ * rows that the forward product read, both over the same expert_offsets and R):
+ *   D[e, n, k] = sum_b sY[b, n] sX[b, k] sum_{t<128} y[b, n, t] x[b, k, t]
+ * over the blocks b of group e; products are exact and all sums binary32.  D [E, N, K] in D_dtype
+ * (MOE_DTYPE_F32, or MOE_DTYPE_BF16: rounded once); every element is written, zeros for an
+ * expert without rows.  Limits: as section 6.
+ * ------------------------------------------------------------------------- */
+typedef struct moe_wgrad_fp8_args {
+  const uint8_t *Y;               /* [blocks, N, 128] */
+  const float *Y_sf;              /* [blocks, N] */
+  const uint8_t *X;               /* [blocks, K, 128] */
+  const float *X_sf;              /* [blocks, K] */
+  const int32_t *expert_offsets;  /* [E+1] */
+  int32_t E, N, K;
+  int32_t D_dtype;
+  int64_t R;
+  void *D;                        /* [E, N, K] */
+} moe_wgrad_fp8_args;
+
+moe_status moe_grouped_wgrad_fp8_can_implement(const moe_wgrad_fp8_args *args);
+moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args *args, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 8. The router's load-balancing term, with its counts and gradient.
+ *
+ * Defined by: this library (the pages serve a trained router; a router is trained with this
+ * term beside the routing of section 1).  logits [T, E] f32 and topk_ids [T, k] as in
+ * section 1.  The tokens of sequence s are [seq_offsets[s], seq_offsets[s+1]) (seq_offsets
+ * [S+1] i32, or NULL with S = 1: all T tokens), of which token_mask (u8 [T], or NULL: all)
+ * keeps the n with a non-zero entry.  With p = softmax of a token's E logits:
+ *   counts[s, e] i32  slots of those tokens that chose e (an id outside [0, E), a dropped
+ *                     slot, counts nowhere)
+ *   coef[s, e]   f32  E counts[s, e] / (k n^2 S), 0 where n = 0: the derivative of the loss
+ *                     with respect to p[t, e] of every kept token of s
+ *   loss         f32  1/S sum_s sum_e (E counts[s, e] / (k n)) (1/n sum_t p[t, e])
+ * (1 when all is balanced; a sequence without kept tokens adds 0).  Logits of -inf have
+ * p = 0, and so has a row of -inf alone; rows that the mask drops are not read into any
+ * result, whatever they hold.  Probabilities are binary32 (hardware exp2), their sums
+ * binary32 within 32 tokens and binary64 beyond.
+ *
+ * moe_balance_loss_backward: the counts are constants, so with a = *grad_loss coef[s]
+ *   dlogits[t, e] = p[t, e] (a[e] - sum_e' p[t, e'] a[e'])
+ * and, where d_topk_w [T, k] is given (else NULL, with topk_ids, topk_w and k ignored), the
+ * gradient of the routing weights topk_w of section 1 in the same pass:
+ *   dlogits[t, topk_ids[t, j]] += topk_w[t, j] (d_topk_w[t, j] - sum_i topk_w[t, i] d_topk_w[t, i])
+ * A masked token's row is 0.  Rows of dlogits outside every sequence are not written.
+ * Limits: T >= 0, 1 <= E <= 1024, 1 <= k <= min(E, 32), 1 <= S <= 65536, T*k < 2^31;
+ * seq_offsets NULL with S != 1 is MOE_ERR_NULL.  ws: moe_balance_loss_workspace(T, E, k, S)
+ * bytes (contents on entry irrelevant; calls that may overlap need one each).
+ * ------------------------------------------------------------------------- */
+size_t moe_balance_loss_workspace(int T, int E, int k, int S);
+moe_status moe_balance_loss(const float *logits, const int32_t *topk_ids, int T, int E, int k,
+                            const int32_t *seq_offsets, int S, const uint8_t *token_mask, int32_t *counts,
+                            float *coef, float *loss, void *ws, size_t ws_bytes, hipStream_t stream);
+moe_status moe_balance_loss_backward(const float *logits, int T, int E, const int32_t *seq_offsets, int S,
+                                     const uint8_t *token_mask, const float *coef, const float *grad_loss,
+                                     const int32_t *topk_ids, const float *topk_w, const float *d_topk_w,
+                                     int k, float *dlogits, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
