@@ -71,17 +71,34 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
 // Copies 16 (4) bytes per lane from `voff` of the buffer to LDS bytes lds + 16 (4) * lane.  The
 // copy is counted by vmcnt like a load; it has no destination registers, so nothing waits for
 // it but the explicit wait in `arrive`.
+// ONCE: the bytes are read by this copy alone and need not stay in the caches.
+template <bool ONCE = false>
 __device__ __forceinline__ void copy16(const Buf &b, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(lds), "v"(voff), "s"(descriptor(b))
-               : "memory");
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(descriptor(b))
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(descriptor(b))
+                 : "memory");
 }
 __device__ __forceinline__ void copy4(const Buf &b, uint32_t lds, uint32_t voff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(descriptor(b))
                : "memory");
+}
+
+// copy16 if `yes` (uniform).  The branch is inside the statement so that the loop around it stays
+// one block to the compiler, which otherwise runs out of registers.
+__device__ __forceinline__ void copy16_if(bool yes, const Buf &b, uint32_t lds, uint32_t voff) {
+  asm volatile("s_cmp_eq_u32 %3, 0\n\ts_cbranch_scc1 .Lnocopy%=\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds\n.Lnocopy%=:"
+               :
+               : "s"(lds), "v"(voff), "s"(descriptor(b)), "s"(uniform(yes ? 1u : 0u))
+               : "memory", "scc");
 }
 
 // Waits until at most `LATER` copies of this wave are under way and its LDS reads are done,
@@ -108,7 +125,10 @@ struct Tile {
   static constexpr int kBytesP = BP * kFp8Block, kBytesQ = kRowsQ * kFp8Block, kBytesS = kWaves * kWave * 4;
   static constexpr int kScaleP = BQ < kWave ? kWave : BQ;    // P's scales stand behind Q's, in another wave's copy
   static constexpr int kStage = kBytesP + kBytesQ + kBytesS;
-  static constexpr int kLds = STAGES * kStage;
+  static constexpr bool kLarge = BQ == 256 && BP == 256;     // contract_large
+  // contract_large keeps its scales apart: two groups of four steps, a float4 per row
+  static constexpr int kScaleRows = kScaleP + kWave, kScaleGroup = kScaleRows * 16;
+  static constexpr int kLds = kLarge ? 2 * (kBytesP + kBytesQ) + 2 * kScaleGroup : STAGES * kStage;
   static_assert(BP % 128 == 0 && BP / 8 % kWaves == 0 && BQ % (16 * WQ) == 0 && kPerHalf >= 1, "tile split");
   static_assert(kScaleP + kHalves <= kWaves * kWave, "a stage's scales fit one copy per wave");
   static_assert(STAGES >= 2 && kCopies * (STAGES - 2) < 64, "copies under way fit the counter");
@@ -124,46 +144,65 @@ struct Source {
   int last_pieces;             // 16-byte pieces that the last stage holds of a row (8: all)
 };
 
-// Row and logical piece that copy j of this wave and lane moves.
+// First LDS row of copy j of P: in the large tile a wave copies as many rows of either half.
+template <class T>
+__device__ __forceinline__ int copy_row_p(int wave, int j) {
+  constexpr int kHalf = T::kCopiesP / 2;
+  return T::kLarge ? j / kHalf * kFp8Block + (wave * kHalf + j % kHalf) * 8 : (wave * T::kCopiesP + j) * 8;
+}
+
+// Row and logical piece that a copy of the rows from `first_row` moves in this lane.
 __device__ __forceinline__ void copy_place(int first_row, int &row, int &piece) {
   const int lane = threadIdx.x & 63;
   row = first_row + lane / 8;
   piece = (lane & 7) ^ ((row >> 1) & 7);
 }
 
-// The copies of stage `kb` into buffer `slot`; beyond the last stage they move nothing.
-template <class T>
-__device__ __forceinline__ void issue(Source<T> &src, uint32_t lds, int wave, int kb, int steps) {
-  const bool tail = kb == steps - 1 && src.last_pieces < 8;
-  const int lane = threadIdx.x & 63;
-  if (kb >= steps) src.p.bytes = src.q.bytes = src.s.bytes = 0;
+// This lane's offset in a copy of the rows from `first_row`: nothing if the last stage ends before
+// the lane's piece.
+__device__ __forceinline__ uint32_t piece_or_none(uint32_t voff, int first_row, bool last, int last_pieces) {
+  int row, piece;
+  copy_place(first_row, row, piece);
+  return last && piece >= last_pieces ? kOob : voff;
+}
+
+template <class T, bool ONCE, int FROM, int TO>
+__device__ __forceinline__ void issue_p(const Source<T> &src, uint32_t lds, int wave, bool last) {
 #pragma unroll
-  for (int j = 0; j < T::kCopiesP; j++) {
-    const int row8 = (wave * T::kCopiesP + j) * 8;
-    uint32_t v = src.vp[j];
-    if (tail && ((lane & 7) ^ (((row8 + lane / 8) >> 1) & 7)) >= src.last_pieces) v = kOob;
-    copy16(src.p, lds + row8 * kFp8Block, v);
+  for (int j = FROM; j < TO; j++) {
+    const int row = copy_row_p<T>(wave, j);
+    copy16<ONCE>(src.p, lds + row * kFp8Block, piece_or_none(src.vp[j], row, last, src.last_pieces));
   }
+}
+template <class T>
+__device__ __forceinline__ void issue_q(const Source<T> &src, uint32_t lds, int wave, bool last) {
 #pragma unroll
   for (int j = 0; j < T::kCopiesQ; j++) {
-    const int row8 = (wave * T::kCopiesQ + j) * 8;
-    uint32_t v = src.vq[j];
-    if (tail && ((lane & 7) ^ (((row8 + lane / 8) >> 1) & 7)) >= src.last_pieces) v = kOob;
-    copy16(src.q, lds + T::kBytesP + row8 * kFp8Block, v);
+    const int row = (wave * T::kCopiesQ + j) * 8;
+    copy16(src.q, lds + T::kBytesP + row * kFp8Block, piece_or_none(src.vq[j], row, last, src.last_pieces));
   }
+}
+
+// The copies of stage `kb` into the buffer at `lds`; beyond the last stage they move nothing.
+template <class T, bool ONCE>
+__device__ __forceinline__ void issue(Source<T> &src, uint32_t lds, int wave, int kb, int steps) {
+  const bool last = kb == steps - 1 && src.last_pieces < 8;
+  if (kb >= steps) src.p.bytes = src.q.bytes = src.s.bytes = 0;
+  issue_p<T, ONCE, 0, T::kCopiesP>(src, lds, wave, last);
+  issue_q<T>(src, lds, wave, last);
   copy4(src.s, lds + T::kBytesP + T::kBytesQ + wave * kWave * 4, src.vs);
   src.p.base += src.step_p;
   src.q.base += src.step_q;
   src.s.base += src.step_s;
 }
 
-// 32 bytes of a tile row: pieces 2g and 2g + 1 for lane group g (both operands take this order;
+// 32 bytes of a tile row: pieces g and g + 4 for lane group g (both operands take this order;
 // within a scale block the contraction's order is free).
 __device__ __forceinline__ int8v fragment(const uint8_t *rows, int row, int g) {
   const int sw = (row >> 1) & 7;
   const uint8_t *p = rows + row * kFp8Block;
-  const int4x a = *reinterpret_cast<const int4x *>(p + ((2 * g) ^ sw) * 16);
-  const int4x b = *reinterpret_cast<const int4x *>(p + ((2 * g + 1) ^ sw) * 16);
+  const int4x a = *reinterpret_cast<const int4x *>(p + (g ^ sw) * 16);
+  const int4x b = *reinterpret_cast<const int4x *>(p + ((g + 4) ^ sw) * 16);
   return int8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
@@ -190,7 +229,7 @@ __device__ __forceinline__ Half32 to_f16(const int8v &v) {
 
 // The whole contraction of one tile.  Scales of a stage: [0, BQ) of the Q rows, from kScaleP one
 // per half of P (WGRAD false) or one per P row.
-template <class T, bool WGRAD>
+template <class T, bool WGRAD, bool ONCE>
 __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps, float4v (&acc)[T::TP][T::TQ]) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x & 63, g = lane / 16, r = lane % 16;
@@ -201,12 +240,12 @@ __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps
 #pragma unroll
     for (int j = 0; j < T::TQ; j++) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int s = 0; s < T::STAGES - 1; s++) issue<T>(src, lds0 + s * T::kStage, wave, s, steps);
+  for (int s = 0; s < T::STAGES - 1; s++) issue<T, ONCE>(src, lds0 + s * T::kStage, wave, s, steps);
   int slot = 0;
   for (int kb = 0; kb < steps; kb++) {
     arrive<T::kCopies *(T::STAGES - 2)>();
     const int next = slot == 0 ? T::STAGES - 1 : slot - 1;
-    issue<T>(src, lds0 + next * T::kStage, wave, kb + T::STAGES - 1, steps);
+    issue<T, ONCE>(src, lds0 + next * T::kStage, wave, kb + T::STAGES - 1, steps);
     const uint8_t *P = lds + slot * T::kStage, *Q = P + T::kBytesP;
     const float *S = reinterpret_cast<const float *>(Q + T::kBytesQ);
     using Frag = std::conditional_t<WGRAD, Half32, int8v>;
@@ -251,9 +290,150 @@ __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps
   arrive<0>();   // the copies past the end (zeros) are in before the buffers serve anything else
 }
 
+// ---- the large tile -------------------------------------------------------------------------
+//
+// 256 x 256 results in eight waves, two on each SIMD, each 128 P rows (64 of either half) by 64 Q
+// rows.  A step (one scale block) has four phases per wave: read half 0 of P and all of Q from LDS
+// into registers, 16 MFMAs, read half 1 of P, 16 MFMAs.  Two workgroup barriers a step, after an
+// MFMA phase of waves 0-3 and a reading phase of waves 4-7, keep the two halves of the workgroup
+// one phase apart, so on every SIMD one wave's matrix instructions run while the other reads.  A
+// stage has two parts, X (Q, half 0 of P) and Y (half 1 of P), whose buffers are free again at
+// the next barrier after they were read: part X of step b + 2 is copied in the reading phase of
+// half 1 of step b, part Y of step b + 1 in that of half 0, about six phases before they are read.
+//
+// A step's scales are one float in each of 256 rows, as many requests to L2 as half the codes;
+// four steps' scales of a row are one 16-byte copy instead, issued with part X of every fourth
+// step.  The last group of a row that has no whole number of groups starts at its fourth scale
+// from the end (a large tile has at least four steps).
+//
+// Measured, one group of 8192 rows, N = K = 8192 (1.1 TFLOP): 480 us, 2.3 PFLOP/s (128 x 128 tiles: 680 us); the same data of zeros 420 us: the card lowers its clock under this load, and a loop of these MFMAs and fmas alone runs at 3.4 PFLOP/s on random data, 4.5 on constants.
+constexpr int kLag = 4;   // an MFMA's result is read that many MFMAs later (3: the same within 1 %; 2: 3 % slower)
+
+template <class T, bool ONCE>
+__device__ __forceinline__ void issue_x(Source<T> &src, uint32_t lds0, int wave, int kb, int steps) {
+  const uint32_t lds = lds0 + (kb & 1) * (T::kBytesP + T::kBytesQ), scales = lds0 + 2 * (T::kBytesP + T::kBytesQ);
+  const bool last = kb == steps - 1 && src.last_pieces < 8;
+  if (kb >= steps) src.p.bytes = src.q.bytes = 0;
+  issue_q<T>(src, lds, wave, last);
+  issue_p<T, ONCE, 0, T::kCopiesP / 2>(src, lds, wave, last);
+  // (kOob plus an offset inside a row of scales is out of range too)
+  copy16_if((kb & 3) == 0 && kb < steps && wave * kWave < T::kScaleRows, src.s,
+            scales + (kb >> 2 & 1) * T::kScaleGroup + wave * kWave * 16, src.vs + 4 * min(kb, steps - 4));
+  src.q.base += src.step_q;
+}
+template <class T, bool ONCE>
+__device__ __forceinline__ void issue_y(Source<T> &src, uint32_t lds0, int wave, int kb, int steps) {
+  if (kb >= steps) src.p.bytes = 0;
+  issue_p<T, ONCE, T::kCopiesP / 2, T::kCopiesP>(src, lds0 + (kb & 1) * (T::kBytesP + T::kBytesQ), wave,
+                                          kb == steps - 1 && src.last_pieces < 8);
+  src.p.base += src.step_p;
+}
+
+template <class T>
+__device__ __forceinline__ void mfma_half(const int8v (&p)[T::kPerHalf], const int8v (&q)[T::TQ], const float (&s)[T::TQ],
+                                          float4v (*acc)[T::TQ]) {
+  constexpr int kAll = T::kPerHalf * T::TQ;
+  float4v t[kLag + 1];
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int n = 0; n < kAll + kLag; n++) {
+    if (n < kAll)
+      t[n % (kLag + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p[n / T::TQ], q[n % T::TQ],
+                                                                           float4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+    if (n >= kLag) {
+      const int m = n - kLag;
+#pragma unroll
+      for (int c = 0; c < 4; c++)
+        acc[m / T::TQ][m % T::TQ][c] = fmaf(t[m % (kLag + 1)][c], s[m % T::TQ], acc[m / T::TQ][m % T::TQ][c]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// Copies that may be under way at a barrier: the two parts issued after the one it waits for.  A
+// group's scales, the last copy of its part X, are not counted, so a barrier with one of them
+// under way waits for one copy more than it has to.
+template <class T>
+constexpr int kLaterCopies = T::kCopiesQ + T::kCopiesP;
+
+// BEHIND: waves 4-7, whose barriers follow their reading phases.
+template <class T, bool ONCE, bool BEHIND>
+__device__ __forceinline__ void large_loop(Source<T> &src, uint8_t *lds, int steps, int wave, float4v (&acc)[T::TP][T::TQ]) {
+  constexpr int kLater = kLaterCopies<T>;
+  const int lane = threadIdx.x & 63, g = lane / 16, r = lane % 16;
+  const int wp = wave % T::WP, wq = wave / T::WP;
+  const uint32_t lds0 = lds_address(lds);
+  for (int kb = 0; kb < steps; kb++) {
+    const uint8_t *P = lds + (kb & 1) * (T::kBytesP + T::kBytesQ), *Q = P + T::kBytesP;
+    const float *S = reinterpret_cast<const float *>(lds + 2 * (T::kBytesP + T::kBytesQ) + (kb >> 2 & 1) * T::kScaleGroup) +
+                     (kb - min(kb & ~3, steps - 4));
+    int8v p[T::kPerHalf], q[T::TQ];
+    float s[2][T::TQ];
+    issue_y<T, ONCE>(src, lds0, wave, kb + 1, steps);
+#pragma unroll
+    for (int j = 0; j < T::TQ; j++) q[j] = fragment(Q, (wq * T::TQ + j) * 16 + r, g);
+#pragma unroll
+    for (int i = 0; i < T::kPerHalf; i++) p[i] = fragment(P, wp * (kFp8Block / T::WP) + i * 16 + r, g);
+#pragma unroll
+    for (int j = 0; j < T::TQ; j++) {
+      const float sq = S[4 * ((wq * T::TQ + j) * 16 + r)];
+      s[0][j] = sq * S[4 * T::kScaleP];
+      s[1][j] = sq * S[4 * (T::kScaleP + 1)];
+    }
+    if (BEHIND) arrive<kLater>();    // part Y of this step is there
+    mfma_half<T>(p, q, s[0], acc);
+    if (!BEHIND) arrive<kLater>();
+    issue_x<T, ONCE>(src, lds0, wave, kb + 2, steps);
+#pragma unroll
+    for (int i = 0; i < T::kPerHalf; i++) p[i] = fragment(P, kFp8Block + wp * (kFp8Block / T::WP) + i * 16 + r, g);
+    if (BEHIND) arrive<kLater>();    // part X of the next step is there
+    mfma_half<T>(p, q, s[1], acc + T::kPerHalf);
+    if (!BEHIND) arrive<kLater>();
+  }
+}
+
+// `rows`: rows of Q in use; a wave whose 64 rows are all behind them only copies.
+template <class T, bool ONCE>
+__device__ __forceinline__ void contract_large(Source<T> &src, uint8_t *lds, int steps, int rows, float4v (&acc)[T::TP][T::TQ]) {
+  static_assert(T::kWaves == 8 && T::WP == 2 && T::kHalves == 2, "the schedule above");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t lds0 = lds_address(lds);
+#pragma unroll
+  for (int i = 0; i < T::TP; i++)
+#pragma unroll
+    for (int j = 0; j < T::TQ; j++) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
+  issue_x<T, ONCE>(src, lds0, wave, 0, steps);
+  issue_y<T, ONCE>(src, lds0, wave, 0, steps);
+  issue_x<T, ONCE>(src, lds0, wave, 1, steps);
+  constexpr int kLater = kLaterCopies<T>;
+  arrive<kLater>();                  // part X of step 0 is there
+  if (wave / T::WP * T::TQ * 16 >= rows) {
+    for (int kb = 0; kb < steps; kb++) {
+      issue_y<T, ONCE>(src, lds0, wave, kb + 1, steps);
+      arrive<kLater>();
+      issue_x<T, ONCE>(src, lds0, wave, kb + 2, steps);
+      arrive<kLater>();
+    }
+  } else if (wave >= T::kWaves / 2) {
+    large_loop<T, ONCE, true>(src, lds, steps, wave, acc);
+  } else {
+    large_loop<T, ONCE, false>(src, lds, steps, wave, acc);
+  }
+  arrive<0>();
+}
+
 __device__ __forceinline__ uint2 bf16x4(const float4v &v) {
   return make_uint2(f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16),
                     f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16));
+}
+
+// STREAM: past the caches, which the operands of the other tiles keep (a large tile's launch writes
+// far more than the next one reads soon).
+template <bool STREAM>
+__device__ __forceinline__ void store16(void *at, const uint4 &v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  if (STREAM) __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, static_cast<u32x4 *>(at));
+  else *static_cast<uint4 *>(at) = v;
 }
 
 // Item number of workgroup b out of `count`: workgroups are dealt to the 8 XCDs in turn, so
@@ -276,18 +456,29 @@ __device__ __forceinline__ void place_in_band(int l, int chunks, int tiles, int 
   chunk = band * kBand + rem - tile * width;
 }
 
+// The item of this workgroup: group g, its chunk of `size` rows and n tile.
+__device__ __forceinline__ bool find_item(const GemmParams &P, int size, groups::Chunk &g, int &chunk, int &nt) {
+  int64_t w;
+  const int total = groups::chunk_count(P.offsets, P.E, P.R, size);
+  if (!item_of(blockIdx.x, static_cast<int64_t>(total) * P.n_tiles, w)) return false;
+  const int i = static_cast<int>(w / P.n_tiles);
+  if (!groups::find_chunk(P.offsets, P.E, P.R, size, i, g)) return false;
+  place_in_band(static_cast<int>(w - static_cast<int64_t>(i - g.index) * P.n_tiles), g.total, P.n_tiles, chunk, nt);
+  return true;
+}
+
+// Row of A that permuted row p reads.
+__device__ __forceinline__ int64_t row_of_a(const GemmParams &P, int p) {
+  const int64_t a = P.A_rows[p];
+  return a < 0 ? 0 : (a >= P.rows_A ? P.rows_A - 1 : a);
+}
+
 template <class T, Mode MODE>
 __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) {
   __shared__ __align__(1024) uint8_t lds[T::kLds];
-  // the item: an expert's row chunk and n tile
-  int64_t w;
-  const int total = groups::chunk_count(P.offsets, P.E, P.R, T::BQ);
-  if (!item_of(blockIdx.x, static_cast<int64_t>(total) * P.n_tiles, w)) return;
-  const int i = static_cast<int>(w / P.n_tiles);
   groups::Chunk g;
-  if (!groups::find_chunk(P.offsets, P.E, P.R, T::BQ, i, g)) return;
   int chunk, nt;
-  place_in_band(static_cast<int>(w - static_cast<int64_t>(i - g.index) * P.n_tiles), g.total, P.n_tiles, chunk, nt);
+  if (!find_item(P, T::BQ, g, chunk, nt)) return;
   const int first = g.lo + chunk * T::BQ, count = min(T::BQ, g.hi - first);
   const int half_n = P.N / 2;                       // SWIGLU: gate rows, then up rows
   const int n0 = nt * (MODE == kSwigluFp8 ? kFp8Block : T::BP);
@@ -303,7 +494,7 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
 #pragma unroll
   for (int j = 0; j < T::kCopiesP; j++) {
     int row, piece;
-    copy_place((wave * T::kCopiesP + j) * 8, row, piece);
+    copy_place(copy_row_p<T>(wave, j), row, piece);
     int n = n0 + row;
     if (MODE == kSwigluFp8) n = n0 + row % kFp8Block + row / kFp8Block * half_n;   // half_n % 128 == 0
     src.vp[j] = n < P.N ? static_cast<uint32_t>(n) * P.K + piece * 16 : kOob;
@@ -312,11 +503,7 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
   const bool gather = P.A_rows != nullptr;
   src.q.base = reinterpret_cast<uint64_t>(P.A) + (gather ? 0 : static_cast<uint64_t>(first) * P.K);
   src.q.bytes = static_cast<uint32_t>((gather ? P.rows_A : count) * P.K);
-  auto row_of = [&](int row) -> int64_t {
-    if (!gather) return row;
-    const int64_t a = P.A_rows[first + row];
-    return a < 0 ? 0 : (a >= P.rows_A ? P.rows_A - 1 : a);
-  };
+  auto row_of = [&](int row) -> int64_t { return gather ? row_of_a(P, first + row) : row; };
 #pragma unroll
   for (int j = 0; j < T::kCopiesQ; j++) {
     int row, piece;
@@ -345,20 +532,43 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
   src.s = uniform(src.s);
 
   float4v acc[T::TP][T::TQ];
-  contract<T, false>(src, lds, kb_n, acc);
+  // the weights of a group of one chunk are read by this workgroup alone (measured at 32 rows per
+  // expert, 805 MB of weights: 130 us past the caches, 138 us through them; with two chunks, whose
+  // second one finds them in L2, 35 us against 24 us for 77 MB)
+  if (g.total == 1 && P.stream_weights) {
+    if constexpr (T::kLarge) contract_large<T, true>(src, lds, kb_n, count, acc);
+    else contract<T, false, true>(src, lds, kb_n, acc);
+  } else {
+    if constexpr (T::kLarge) contract_large<T, false>(src, lds, kb_n, count, acc);
+    else contract<T, false, false>(src, lds, kb_n, acc);
+  }
 
   const int wp = wave % T::WP, wq = wave / T::WP;
   if (MODE == kNone) {
+    // each wave turns its tile around in LDS, 16 rows (or a few times 16, to have a piece for every
+    // lane) at a time, and stores whole pieces of rows (straight from the MFMA layout they would be
+    // 32 bytes long: 490 us against 480 us for the large tile's 1.1 TFLOP)
+    constexpr int kCols = kFp8Block / T::WP, kRow = T::kHalves * kCols * 2, kStride = kRow + 16;   // bytes
+    constexpr int kTurn = kRow < kWave ? kWave / kRow : 1;   // 16-row tiles turned together
+    constexpr int kPieces = kTurn * 16 * kRow / 16 / kWave;
+    static_assert(T::TQ % kTurn == 0 && kPieces * kWave == kTurn * kRow && T::kWaves * kTurn * 16 * kStride <= T::kLds, "staging");
+    uint8_t *mine = lds + wave * kTurn * 16 * kStride;
     uint16_t *D = static_cast<uint16_t *>(P.D);
 #pragma unroll
-    for (int j = 0; j < T::TQ; j++) {
-      const int t = (wq * T::TQ + j) * 16 + r;
-      if (t >= count) continue;
-      uint16_t *row = D + static_cast<int64_t>(first + t) * P.N;
+    for (int j0 = 0; j0 < T::TQ; j0 += kTurn) {
 #pragma unroll
-      for (int ti = 0; ti < T::TP; ti++) {
-        const int n = n0 + (ti / T::kPerHalf) * kFp8Block + wp * (kFp8Block / T::WP) + (ti % T::kPerHalf) * 16 + 4 * lg;
-        if (n < P.N) *reinterpret_cast<uint2 *>(row + n) = bf16x4(acc[ti][j]);
+      for (int j = 0; j < kTurn; j++)
+#pragma unroll
+        for (int ti = 0; ti < T::TP; ti++)
+          *reinterpret_cast<uint2 *>(mine + (j * 16 + r) * kStride + ti * 32 + lg * 8) = bf16x4(acc[ti][j0 + j]);
+#pragma unroll
+      for (int c = 0; c < kPieces; c++) {
+        const int at = c * kWave + lane, row = at / (kRow / 16), col = at % (kRow / 16) * 8;   // col: of the wave's columns
+        const int t = (wq * T::TQ + j0) * 16 + row;
+        const int n = n0 + col / kCols * kFp8Block + wp * kCols + col % kCols;
+        const uint4 v = *reinterpret_cast<const uint4 *>(mine + row * kStride + col * 2);
+        if (t >= count || n >= P.N) continue;
+        store16<T::kLarge>(D + static_cast<int64_t>(first + t) * P.N + n, v);
       }
     }
   } else {
@@ -402,6 +612,126 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
             fp8_quantize4(acc[ti][j][0], acc[ti][j][1], acc[ti][j][2], acc[ti][j][3], s);
       }
     }
+  }
+}
+
+// ---- few items ------------------------------------------------------------------------------
+//
+// When 128-column tiles are fewer than the CUs (a single token: k experts' weights, each a few
+// hundred rows), the contraction is dealt to the eight waves of a workgroup: wave w takes the
+// scale blocks w, w + 8, ... of a tile of 32 columns and 16 rows, with a ring of its own and no
+// barrier before the end, and the eight partial tiles are added in order through LDS.  Bound by
+// latency: the item lookup, about two round trips to HBM and the sum.  One token, eight experts of
+// 512 x 6144: 9.7 us (28 us in 64 x 128 tiles).
+template <int Q_, int WAVES_, int STAGES_>
+struct Split {
+  static constexpr int Q = Q_, P = 32, WAVES = WAVES_, STAGES = STAGES_;
+  static constexpr int TQ = Q / 16, TP = P / 16;
+  static constexpr int kCopies = (P + Q) / 8 + 2;
+  static constexpr int kStage = (P + Q) * kFp8Block + 2 * kWave * 4;
+  static constexpr int kLds = WAVES * STAGES * kStage;
+  static_assert(Q <= kWave && TP * TQ * kWave * 16 <= STAGES * kStage, "a wave's scales and partial tiles fit");
+};
+
+template <class T>
+__global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams P) {
+  __shared__ __align__(1024) uint8_t lds[T::kLds];
+  groups::Chunk g;
+  int chunk, nt;
+  if (!find_item(P, T::Q, g, chunk, nt)) return;
+  const int first = g.lo + chunk * T::Q, count = min(T::Q, g.hi - first), n0 = nt * T::P;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x & 63, lg = lane / 16, r = lane % 16;
+  const int kb_n = (P.K + kFp8Block - 1) / kFp8Block, nb_n = (P.N + kFp8Block - 1) / kFp8Block;
+  const bool gather = P.A_rows != nullptr;
+  auto row_of = [&](int row) -> int64_t { return gather ? row_of_a(P, first + row) : row; };
+  const Buf bp = {reinterpret_cast<uint64_t>(P.B) + static_cast<uint64_t>(g.group) * P.N * P.K, static_cast<uint32_t>(P.N) * P.K};
+  const Buf bq = {reinterpret_cast<uint64_t>(P.A) + (gather ? 0 : static_cast<uint64_t>(first) * P.K),
+                  static_cast<uint32_t>((gather ? P.rows_A : count) * P.K)};
+  const Buf bsq = {reinterpret_cast<uint64_t>(P.A_sf) + (gather ? 0 : static_cast<uint64_t>(first) * kb_n * 4),
+                   static_cast<uint32_t>((gather ? P.rows_A : count) * kb_n * 4)};
+  const Buf bsp = {reinterpret_cast<uint64_t>(P.B_sf) + (static_cast<uint64_t>(g.group) * nb_n + n0 / kFp8Block) * kb_n * 4,
+                   static_cast<uint32_t>(kb_n) * 4};
+  uint32_t vp[T::P / 8], vq[T::Q / 8];
+#pragma unroll
+  for (int j = 0; j < T::P / 8; j++) {
+    int row, piece;
+    copy_place(8 * j, row, piece);
+    vp[j] = n0 + row < P.N ? static_cast<uint32_t>(n0 + row) * P.K + piece * 16 : kOob;
+  }
+#pragma unroll
+  for (int j = 0; j < T::Q / 8; j++) {
+    int row, piece;
+    copy_place(8 * j, row, piece);
+    vq[j] = row < count ? static_cast<uint32_t>(row_of(row)) * P.K + piece * 16 : kOob;
+  }
+  const uint32_t vsq = lane < count ? static_cast<uint32_t>(row_of(lane)) * kb_n * 4 : kOob;
+  const int last_pieces = P.K % kFp8Block ? P.K % kFp8Block / 16 : 8;
+  uint8_t *ring = lds + wave * T::STAGES * T::kStage;
+  const uint32_t ring0 = lds_address(ring);
+  // the wave's i-th scale block into buffer `slot`
+  auto issue_block = [&](int i, int slot) {
+    const int kb = wave + T::WAVES * i;
+    const uint32_t at = ring0 + slot * T::kStage;
+    const bool past = kb >= kb_n, last = kb == kb_n - 1;
+#pragma unroll
+    for (int j = 0; j < T::P / 8; j++) {
+      int row, piece;
+      copy_place(8 * j, row, piece);
+      copy16(bp, at + j * 1024, past || (last && piece >= last_pieces) ? kOob : vp[j] + kb * kFp8Block);
+    }
+#pragma unroll
+    for (int j = 0; j < T::Q / 8; j++) {
+      int row, piece;
+      copy_place(8 * j, row, piece);
+      copy16(bq, at + T::P * kFp8Block + j * 1024, past || (last && piece >= last_pieces) ? kOob : vq[j] + kb * kFp8Block);
+    }
+    copy4(bsq, at + (T::P + T::Q) * kFp8Block, past ? kOob : vsq + kb * 4);
+    copy4(bsp, at + (T::P + T::Q) * kFp8Block + kWave * 4, past || lane != 0 ? kOob : kb * 4);
+  };
+  float4v acc[T::TP][T::TQ] = {};
+#pragma unroll
+  for (int i = 0; i < T::STAGES; i++) issue_block(i, i);
+  int slot = 0;
+  for (int i = 0; wave + T::WAVES * i < kb_n; i++) {
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(T::kCopies * (T::STAGES - 1)) : "memory");
+    const uint8_t *S = ring + slot * T::kStage;
+    const float *sc = reinterpret_cast<const float *>(S + (T::P + T::Q) * kFp8Block);
+    int8v q[T::TQ], p[T::TP];
+    float s[T::TQ];
+#pragma unroll
+    for (int j = 0; j < T::TQ; j++) {
+      q[j] = fragment(S + T::P * kFp8Block, j * 16 + r, lg);
+      s[j] = sc[j * 16 + r] * sc[kWave];
+    }
+#pragma unroll
+    for (int t = 0; t < T::TP; t++) p[t] = fragment(S, t * 16 + r, lg);
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // the buffer is read before it is filled again
+    issue_block(i + T::STAGES, slot);
+#pragma unroll
+    for (int t = 0; t < T::TP; t++)
+#pragma unroll
+      for (int j = 0; j < T::TQ; j++) {
+        const float4v v =
+            __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p[t], q[j], float4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 4; c++) acc[t][j][c] = fmaf(v[c], s[j], acc[t][j][c]);
+      }
+    slot = slot == T::STAGES - 1 ? 0 : slot + 1;
+  }
+  arrive<0>();
+  float4v *part = reinterpret_cast<float4v *>(lds);   // [wave][tile][lane]
+  constexpr int kTiles = T::TP * T::TQ;
+#pragma unroll
+  for (int t = 0; t < kTiles; t++) part[(wave * kTiles + t) * kWave + lane] = acc[t / T::TQ][t % T::TQ];
+  __syncthreads();
+  for (int t = wave; t < kTiles; t += T::WAVES) {
+    float4v sum = part[t * kWave + lane];
+#pragma unroll
+    for (int w = 1; w < T::WAVES; w++) sum += part[(w * kTiles + t) * kWave + lane];
+    const int n = n0 + t / T::TQ * 16 + 4 * lg, row = t % T::TQ * 16 + r;
+    if (row < count && n < P.N)
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.D) + static_cast<int64_t>(first + row) * P.N + n) = bf16x4(sum);
   }
 }
 
@@ -458,7 +788,7 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
   src.step_s = uniform(src.step_s);
 
   float4v acc[T::TP][T::TQ];
-  contract<T, true>(src, lds, steps, acc);
+  contract<T, true, false>(src, lds, steps, acc);
 
   const int wp = wave % T::WP, wq = wave / T::WP;
 #pragma unroll
@@ -488,6 +818,20 @@ hipError_t run_gemm(GemmParams p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <class T>
+hipError_t run_split(GemmParams p, hipStream_t stream) {
+  p.n_tiles = (p.N + T::P - 1) / T::P;
+  const int64_t items = groups::max_chunks(p.R, p.E, T::Q) * p.n_tiles;
+  const int64_t grid = (items + kXcds - 1) / kXcds * kXcds;
+  hipLaunchKernelGGL(split_kernel<T>, dim3(static_cast<uint32_t>(grid)), dim3(T::WAVES * kWave), 0, stream, p);
+  return hipGetLastError();
+}
+
+using Large = Tile<256, 256, 4, 2, 2>;
+constexpr int64_t kCacheBytes = 256 << 20;   // MI355X's memory-side cache
+constexpr int kManyTiles = 192;              // three quarters of the CUs
+constexpr int kLargeRows = 44;
+
 template <class T, Mode MODE>
 hipError_t run_wgrad(const WgradParams &p, hipStream_t stream) {
   const int64_t items = static_cast<int64_t>(p.E) * ((p.N + T::BQ - 1) / T::BQ) * ((p.K + T::BP - 1) / T::BP);
@@ -498,9 +842,28 @@ hipError_t run_wgrad(const WgradParams &p, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_gemm(const GemmParams &p, bool swiglu, hipStream_t stream) {
-  if (swiglu) return run_gemm<Tile<64, 256, 1, 4, 2>, kSwigluFp8>(p, stream);
-  return run_gemm<Tile<128, 128, 2, 2, 2>, kNone>(p, stream);
+hipError_t launch_gemm(GemmParams p, bool swiglu, hipStream_t stream) {
+  const int64_t hit = p.R < p.E ? p.R : p.E;   // at most so many experts have rows
+  if (hit == 0) return hipSuccess;
+  const int64_t mean = p.R / hit;
+  p.stream_weights = static_cast<int64_t>(p.E) * p.N * p.K > kCacheBytes / 2;
+  // tiles of q rows by c columns that there can be
+  auto tiles = [&](int q, int c) { return groups::max_chunks(p.R, p.E, q) * ((p.N + c - 1) / c); };
+  const bool large = mean > kLargeRows && p.K > 3 * kFp8Block && tiles(256, 256) >= kManyTiles;
+  if (swiglu) {
+    if (large) return run_gemm<Large, kSwigluFp8>(p, stream);
+    if (tiles(64, 256) < kManyTiles) return run_gemm<Tile<32, 256, 1, 4, 3>, kSwigluFp8>(p, stream);
+    return run_gemm<Tile<64, 256, 1, 8, 3>, kSwigluFp8>(p, stream);
+  }
+  if (large) return run_gemm<Large, kNone>(p, stream);
+  if (tiles(64, 128) < kManyTiles && p.K >= 4 * kFp8Block) {
+    if (mean <= 16) return run_split<Split<16, 8, 3>>(p, stream);
+    if (mean <= 32) return run_split<Split<32, 8, 2>>(p, stream);
+    return run_split<Split<64, 4, 3>>(p, stream);
+  }
+  if (mean > 2 * kLargeRows && tiles(128, 128) >= kManyTiles) return run_gemm<Tile<128, 128, 2, 2, 2>, kNone>(p, stream);
+  if (p.K <= 4 * kFp8Block) return run_gemm<Tile<64, 128, 1, 4, 2>, kNone>(p, stream);
+  return run_gemm<Tile<64, 128, 1, 4, 3>, kNone>(p, stream);
 }
 
 hipError_t launch_wgrad(const WgradParams &p, bool bf16, hipStream_t stream) {

@@ -17,7 +17,8 @@ struct GemmParams {
   int E, N, K, R;
   void *D;
   float *D_sf;
-  int n_tiles;              // set by the launcher
+  int n_tiles;              // set by the launcher, with:
+  bool stream_weights;      // the weights are too many to stay cached from one call to the next
 };
 
 struct WgradParams {
@@ -29,7 +30,7 @@ struct WgradParams {
   void *D;                  // [E, N, K]
 };
 
-hipError_t launch_gemm(const GemmParams &p, bool swiglu, hipStream_t stream);
+hipError_t launch_gemm(GemmParams p, bool swiglu, hipStream_t stream);
 hipError_t launch_wgrad(const WgradParams &p, bool bf16, hipStream_t stream);
 
 }  // namespace fp8

@@ -292,3 +292,69 @@ def test_product_gradients_match_differences():
         want = ((f(xc, up) - f(xc, w)) * cols).sum() / (5.0 - w[e, n, k])
         y = (f(xc, up).abs() + f(xc, w).abs())[:, n]
         assert abs(want - dw[e, n, k]) <= U16 * (y * cols[:, n].abs()).sum() / abs(5.0 - w[e, n, k]) + U32 * 1e3
+
+
+# ---- every kernel behind the product ----------------------------------------------------------
+
+def _values_gpu(q, s, per_tile):
+    v = torch.from_numpy(ref.e4m3_values()).cuda()[q.long()]
+    s = s.double().repeat_interleave(128, -1)[..., :q.shape[-1]]
+    if per_tile:
+        s = s.repeat_interleave(128, -2)[..., :q.shape[-2], :]
+    return v * s
+
+
+def _uneven(rng, E, mean, empty=0.1):
+    sizes = rng.integers(0, 2 * mean + 1, E) * (rng.random(E) >= empty)
+    sizes[E // 2] = 5 * mean      # one long group
+    return [int(s) for s in sizes]
+
+
+KERNELS = {
+    "few tiles, up to 16 rows": (6, 9, 272, 2064), "few tiles, up to 32 rows": (4, 26, 240, 1104),
+    "few tiles, more rows": (3, 80, 400, 656), "many tiles, short": (90, 12, 528, 400), "many tiles, long": (90, 20, 528, 1552),
+    "middle": (8, 220, 1648, 368), "large": (70, 70, 1040, 528), "large, four steps": (70, 60, 1024, 400),
+    "large, whole steps": (64, 200, 1024, 1024), "weights past the caches": (40, 6, 2048, 2064),
+    "weights past the caches, large": (72, 90, 2048, 1040),
+}
+
+
+@pytest.mark.parametrize("case", KERNELS)
+@pytest.mark.parametrize("gather", [False, True])
+def test_product_kernels(case, gather):
+    E, mean, N, K = KERNELS[case]
+    rng = np.random.default_rng(E * N + K)
+    g = torch.Generator(device="cuda").manual_seed(E + N)
+    sizes = _uneven(rng, E, mean)
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    R = int(off[-1])
+    a = moe.quantize_fp8_alloc(torch.randn(R // 2 + 1 if gather else R, K, generator=g, device="cuda").to(torch.bfloat16))
+    w = moe.quantize_fp8_weights_alloc(torch.randn(E, N, K, generator=g, device="cuda").to(torch.bfloat16))
+    rows = torch.randint(0, a.q.shape[0], (R,), generator=g, device="cuda", dtype=torch.int32) if gather else None
+    D = torch.full((R + 3, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_grouped_gemm_fp8(moe.make_gemm_fp8_args(a.q, a.sf, w.q, w.sf, dev(off), R, moe.MOE_EPI_NONE, D, A_rows=rows))
+    av = _values_gpu(a.q, a.sf, False)
+    av = av if rows is None else av[rows.long()]
+    swiglu = N % 256 == 0 and moe.grouped_gemm_fp8_alloc(a, w, dev(off), R, moe.MOE_EPI_SWIGLU_FP8, rows)
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        wv = _values_gpu(w.q[e], w.sf[e], True)
+        y, mag = av[lo:hi] @ wv.T, av[lo:hi].abs() @ wv.abs().T
+        err = (D[lo:hi].double() - y).abs()
+        bound = U16 * y.abs() + (1 + U16) * ref.core_error(K) * mag
+        assert (err <= bound).all(), (case, e, (err / bound).max().item())
+        if N % 256 == 0:
+            # as in test_swiglu_quantized
+            I = N // 2
+            gate, up, eb = y[:, :I], y[:, I:], ref.core_error(K) * mag
+            silu = gate / (1 + torch.exp(-gate))
+            want = silu * up
+            tol = 1.1 * up.abs() * eb[:, :I] + (silu.abs() + eb[:, :I]) * eb[:, I:] + (8 + 2 * gate.abs()) * 2 * U32 * want.abs()
+            s = swiglu.sf[lo:hi].double().repeat_interleave(128, 1)
+            got = _values_gpu(swiglu.q[lo:hi], swiglu.sf[lo:hi], False)
+            lim = (want.abs() + tol) * 2.0 ** -4 + s * 2.0 ** -10 + tol + 4 * U32 * want.abs()
+            assert ((got - want).abs() <= lim).all(), (case, e, "swiglu")
+    assert (D[R:] == 7.0).all()
+    again = torch.empty_like(D)
+    moe.moe_grouped_gemm_fp8(moe.make_gemm_fp8_args(a.q, a.sf, w.q, w.sf, dev(off), R, moe.MOE_EPI_NONE, again, A_rows=rows))
+    assert torch.equal(D[:R].view(torch.int16), again[:R].view(torch.int16))
