@@ -30,8 +30,6 @@
 #include "fp8_round.hpp"
 #include "groups.hpp"
 
-#include <type_traits>
-
 #pragma clang fp contract(off)
 
 namespace moe {
@@ -228,8 +226,8 @@ __device__ __forceinline__ Half32 to_f16(const int8v &v) {
 }
 
 // The whole contraction of one tile.  Scales of a stage: [0, BQ) of the Q rows, from kScaleP one
-// per half of P (WGRAD false) or one per P row.
-template <class T, bool WGRAD, bool ONCE>
+// per half of P.
+template <class T, bool ONCE>
 __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps, float4v (&acc)[T::TP][T::TQ]) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x & 63, g = lane / 16, r = lane % 16;
@@ -248,41 +246,26 @@ __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps
     issue<T, ONCE>(src, lds0 + next * T::kStage, wave, kb + T::STAGES - 1, steps);
     const uint8_t *P = lds + slot * T::kStage, *Q = P + T::kBytesP;
     const float *S = reinterpret_cast<const float *>(Q + T::kBytesQ);
-    using Frag = std::conditional_t<WGRAD, Half32, int8v>;
-    Frag q[T::TQ];
+    int8v q[T::TQ];
     float sq[T::TQ];
 #pragma unroll
     for (int j = 0; j < T::TQ; j++) {
       const int row = (wq * T::TQ + j) * 16 + r;
-      if constexpr (WGRAD) q[j] = to_f16(fragment(Q, row, g));
-      else q[j] = fragment(Q, row, g);
+      q[j] = fragment(Q, row, g);
       sq[j] = S[row];
     }
 #pragma unroll
     for (int i = 0; i < T::TP; i++) {
       const int row0 = (i / T::kPerHalf) * kFp8Block + wp * (kFp8Block / T::WP) + (i % T::kPerHalf) * 16;
       const int8v p = fragment(P, row0 + r, g);
-      if constexpr (WGRAD) {
-        const Half32 ph = to_f16(p);
-        const float4v sp = *reinterpret_cast<const float4v *>(S + T::kScaleP + row0 + 4 * g);
+      const float sp = S[T::kScaleP + i / T::kPerHalf];
 #pragma unroll
-        for (int j = 0; j < T::TQ; j++) {
-          float4v t = {0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < T::TQ; j++) {
+        const float4v t =
+            __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q[j], float4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+        const float s = sp * sq[j];
 #pragma unroll
-          for (int h = 0; h < 4; h++) t = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph.h[h], q[j].h[h], t, 0, 0, 0);
-#pragma unroll
-          for (int c = 0; c < 4; c++) acc[i][j][c] = fmaf(t[c], sp[c] * sq[j], acc[i][j][c]);
-        }
-      } else {
-        const float sp = S[T::kScaleP + i / T::kPerHalf];
-#pragma unroll
-        for (int j = 0; j < T::TQ; j++) {
-          const float4v t =
-              __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q[j], float4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-          const float s = sp * sq[j];
-#pragma unroll
-          for (int c = 0; c < 4; c++) acc[i][j][c] = fmaf(t[c], s, acc[i][j][c]);
-        }
+        for (int c = 0; c < 4; c++) acc[i][j][c] = fmaf(t[c], s, acc[i][j][c]);
       }
     }
     slot = slot == T::STAGES - 1 ? 0 : slot + 1;
@@ -537,10 +520,10 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
   // second one finds them in L2, 35 us against 24 us for 77 MB)
   if (g.total == 1 && P.stream_weights) {
     if constexpr (T::kLarge) contract_large<T, true>(src, lds, kb_n, count, acc);
-    else contract<T, false, true>(src, lds, kb_n, acc);
+    else contract<T, true>(src, lds, kb_n, acc);
   } else {
     if constexpr (T::kLarge) contract_large<T, false>(src, lds, kb_n, count, acc);
-    else contract<T, false, false>(src, lds, kb_n, acc);
+    else contract<T, false>(src, lds, kb_n, acc);
   }
 
   const int wp = wave % T::WP, wq = wave / T::WP;
@@ -735,75 +718,149 @@ __global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams
   }
 }
 
+// ---- the weight gradient -----------------------------------------------------------------------
+//
+// A tile of D has a few steps (one per 128 tokens of its expert).  Measured, 16 experts of 512 rows, N
+// 4096, K 6144, binary32 D (412 GFLOP, 1.6 GB written): 605 us; 64 rows each: 284 us, 5.7 TB/s
+// written.  Per step and wave 64 MFMAs (1024 cycles) stand against 128 conversions and 128
+// scalings (1024), which the MFMAs hide in part only.  One pipeline through several tiles, the
+// next one's first stage copied during the last step: 620 to 710 us.
+struct GradTile {
+  Buf p, q, s;     // this wave's stages: X codes, Y codes, scales of one of them
+  int steps;       // token blocks
+  int e, n0, k0;
+};
+
+template <class T>
+__device__ __forceinline__ bool grad_tile(const WgradParams &P, int wave, GradTile &t) {
+  const int n_tiles = (P.N + T::BQ - 1) / T::BQ, k_tiles = (P.K + T::BP - 1) / T::BP, per = n_tiles * k_tiles;
+  int64_t w;
+  if (!item_of(blockIdx.x, static_cast<int64_t>(P.E) * per, w)) return false;
+  t.e = static_cast<int>(w / per);
+  int nt, kt;
+  place_in_band(static_cast<int>(w - static_cast<int64_t>(t.e) * per), n_tiles, k_tiles, nt, kt);
+  t.n0 = nt * T::BQ;
+  t.k0 = kt * T::BP;
+  const int b0 = groups::chunks_before(P.offsets, t.e, P.E, P.R, kFp8Block);
+  int lo = __builtin_amdgcn_readfirstlane(P.offsets[t.e]), hi = __builtin_amdgcn_readfirstlane(P.offsets[t.e + 1]);
+  groups::clamp_pair(lo, hi, P.R);
+  t.steps = (hi - lo + kFp8Block - 1) / kFp8Block;
+  t.steps = max(0, min(t.steps, P.blocks - b0));   // offsets that are not monotone stay inside the buffers
+  const bool of_q = wave * kWave < T::BQ;
+  const uint32_t rows_p = min(T::BP, P.K - t.k0), rows_q = min(T::BQ, P.N - t.n0);
+  t.p.base = reinterpret_cast<uint64_t>(P.X) + (static_cast<uint64_t>(b0) * P.K + t.k0) * kFp8Block;
+  t.q.base = reinterpret_cast<uint64_t>(P.Y) + (static_cast<uint64_t>(b0) * P.N + t.n0) * kFp8Block;
+  t.s.base = of_q ? reinterpret_cast<uint64_t>(P.Y_sf) + (static_cast<uint64_t>(b0) * P.N + t.n0) * 4
+                  : reinterpret_cast<uint64_t>(P.X_sf) + (static_cast<uint64_t>(b0) * P.K + t.k0) * 4;
+  t.p.bytes = rows_p * kFp8Block;
+  t.q.bytes = rows_q * kFp8Block;
+  t.s.bytes = 4 * (of_q ? rows_q : rows_p);
+  t.p = uniform(t.p);
+  t.q = uniform(t.q);
+  t.s = uniform(t.s);
+  return true;
+}
+
 template <class T, Mode MODE>
 __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P) {
+  static_assert(T::BQ % kWave == 0 && T::BQ + T::BP <= T::kThreadsT && T::STAGES == 2 && !T::kLarge, "the schedule below");
   __shared__ __align__(1024) uint8_t lds[T::kLds];
-  const int n_tiles = (P.N + T::BQ - 1) / T::BQ, k_tiles = (P.K + T::BP - 1) / T::BP;
-  int64_t w;
-  if (!item_of(blockIdx.x, static_cast<int64_t>(P.E) * n_tiles * k_tiles, w)) return;
-  const int per = n_tiles * k_tiles;
-  const int e = static_cast<int>(w / per);
-  int nt, kt;
-  place_in_band(static_cast<int>(w - static_cast<int64_t>(e) * per), n_tiles, k_tiles, nt, kt);
-  const int n0 = nt * T::BQ, k0 = kt * T::BP;
-  // the expert's token blocks
-  const int b0 = groups::chunks_before(P.offsets, e, P.E, P.R, kFp8Block);
-  int lo = __builtin_amdgcn_readfirstlane(P.offsets[e]), hi = __builtin_amdgcn_readfirstlane(P.offsets[e + 1]);
-  groups::clamp_pair(lo, hi, P.R);
-  int steps = (hi - lo + kFp8Block - 1) / kFp8Block;
-  steps = max(0, min(steps, P.blocks - b0));   // offsets that are not monotone stay inside the buffers
-
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int lane = threadIdx.x & 63, lg = lane / 16, r = lane % 16;
-  Source<T> src;
-  src.last_pieces = 8;
-  src.step_p = static_cast<uint32_t>(P.K) * kFp8Block;
-  src.step_q = static_cast<uint32_t>(P.N) * kFp8Block;
-  src.p.base = reinterpret_cast<uint64_t>(P.X) + (static_cast<uint64_t>(b0) * P.K + k0) * kFp8Block;
-  src.p.bytes = static_cast<uint32_t>(min(T::BP, P.K - k0)) * kFp8Block;
-  src.q.base = reinterpret_cast<uint64_t>(P.Y) + (static_cast<uint64_t>(b0) * P.N + n0) * kFp8Block;
-  src.q.bytes = static_cast<uint32_t>(min(T::BQ, P.N - n0)) * kFp8Block;
+  const int lane = threadIdx.x & 63, g = lane / 16, r = lane % 16;
+  const int wp = wave % T::WP, wq = wave / T::WP;
+  const uint32_t lds0 = lds_address(lds);
+  uint32_t vp[T::kCopiesP], vq[T::kCopiesQ];
 #pragma unroll
   for (int j = 0; j < T::kCopiesP; j++) {
     int row, piece;
     copy_place((wave * T::kCopiesP + j) * 8, row, piece);
-    src.vp[j] = row * kFp8Block + piece * 16;
+    vp[j] = row * kFp8Block + piece * 16;
   }
 #pragma unroll
   for (int j = 0; j < T::kCopiesQ; j++) {
     int row, piece;
     copy_place((wave * T::kCopiesQ + j) * 8, row, piece);
-    src.vq[j] = row * kFp8Block + piece * 16;
+    vq[j] = row * kFp8Block + piece * 16;
   }
-  static_assert(T::BQ % kWave == 0 && T::BQ + T::BP <= T::kThreadsT, "one scale copy per wave serves both operands");
-  const int slot0 = wave * kWave;
-  const bool of_q = slot0 < T::BQ;
-  src.s.base = of_q ? reinterpret_cast<uint64_t>(P.Y_sf) + (static_cast<uint64_t>(b0) * P.N + n0) * 4
-                    : reinterpret_cast<uint64_t>(P.X_sf) + (static_cast<uint64_t>(b0) * P.K + k0) * 4;
-  src.s.bytes = 4 * static_cast<uint32_t>(of_q ? min(T::BQ, P.N - n0) : min(T::BP, P.K - k0));
-  src.step_s = 4 * static_cast<uint32_t>(of_q ? P.N : P.K);
-  src.vs = 4 * static_cast<uint32_t>(slot0 + lane - (of_q ? 0 : T::BQ));
-
-  src.s = uniform(src.s);
-  src.step_s = uniform(src.step_s);
-
+  const bool of_q = wave * kWave < T::BQ;
+  const uint32_t vs = 4 * static_cast<uint32_t>(wave * kWave + lane - (of_q ? 0 : T::BQ));
+  const uint32_t step_p = static_cast<uint32_t>(P.K) * kFp8Block, step_q = static_cast<uint32_t>(P.N) * kFp8Block;
+  const uint32_t step_s = uniform(4u * static_cast<uint32_t>(of_q ? P.N : P.K));
+  GradTile t;
+  if (!grad_tile<T>(P, wave, t)) return;
+  auto issue_stage = [&](int kb) {   // past the last one: nothing
+    const uint32_t at = lds0 + (kb & 1) * T::kStage;
+    if (kb >= t.steps) t.p.bytes = t.q.bytes = t.s.bytes = 0;
+#pragma unroll
+    for (int j = 0; j < T::kCopiesP; j++) copy16(t.p, at + (wave * T::kCopiesP + j) * 8 * kFp8Block, vp[j]);
+#pragma unroll
+    for (int j = 0; j < T::kCopiesQ; j++) copy16(t.q, at + T::kBytesP + (wave * T::kCopiesQ + j) * 8 * kFp8Block, vq[j]);
+    copy4(t.s, at + T::kBytesP + T::kBytesQ + wave * kWave * 4, vs);
+    t.p.base += step_p;
+    t.q.base += step_q;
+    t.s.base += step_s;
+  };
   float4v acc[T::TP][T::TQ];
-  contract<T, true, false>(src, lds, steps, acc);
-
-  const int wp = wave % T::WP, wq = wave / T::WP;
+#pragma unroll
+  for (int i = 0; i < T::TP; i++)
+#pragma unroll
+    for (int j = 0; j < T::TQ; j++) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
+  issue_stage(0);
+  for (int kb = 0; kb < t.steps; kb++) {
+    arrive<0>();
+    issue_stage(kb + 1);
+    const uint8_t *Ps = lds + (kb & 1) * T::kStage, *Qs = Ps + T::kBytesP;
+    const float *S = reinterpret_cast<const float *>(Qs + T::kBytesQ);
+    Half32 q[T::TQ];
+    float sq[T::TQ];
+#pragma unroll
+    for (int j = 0; j < T::TQ; j++) {
+      const int row = (wq * T::TQ + j) * 16 + r;
+      q[j] = to_f16(fragment(Qs, row, g));
+      sq[j] = S[row];
+    }
+#pragma unroll
+    for (int i = 0; i < T::TP; i++) {
+      const int row0 = (i / T::kPerHalf) * kFp8Block + wp * (kFp8Block / T::WP) + (i % T::kPerHalf) * 16;
+      const Half32 p = to_f16(fragment(Ps, row0 + r, g));
+      const float4v sp = *reinterpret_cast<const float4v *>(S + T::kScaleP + row0 + 4 * g);
+      float4v v[T::TQ];
+#pragma unroll
+      for (int j = 0; j < T::TQ; j++) v[j] = float4v{0.f, 0.f, 0.f, 0.f};
+      // piece by piece over all columns: neighbouring MFMAs do not wait for each other
+#pragma unroll
+      for (int h = 0; h < 4; h++)
+#pragma unroll
+        for (int j = 0; j < T::TQ; j++) v[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(p.h[h], q[j].h[h], v[j], 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < T::TQ; j++)
+#pragma unroll
+        for (int c = 0; c < 4; c++) acc[i][j][c] = fmaf(v[j][c], sp[c] * sq[j], acc[i][j][c]);
+    }
+  }
+  arrive<0>();   // the copies past the end (zeros) are in before the buffers serve anything else
+  // each wave turns 16 rows of its tile at a time in LDS and stores whole pieces of them (16 rows
+  // of 64 bytes straight from the MFMA layout: 444 us against 306 us where every expert has one step)
+  constexpr int kElem = MODE == kWgradF32 ? 4 : 2, kRow = T::TP * 16 * kElem, kStride = kRow + 16;   // bytes
+  constexpr int kCols = kFp8Block / T::WP, kPieces = kRow / kWave, kPer = 16 / kElem;
+  static_assert(kPieces >= 1 && T::kWaves * 16 * kStride <= T::kBytesP + T::kBytesQ, "staging");
+  uint8_t *mine = lds + wave * 16 * kStride;
 #pragma unroll
   for (int j = 0; j < T::TQ; j++) {
-    const int n = n0 + (wq * T::TQ + j) * 16 + r;
-    if (n >= P.N) continue;
-    const int64_t row = (static_cast<int64_t>(e) * P.N + n) * P.K;
 #pragma unroll
     for (int ti = 0; ti < T::TP; ti++) {
-      const int k = k0 + (ti / T::kPerHalf) * kFp8Block + wp * (kFp8Block / T::WP) + (ti % T::kPerHalf) * 16 + 4 * lg;
-      if (k >= P.K) continue;
-      if (MODE == kWgradF32)
-        *reinterpret_cast<float4v *>(static_cast<float *>(P.D) + row + k) = acc[ti][j];
-      else
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.D) + row + k) = bf16x4(acc[ti][j]);
+      uint8_t *at = mine + r * kStride + (ti * 16 + 4 * g) * kElem;
+      if (MODE == kWgradF32) *reinterpret_cast<float4v *>(at) = acc[ti][j];
+      else *reinterpret_cast<uint2 *>(at) = bf16x4(acc[ti][j]);
+    }
+#pragma unroll
+    for (int c = 0; c < kPieces; c++) {
+      const int at = c * kWave + lane, row = at / (kRow / 16), col = at % (kRow / 16) * kPer;   // col: of the wave's columns
+      const int n = t.n0 + (wq * T::TQ + j) * 16 + row;
+      const int k = t.k0 + col / kCols * kFp8Block + wp * kCols + col % kCols;
+      const uint4 v = *reinterpret_cast<const uint4 *>(mine + row * kStride + col * kElem);
+      if (n >= P.N || k >= P.K) continue;
+      store16<true>(static_cast<uint8_t *>(P.D) + ((static_cast<int64_t>(t.e) * P.N + n) * P.K + k) * kElem, v);
     }
   }
 }

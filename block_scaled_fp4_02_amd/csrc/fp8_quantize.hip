@@ -79,13 +79,47 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const void *__rest
   if (threadIdx.x % kLanes == 0) sf[b] = s.scale;
 }
 
+// Byte b of four words, for b = 0..3.
+__device__ __forceinline__ void turn4(const uint32_t (&w)[4], uint32_t (&t)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400), b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602);
+  const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602);
+  t[0] = __builtin_amdgcn_perm(c, a, 0x05040100);
+  t[1] = __builtin_amdgcn_perm(c, a, 0x07060302);
+  t[2] = __builtin_amdgcn_perm(d, b, 0x05040100);
+  t[3] = __builtin_amdgcn_perm(d, b, 0x07060302);
+}
+
+// Columns of a 128 x 128 tile of codes in LDS as rows of `out`: column c of the tile is row c0 + c
+// (< rows_end), its elements stand from column n0 (< cols_end) on.  A thread turns 16 x 4 codes, and
+// 8 neighbouring lanes write one row's 128 bytes (with 8 bytes a lane and neighbouring lanes on
+// other rows the weight quantiser takes 400 us instead of 330 us for 403 M weights).
+typedef uint32_t TileRow[kFp8Block / 4 + 1];   // one word of padding
+__device__ __forceinline__ void store_turned(const TileRow *tile, uint8_t *out, int c0, int rows_end, int n0, int cols_end,
+                                             int64_t stride) {
+  const int part = threadIdx.x % 8, word = threadIdx.x / 8;
+  uint32_t t[4][4];   // [group of 4 elements][column]
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) w[j] = tile[16 * part + 4 * i + j][word];
+    turn4(w, t[i]);
+  }
+#pragma unroll
+  for (int b = 0; b < 4; b++) {
+    const int row = c0 + 4 * word + b, col = n0 + 16 * part;
+    if (row < rows_end && col < cols_end)
+      *reinterpret_cast<uint4 *>(out + row * stride + col) = make_uint4(t[0][b], t[1][b], t[2][b], t[3][b]);
+  }
+}
+
 // One 128 x 128 tile of one expert per workgroup; a thread holds 8 columns of 8 rows.
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void quant_weights_kernel(const void *__restrict__ w, int N, int K, int nb, int kb,
                                                                  uint8_t *__restrict__ q, float *__restrict__ sf,
                                                                  uint8_t *__restrict__ qt, float *__restrict__ sft) {
   __shared__ uint32_t wave_amax[kThreads / kWave];
-  __shared__ uint32_t tile[kFp8Block][kFp8Block / 4 + 1];   // codes, one word of padding per row
+  __shared__ TileRow tile[kFp8Block];   // codes
   const int tk = blockIdx.x % kb, tn = blockIdx.x / kb % nb;
   const int64_t e = blockIdx.x / kb / nb;
   const int n0 = tn * kFp8Block, k0 = tk * kFp8Block;
@@ -122,27 +156,7 @@ __global__ __launch_bounds__(kThreads) void quant_weights_kernel(const void *__r
   }
   if (!qt) return;
   __syncthreads();
-  // column k0 + 4 lw + b of the tile becomes a row of qt: a thread gathers 8 rows' words and
-  // writes the 8 bytes of each of its four columns
-  const int lw = threadIdx.x % 32, ln = threadIdx.x / 32;
-#pragma unroll
-  for (int h = 0; h < 2; h++) {
-    const int row = 8 * (ln + 8 * h);
-    uint32_t v[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = tile[row + i][lw];
-#pragma unroll
-    for (int b = 0; b < 4; b++) {
-      const int k = k0 + 4 * lw + b, n = n0 + row;
-      uint32_t lo = 0, hi = 0;
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        lo |= ((v[i] >> (8 * b)) & 0xffu) << (8 * i);
-        hi |= ((v[4 + i] >> (8 * b)) & 0xffu) << (8 * i);
-      }
-      if (k < K && n < N) *reinterpret_cast<uint2 *>(qt + base + static_cast<int64_t>(k) * N + n) = make_uint2(lo, hi);
-    }
-  }
+  store_turned(tile, qt + base, k0, K, n0, N, N);
 }
 
 // One block of up to 128 rows of a group, 128 columns, per workgroup: a scale per column, and
@@ -154,7 +168,7 @@ __global__ __launch_bounds__(kThreads) void quant_tokens_kernel(const void *__re
                                                                 int col_tiles, uint8_t *__restrict__ q,
                                                                 float *__restrict__ sf) {
   __shared__ uint32_t col_amax[kThreads / kWave][kFp8Block];
-  __shared__ uint32_t tile[kFp8Block][kFp8Block / 4 + 1];
+  __shared__ TileRow tile[kFp8Block];
   const int blk = blockIdx.x / col_tiles, c0 = blockIdx.x % col_tiles * kFp8Block;
   groups::Chunk g;
   if (!groups::find_chunk(offsets, E, R, kFp8Block, blk, g)) return;
@@ -208,26 +222,7 @@ __global__ __launch_bounds__(kThreads) void quant_tokens_kernel(const void *__re
                     fp8_quotient(r[i].v[4 * h + 2], s[4 * h + 2]), fp8_quotient(r[i].v[4 * h + 3], s[4 * h + 3]));
   }
   __syncthreads();
-  const int lw = threadIdx.x % 32, ln = threadIdx.x / 32;
-#pragma unroll
-  for (int h = 0; h < 2; h++) {
-    const int t = 8 * (ln + 8 * h);
-    uint32_t v[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = tile[t + i][lw];
-#pragma unroll
-    for (int b = 0; b < 4; b++) {
-      const int col = c0 + 4 * lw + b;
-      uint32_t lo = 0, hi = 0;
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        lo |= ((v[i] >> (8 * b)) & 0xffu) << (8 * i);
-        hi |= ((v[4 + i] >> (8 * b)) & 0xffu) << (8 * i);
-      }
-      if (col < C)
-        *reinterpret_cast<uint2 *>(q + (static_cast<int64_t>(blk) * C + col) * kFp8Block + t) = make_uint2(lo, hi);
-    }
-  }
+  store_turned(tile, q + static_cast<int64_t>(blk) * C * kFp8Block, c0, C, 0, kFp8Block, kFp8Block);
 }
 
 }  // namespace
