@@ -16,9 +16,9 @@ struct LossParams {
   float *coef;                  // [S, E]
   float *loss;
   // workspace, laid out by the launcher
-  int chunks;
+  int chunks, chunk;            // partial rows, and the most tokens of one
   uint32_t *ticket;
-  double *part_loss;            // [S, ceil(E / 64)]
+  double *part_loss;            // one per workgroup of the second kernel
   int32_t *part_kept;           // [chunks]
   int32_t *part_count;          // [chunks, E]
   float *part_sum;              // [chunks, E]

@@ -441,11 +441,12 @@ __device__ __forceinline__ void place_in_band(int l, int chunks, int tiles, int 
 
 // The item of this workgroup: group g, its chunk of `size` rows and n tile.
 __device__ __forceinline__ bool find_item(const GemmParams &P, int size, groups::Chunk &g, int &chunk, int &nt) {
-  int64_t w;
-  const int total = groups::chunk_count(P.offsets, P.E, P.R, size);
-  if (!item_of(blockIdx.x, static_cast<int64_t>(total) * P.n_tiles, w)) return false;
-  const int i = static_cast<int>(w / P.n_tiles);
-  if (!groups::find_chunk(P.offsets, P.E, P.R, size, i, g)) return false;
+  int64_t w = 0;
+  int i;
+  auto index = [&](int total) {
+    return item_of(blockIdx.x, static_cast<int64_t>(total) * P.n_tiles, w) ? static_cast<int>(w / P.n_tiles) : -1;
+  };
+  if (!groups::find_chunk_of_all(P.offsets, P.E, P.R, size, index, i, g)) return false;
   place_in_band(static_cast<int>(w - static_cast<int64_t>(i - g.index) * P.n_tiles), g.total, P.n_tiles, chunk, nt);
   return true;
 }

@@ -25,24 +25,35 @@ struct Vec8 {
   float v[8];
 };
 
-// Eight consecutive elements at element offset `at` (a multiple of 8).
+// Eight consecutive elements from element offset `at` (a multiple of 8) as they stand in memory.
 template <bool BF16>
-__device__ __forceinline__ Vec8 load8(const void *x, int64_t at) {
-  Vec8 r;
-  if (BF16) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + at);
-    const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+struct Raw8 {
+  uint4 w[BF16 ? 1 : 2];
+};
+template <bool BF16>
+__device__ __forceinline__ Raw8<BF16> load_raw8(const void *x, int64_t at) {
+  Raw8<BF16> r;
+  const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(x) + at * (BF16 ? 2 : 4));
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); i++) r.w[i] = p[i];
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ Vec8 values(const Raw8<BF16> &r) {
+  if constexpr (BF16) {
+    const uint32_t p[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+    Vec8 v;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      r.v[2 * i] = __uint_as_float(p[i] << 16);
-      r.v[2 * i + 1] = __uint_as_float(p[i] & 0xffff0000u);
+      v.v[2 * i] = __uint_as_float(p[i] << 16);
+      v.v[2 * i + 1] = __uint_as_float(p[i] & 0xffff0000u);
     }
+    return v;
   } else {
-    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(x) + at);
-    const float4 a = p[0], b = p[1];
-    r = {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+    const uint4 a = r.w[0], b = r.w[1];
+    return {{__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w), __uint_as_float(b.x),
+             __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)}};
   }
-  return r;
 }
 
 __device__ __forceinline__ uint32_t amax8(const Vec8 &r) {
@@ -71,8 +82,9 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const void *__rest
   const uint32_t row = bc / per_row;
   const int c = static_cast<int>(bc - row * per_row) * kFp8Block + 8 * static_cast<int>(threadIdx.x % kLanes);
   const int64_t at = static_cast<int64_t>(row) * C + c;
-  Vec8 r = {};
-  if (c < C) r = load8<BF16>(x, at);
+  Raw8<BF16> raw = {};
+  if (c < C) raw = load_raw8<BF16>(x, at);
+  const Vec8 r = values(raw);
   const Fp8Block s = fp8_block(max_over16(amax8(r)));
   if (b >= nblk) return;
   if (c < C) *reinterpret_cast<uint2 *>(q + at) = codes8(r, s);
@@ -115,7 +127,7 @@ __device__ __forceinline__ void store_turned(const TileRow *tile, uint8_t *out, 
 
 // One 128 x 128 tile of one expert per workgroup; a thread holds 8 columns of 8 rows.
 template <bool BF16>
-__global__ __launch_bounds__(kThreads) void quant_weights_kernel(const void *__restrict__ w, int N, int K, int nb, int kb,
+__global__ __launch_bounds__(kThreads, 6) void quant_weights_kernel(const void *__restrict__ w, int N, int K, int nb, int kb,
                                                                  uint8_t *__restrict__ q, float *__restrict__ sf,
                                                                  uint8_t *__restrict__ qt, float *__restrict__ sft) {
   __shared__ uint32_t wave_amax[kThreads / kWave];
@@ -125,16 +137,16 @@ __global__ __launch_bounds__(kThreads) void quant_weights_kernel(const void *__r
   const int n0 = tn * kFp8Block, k0 = tk * kFp8Block;
   const int lr = threadIdx.x / kLanes, lc = threadIdx.x % kLanes;
   const int64_t base = e * N * K;
-  Vec8 r[8];
+  Raw8<BF16> r[8];
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; i++) {
     const int n = n0 + lr + kRows * i, k = k0 + 8 * lc;
     r[i] = {};
-    if (n < N && k < K) r[i] = load8<BF16>(w, base + static_cast<int64_t>(n) * K + k);
+    if (n < N && k < K) r[i] = load_raw8<BF16>(w, base + static_cast<int64_t>(n) * K + k);
   }
 #pragma unroll
-  for (int i = 0; i < 8; i++) m = max(m, amax8(r[i]));
+  for (int i = 0; i < 8; i++) m = max(m, amax8(values(r[i])));
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), o, kWave)));
   if (threadIdx.x % kWave == 0) wave_amax[threadIdx.x / kWave] = m;
@@ -145,7 +157,7 @@ __global__ __launch_bounds__(kThreads) void quant_weights_kernel(const void *__r
 #pragma unroll
   for (int i = 0; i < 8; i++) {
     const int row = lr + kRows * i, n = n0 + row, k = k0 + 8 * lc;
-    const uint2 c = codes8(r[i], s);
+    const uint2 c = codes8(values(r[i]), s);
     if (n < N && k < K) *reinterpret_cast<uint2 *>(q + base + static_cast<int64_t>(n) * K + k) = c;
     tile[row][2 * lc] = c.x;
     tile[row][2 * lc + 1] = c.y;
@@ -162,7 +174,7 @@ __global__ __launch_bounds__(kThreads) void quant_weights_kernel(const void *__r
 // One block of up to 128 rows of a group, 128 columns, per workgroup: a scale per column, and
 // the codes of a column contiguous: q [block][C][128], zeros behind the group's last row.
 template <bool BF16>
-__global__ __launch_bounds__(kThreads) void quant_tokens_kernel(const void *__restrict__ x, int64_t rows_x,
+__global__ __launch_bounds__(kThreads, 6) void quant_tokens_kernel(const void *__restrict__ x, int64_t rows_x,
                                                                 const int32_t *__restrict__ rows,
                                                                 const int32_t *__restrict__ offsets, int E, int R, int C,
                                                                 int col_tiles, uint8_t *__restrict__ q,
@@ -175,7 +187,7 @@ __global__ __launch_bounds__(kThreads) void quant_tokens_kernel(const void *__re
   const int first = g.lo + g.index * kFp8Block, count = min(kFp8Block, g.hi - first);
   const int lr = threadIdx.x / kLanes, lc = threadIdx.x % kLanes;
   const int c = c0 + 8 * lc;
-  Vec8 r[8];
+  Raw8<BF16> r[8];
   int64_t src[8];
 #pragma unroll
   for (int i = 0; i < 8; i++) {
@@ -187,15 +199,18 @@ __global__ __launch_bounds__(kThreads) void quant_tokens_kernel(const void *__re
 #pragma unroll
   for (int i = 0; i < 8; i++) {
     r[i] = {};
-    if (lr + kRows * i < count && c < C) r[i] = load8<BF16>(x, src[i] * C + c);
+    if (lr + kRows * i < count && c < C) r[i] = load_raw8<BF16>(x, src[i] * C + c);
   }
   // column maxima: over the thread's 8 rows, the wave's 4 row groups, then the 4 waves
-  uint32_t m[8];
+  uint32_t m[8] = {};
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const Vec8 v = values(r[i]);
+#pragma unroll
+    for (int j = 0; j < 8; j++) m[j] = max(m[j], abs_bits(v.v[j]));
+  }
 #pragma unroll
   for (int j = 0; j < 8; j++) {
-    m[j] = 0;
-#pragma unroll
-    for (int i = 0; i < 8; i++) m[j] = max(m[j], abs_bits(r[i].v[j]));
     m[j] = max(m[j], static_cast<uint32_t>(__shfl_xor(static_cast<int>(m[j]), 16, kWave)));
     m[j] = max(m[j], static_cast<uint32_t>(__shfl_xor(static_cast<int>(m[j]), 32, kWave)));
   }
@@ -214,12 +229,12 @@ __global__ __launch_bounds__(kThreads) void quant_tokens_kernel(const void *__re
   }
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    const int t = lr + kRows * i;
+    const Vec8 v = values(r[i]);
 #pragma unroll
     for (int h = 0; h < 2; h++)
-      tile[t][2 * lc + h] =
-          fp8_pack4(fp8_quotient(r[i].v[4 * h], s[4 * h]), fp8_quotient(r[i].v[4 * h + 1], s[4 * h + 1]),
-                    fp8_quotient(r[i].v[4 * h + 2], s[4 * h + 2]), fp8_quotient(r[i].v[4 * h + 3], s[4 * h + 3]));
+      tile[lr + kRows * i][2 * lc + h] =
+          fp8_pack4(fp8_quotient(v.v[4 * h], s[4 * h]), fp8_quotient(v.v[4 * h + 1], s[4 * h + 1]),
+                    fp8_quotient(v.v[4 * h + 2], s[4 * h + 2]), fp8_quotient(v.v[4 * h + 3], s[4 * h + 3]));
   }
   __syncthreads();
   store_turned(tile, q + static_cast<int64_t>(blk) * C * kFp8Block, c0, C, 0, kFp8Block, kFp8Block);

@@ -32,77 +32,96 @@ __device__ __forceinline__ void clamp_pair(int &lo, int &hi, int limit) {
   hi = hi < lo ? lo : (hi > limit ? limit : hi);
 }
 
-// Chunks of `size` rows held by the groups base + 4 * lane + q, q = 0..3, of this lane.
-__device__ __forceinline__ void lane_chunks(const int32_t *off, int G, int limit, int size, int base, int (&n)[4]) {
+// The groups base + 4 * lane + q, q = 0..3, of this lane: rows [lo, hi), n chunks of `size` rows; and
+// the chunks of all lanes' groups up to this lane's last and in all.
+struct Round {
+  int lo[4], hi[4], n[4];
+  int mine, incl, sum;
+};
+
+__device__ __forceinline__ Round round_of(const int32_t *off, int G, int limit, int size, int base) {
+  Round r;
   const int g0 = base + 4 * static_cast<int>(threadIdx.x & 63);
   int o[5];
 #pragma unroll
   for (int q = 0; q < 5; q++) o[q] = off[min(g0 + q, G)];
+  r.mine = 0;
 #pragma unroll
   for (int q = 0; q < 4; q++) {
-    int lo = o[q], hi = o[q + 1];
-    clamp_pair(lo, hi, limit);
-    n[q] = g0 + q < G ? (hi - lo + size - 1) / size : 0;
+    r.lo[q] = o[q];
+    r.hi[q] = o[q + 1];
+    clamp_pair(r.lo[q], r.hi[q], limit);
+    r.n[q] = g0 + q < G ? (r.hi[q] - r.lo[q] + size - 1) / size : 0;
+    r.mine += r.n[q];
   }
+  r.incl = wave_inclusive_sum(r.mine);
+  r.sum = __builtin_amdgcn_readlane(r.incl, kWave - 1);
+  return r;
+}
+
+// Chunk `i` of a round's (i < r.sum), read out of the lane that has it.
+__device__ __forceinline__ Chunk pick(const Round &r, int base, int i) {
+  const int local = i - (r.incl - r.mine);
+  const int src = __builtin_ctzll(__ballot(local >= 0 && local < r.mine));
+  Chunk c = {};
+  c.index = __builtin_amdgcn_readlane(local, src);
+#pragma unroll
+  for (int q = 0; q < 4; q++) {
+    const int n = __builtin_amdgcn_readlane(r.n[q], src);
+    if (c.total == 0) {
+      if (c.index < n) {
+        c.group = base + 4 * src + q;
+        c.total = n;
+        c.lo = __builtin_amdgcn_readlane(r.lo[q], src);
+        c.hi = __builtin_amdgcn_readlane(r.hi[q], src);
+      } else {
+        c.index -= n;
+      }
+    }
+  }
+  return c;
 }
 
 // Chunks of all groups before group g (g <= G).
 __device__ __forceinline__ int chunks_before(const int32_t *off, int g, int G, int limit, int size) {
   int sum = 0;
   for (int base = 0; base < g; base += 4 * kWave) {
-    int n[4];
-    lane_chunks(off, G, limit, size, base, n);
+    const Round r = round_of(off, G, limit, size, base);
     const int g0 = base + 4 * static_cast<int>(threadIdx.x & 63);
 #pragma unroll
     for (int q = 0; q < 4; q++)
-      if (g0 + q < g) sum += n[q];
+      if (g0 + q < g) sum += r.n[q];
   }
   return __builtin_amdgcn_readlane(wave_inclusive_sum(sum), kWave - 1);
 }
 
 // Chunk `i` of the concatenated chunks of all groups; false if there are not that many.
 __device__ __forceinline__ bool find_chunk(const int32_t *off, int G, int limit, int size, int i, Chunk &c) {
-  int before = 0;
   for (int base = 0; base < G; base += 4 * kWave) {
-    int n[4];
-    lane_chunks(off, G, limit, size, base, n);
-    const int mine = n[0] + n[1] + n[2] + n[3];
-    const int incl = wave_inclusive_sum(mine);
-    const int sum = __builtin_amdgcn_readlane(incl, kWave - 1);
-    if (i < before + sum) {
-      const int local = i - before - (incl - mine);
-      const int src = __builtin_ctzll(__ballot(local >= 0 && local < mine));
-      int l = __builtin_amdgcn_readlane(local, src);
-      int g = base + 4 * src, total = 0;
-#pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const int nq = __builtin_amdgcn_readlane(n[q], src);
-        if (total == 0) {
-          if (l < nq) {
-            g = base + 4 * src + q;
-            total = nq;
-          } else {
-            l -= nq;
-          }
-        }
-      }
-      int lo = __builtin_amdgcn_readfirstlane(off[g]), hi = __builtin_amdgcn_readfirstlane(off[g + 1]);
-      clamp_pair(lo, hi, limit);
-      c.group = g;
-      c.lo = lo;
-      c.hi = hi;
-      c.index = l;
-      c.total = total;
+    const Round r = round_of(off, G, limit, size, base);
+    if (i < r.sum) {
+      c = pick(r, base, i);
       return true;
     }
-    before += sum;
+    i -= r.sum;
   }
   return false;
 }
 
-// Chunks of all groups.
-__device__ __forceinline__ int chunk_count(const int32_t *off, int G, int limit, int size) {
-  return chunks_before(off, G, G, limit, size);
+// The chunk that `index(total)` names, a number that depends on the number of all chunks (negative:
+// none); false if there is no such chunk.  Up to 256 groups' offsets are read once.
+template <class F>
+__device__ __forceinline__ bool find_chunk_of_all(const int32_t *off, int G, int limit, int size, F index, int &i, Chunk &c) {
+  const Round first = round_of(off, G, limit, size, 0);
+  int total = first.sum;
+  for (int base = 4 * kWave; base < G; base += 4 * kWave) total += round_of(off, G, limit, size, base).sum;
+  i = index(total);
+  if (i < 0) return false;
+  if (i < first.sum) {
+    c = pick(first, 0, i);
+    return true;
+  }
+  return find_chunk(off, G, limit, size, i, c);
 }
 
 // Most chunks that R rows in G groups can hold (host): a group's last chunk may be short.

@@ -179,3 +179,13 @@ def test_gradient_matches_differences():
             # the difference is off by h^2 of the third derivative (at most 6 max c) and by
             # binary64 rounding of the loss over h
             assert abs((f(up) - f(dn)) / (2 * h) - dl[t, e].item()) <= 12 * c.max() * (h * h + 200 * U32) + 1e-15 * f(z) / h
+
+
+@pytest.mark.parametrize("T, E, k, S", [(4096, 1024, 8, 4), (9000, 96, 4, 1), (8200, 40, 2, 70), (2050, 300, 8, 2)])
+def test_sizes_behind_every_variant(T, E, k, S):
+    """Tokens per wave and the shape of the second kernel follow T, E and S."""
+    rng = np.random.default_rng(T)
+    z, ids = _inputs(T, E, k, T)
+    cuts = np.sort(rng.integers(0, T + 1, S - 1))
+    mask = (rng.random(T) < 0.8).astype(np.uint8)
+    _check(z, ids, None if S == 1 else [0, *cuts, T], mask, routed=True)
