@@ -140,6 +140,10 @@ def _p(t):
     return None if t is None else C.c_void_p(t.data_ptr())
 
 
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -241,28 +245,32 @@ def _fp8_blocks(n: int) -> int:
     return -(-n // 128)
 
 
-def _dense(fn: str, **tensors):
-    """The library reads raw pointers: every tensor given has to be dense, of the named dtype and on
-    one device, and what is read 16 bytes at a time (codes and bf16 or f32 data) aligned to that."""
+def _dense(fn: str, *tensors):
+    """The library reads raw pointers: every (name, tensor, dtypes) given, None apart, has to be dense, of
+    one of the dtypes and on one device, and what is read 16 bytes at a time (codes and bf16 or f32
+    data) aligned to that."""
     device = None
-    for name, (t, dtypes) in tensors.items():
+    for name, t, dtypes in tensors:
         if t is None:
             continue
-        if t.dtype not in dtypes or not t.is_contiguous() or (device is not None and t.device != device) or (
-                dtypes in (_U8, _REAL, _BF16) and t.data_ptr() % 16):
+        at = t.get_device()
+        if device is None:
+            device = at
+        if t.dtype not in dtypes or at != device or not t.is_contiguous() or (dtypes in _WIDE and t.data_ptr() % 16):
             raise MoeError(fn, MOE_ERR_UNSUPPORTED, f"{name}: a dense, aligned tensor of {dtypes} on one device is needed, got "
                            f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-        device = t.device
 
 
 def _current(fn: str, t):
     """Kernels are launched on the current device: its tensors only."""
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    at = t.get_device()
+    if at < 0 or at != torch.cuda.current_device():
         raise MoeError(fn, MOE_ERR_UNSUPPORTED, f"tensors of the current device are needed, got {t.device}")
 
 
 _U8, _MASK, _I32, _F32 = (torch.uint8,), (torch.uint8, torch.bool), (torch.int32,), (torch.float32,)
 _BF16, _REAL = (torch.bfloat16,), (torch.bfloat16, torch.float32)
+_WIDE = (_U8, _BF16, _REAL)
 
 
 def _sized(fn: str, ok: bool, what: str):
@@ -272,24 +280,24 @@ def _sized(fn: str, ok: bool, what: str):
 
 def moe_quantize_fp8(x, q, sf, stream=None):
     """x [rows, C] bf16 or f32 -> q [rows, C] u8 E4M3 codes, sf [rows, ceil(C/128)] f32 scales."""
-    _dense("moe_quantize_fp8", x=(x, _REAL), q=(q, _U8), sf=(sf, _F32))
+    _dense("moe_quantize_fp8", ("x", x, _REAL), ("q", q, _U8), ("sf", sf, _F32))
     rows, cols = x.shape
     _sized("moe_quantize_fp8", q.numel() == rows * cols and sf.numel() == rows * _fp8_blocks(cols), "q or sf size")
     _current("moe_quantize_fp8", x)
-    _check("moe_quantize_fp8", lib().moe_quantize_fp8(_p(x), _DTYPES[x.dtype], rows, cols, _p(q), _p(sf), _stream(stream)))
+    _check("moe_quantize_fp8", lib().moe_quantize_fp8(_at(x), _DTYPES[x.dtype], rows, cols, _at(q), _at(sf), _stream(stream)))
 
 
 def moe_quantize_fp8_weights(w, q, sf, qt=None, sft=None, stream=None):
     """w [E, N, K] bf16 or f32 -> q, sf with one scale per 128 x 128 tile; qt [E, K, N] and sft
     receive the transposed copy."""
-    _dense("moe_quantize_fp8_weights", w=(w, _REAL), q=(q, _U8), sf=(sf, _F32), qt=(qt, _U8), sft=(sft, _F32))
+    _dense("moe_quantize_fp8_weights", ("w", w, _REAL), ("q", q, _U8), ("sf", sf, _F32), ("qt", qt, _U8), ("sft", sft, _F32))
     E, N, K = w.shape
     tiles = E * _fp8_blocks(N) * _fp8_blocks(K)
     _sized("moe_quantize_fp8_weights", all(t is None or t.numel() == n for t, n in (
         (q, w.numel()), (sf, tiles), (qt, w.numel()), (sft, tiles))), "an output's size")
     _current("moe_quantize_fp8_weights", w)
     _check("moe_quantize_fp8_weights", lib().moe_quantize_fp8_weights(
-        _p(w), _DTYPES[w.dtype], E, N, K, _p(q), _p(sf), _p(qt), _p(sft), _stream(stream)))
+        _at(w), _DTYPES[w.dtype], E, N, K, _at(q), _at(sf), _at(qt), _at(sft), _stream(stream)))
 
 
 def moe_fp8_token_blocks(R: int, E: int) -> int:
@@ -299,7 +307,7 @@ def moe_fp8_token_blocks(R: int, E: int) -> int:
 def moe_quantize_fp8_tokens(x, expert_offsets, R, q, sf, rows=None, stream=None):
     """x [rows_x, C] -> q [blocks, C, 128], sf [blocks, C]: blocks of 128 permuted rows of a group,
     one scale per column (blocks = moe_fp8_token_blocks(R, E))."""
-    _dense("moe_quantize_fp8_tokens", x=(x, _REAL), expert_offsets=(expert_offsets, _I32), q=(q, _U8), sf=(sf, _F32), rows=(rows, _I32))
+    _dense("moe_quantize_fp8_tokens", ("x", x, _REAL), ("expert_offsets", expert_offsets, _I32), ("q", q, _U8), ("sf", sf, _F32), ("rows", rows, _I32))
     rows_x, cols = x.shape
     E = expert_offsets.numel() - 1
     blocks = moe_fp8_token_blocks(R, E)
@@ -307,7 +315,7 @@ def moe_quantize_fp8_tokens(x, expert_offsets, R, q, sf, rows=None, stream=None)
            and (rows is None or rows.numel() >= R), "q, sf or rows size")
     _current("moe_quantize_fp8_tokens", x)
     _check("moe_quantize_fp8_tokens", lib().moe_quantize_fp8_tokens(
-        _p(x), _DTYPES[x.dtype], rows_x, _p(rows), _p(expert_offsets), E, int(R), cols, _p(q), _p(sf), _stream(stream)))
+        _at(x), _DTYPES[x.dtype], rows_x, _at(rows), _at(expert_offsets), E, int(R), cols, _at(q), _at(sf), _stream(stream)))
 
 
 def make_gemm_fp8_args(A, A_sf, B, B_sf, expert_offsets, R, epilogue, D=None, D_sf=None, A_rows=None) -> moe_gemm_fp8_args:
@@ -315,8 +323,8 @@ def make_gemm_fp8_args(A, A_sf, B, B_sf, expert_offsets, R, epilogue, D=None, D_
     D bf16 [R, N] (NONE), or u8 [R, N/2] with D_sf f32 [R, N/256] (SWIGLU_FP8).  The tensors must
     outlive the arguments' use."""
     fp8_act = epilogue == MOE_EPI_SWIGLU_FP8
-    _dense("make_gemm_fp8_args", A=(A, _U8), A_sf=(A_sf, _F32), B=(B, _U8), B_sf=(B_sf, _F32), expert_offsets=(expert_offsets, _I32),
-           D=(D, _U8 if fp8_act else _BF16), D_sf=(D_sf, _F32), A_rows=(A_rows, _I32))
+    _dense("make_gemm_fp8_args", ("A", A, _U8), ("A_sf", A_sf, _F32), ("B", B, _U8), ("B_sf", B_sf, _F32), ("expert_offsets", expert_offsets, _I32),
+           ("D", D, _U8 if fp8_act else _BF16), ("D_sf", D_sf, _F32), ("A_rows", A_rows, _I32))
     E, N, K = B.shape
     rows_A, R, kb = A.shape[0], int(R), _fp8_blocks(K)
     _sized("make_gemm_fp8_args", A.shape[1] == K and A_sf.numel() == rows_A * kb and B_sf.numel() == E * _fp8_blocks(N) * kb
@@ -340,7 +348,7 @@ def moe_grouped_gemm_fp8(args: moe_gemm_fp8_args, stream=None):
 def make_wgrad_fp8_args(Y, Y_sf, X, X_sf, expert_offsets, R, D) -> moe_wgrad_fp8_args:
     """Y [blocks, N, 128] / Y_sf and X [blocks, K, 128] / X_sf from moe_quantize_fp8_tokens over the
     same expert_offsets and R; D [E, N, K] f32 or bf16."""
-    _dense("make_wgrad_fp8_args", Y=(Y, _U8), Y_sf=(Y_sf, _F32), X=(X, _U8), X_sf=(X_sf, _F32), expert_offsets=(expert_offsets, _I32), D=(D, _REAL))
+    _dense("make_wgrad_fp8_args", ("Y", Y, _U8), ("Y_sf", Y_sf, _F32), ("X", X, _U8), ("X_sf", X_sf, _F32), ("expert_offsets", expert_offsets, _I32), ("D", D, _REAL))
     E, N, K = D.shape
     blocks = moe_fp8_token_blocks(R, E)
     _sized("make_wgrad_fp8_args", expert_offsets.numel() == E + 1 and Y.numel() >= blocks * N * 128
@@ -366,8 +374,8 @@ def moe_balance_loss_workspace(T: int, E: int, k: int, S: int) -> int:
 def moe_balance_loss(logits, topk_ids, counts, coef, loss, seq_offsets=None, token_mask=None, ws=None, stream=None):
     """logits [T, E] f32, topk_ids [T, k] i32, seq_offsets [S+1] i32 or None (S = 1), token_mask [T] u8
     or None -> counts [S, E] i32, coef [S, E] f32 (for the backward pass), loss [1] f32."""
-    _dense("moe_balance_loss", logits=(logits, _F32), topk_ids=(topk_ids, _I32), counts=(counts, _I32), coef=(coef, _F32), loss=(loss, _F32),
-           seq_offsets=(seq_offsets, _I32), token_mask=(token_mask, _MASK))
+    _dense("moe_balance_loss", ("logits", logits, _F32), ("topk_ids", topk_ids, _I32), ("counts", counts, _I32), ("coef", coef, _F32), ("loss", loss, _F32),
+           ("seq_offsets", seq_offsets, _I32), ("token_mask", token_mask, _MASK))
     (T, E), k = logits.shape, topk_ids.shape[1]
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
     _sized("moe_balance_loss", topk_ids.shape[0] == T and counts.numel() == S * E and coef.numel() == S * E
@@ -376,17 +384,17 @@ def moe_balance_loss(logits, topk_ids, counts, coef, loss, seq_offsets=None, tok
     if ws is None:
         ws = _ws(moe_balance_loss_workspace(T, E, k, S), logits.device)
     _check("moe_balance_loss", lib().moe_balance_loss(
-        _p(logits), _p(topk_ids), T, E, k, _p(seq_offsets), S, _p(token_mask), _p(counts), _p(coef), _p(loss),
-        _p(ws), ws.numel(), _stream(stream)))
+        _at(logits), _at(topk_ids), T, E, k, _at(seq_offsets), S, _at(token_mask), _at(counts), _at(coef), _at(loss),
+        _at(ws), ws.numel(), _stream(stream)))
 
 
 def moe_balance_loss_backward(logits, coef, grad_loss, dlogits, seq_offsets=None, token_mask=None,
                               topk_ids=None, topk_w=None, d_topk_w=None, stream=None):
     """dlogits [T, E] from grad_loss [1] and coef (moe_balance_loss); with topk_ids, topk_w and
     d_topk_w [T, k] the gradient of the routing weights is added in the same pass."""
-    _dense("moe_balance_loss_backward", logits=(logits, _F32), coef=(coef, _F32), grad_loss=(grad_loss, _F32), dlogits=(dlogits, _F32),
-           seq_offsets=(seq_offsets, _I32), token_mask=(token_mask, _MASK), topk_ids=(topk_ids, _I32), topk_w=(topk_w, _F32),
-           d_topk_w=(d_topk_w, _F32))
+    _dense("moe_balance_loss_backward", ("logits", logits, _F32), ("coef", coef, _F32), ("grad_loss", grad_loss, _F32), ("dlogits", dlogits, _F32),
+           ("seq_offsets", seq_offsets, _I32), ("token_mask", token_mask, _MASK), ("topk_ids", topk_ids, _I32), ("topk_w", topk_w, _F32),
+           ("d_topk_w", d_topk_w, _F32))
     T, E = logits.shape
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
     k = 1 if d_topk_w is None else d_topk_w.shape[1]
@@ -396,8 +404,8 @@ def moe_balance_loss_backward(logits, coef, grad_loss, dlogits, seq_offsets=None
            "operand sizes do not agree")
     _current("moe_balance_loss_backward", logits)
     _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
-        _p(logits), T, E, _p(seq_offsets), S, _p(token_mask), _p(coef), _p(grad_loss), _p(topk_ids), _p(topk_w),
-        _p(d_topk_w), k, _p(dlogits), _stream(stream)))
+        _at(logits), T, E, _at(seq_offsets), S, _at(token_mask), _at(coef), _at(grad_loss), _at(topk_ids), _at(topk_w),
+        _at(d_topk_w), k, _at(dlogits), _stream(stream)))
 
 
 # ---- allocating helpers ------------------------------------------------------------

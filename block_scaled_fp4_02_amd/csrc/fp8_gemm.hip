@@ -13,9 +13,11 @@
 // binary32 (measured on gfx950: the same for the 16x16x32 form).  That is 5e-5 of the result in
 // the 2-norm, a thirtieth of the rounding of D to bf16, for twice the rate of the fp16 matrix core.
 //
-// wgrad_kernel: D may be binary32, where that would show, so the codes become fp16 (exactly) and
-// the fp16 matrix core, whose products and sums are whole, takes them.  A launch of a few hundred
-// tokens per expert is bound by writing D all the same.
+// Where that would show, the codes become fp16 (exactly) and the fp16 matrix core, whose products
+// and sums are whole, takes them: in wgrad_kernel, whose D may be binary32, and in the SwiGLU
+// epilogue's smaller tiles, whose act is rounded again to E4M3 (a code next to a border falls the
+// other way for the least difference: 1.3 to 1.6 times the error of the down projection's result,
+// against 4 % of a decode batch's time; the large tile, at half its rate with fp16, keeps FP8).  
 //
 // Both products have the same inner form.  The "row" operand P (weight rows; columns k of x)
 // gives the MFMA's rows, of which a lane holds 4 consecutive ones, so results are contiguous
@@ -29,6 +31,8 @@
 #include "fp8_gemm.hpp"
 #include "fp8_round.hpp"
 #include "groups.hpp"
+
+#include <type_traits>
 
 #pragma clang fp contract(off)
 
@@ -227,7 +231,7 @@ __device__ __forceinline__ Half32 to_f16(const int8v &v) {
 
 // The whole contraction of one tile.  Scales of a stage: [0, BQ) of the Q rows, from kScaleP one
 // per half of P.
-template <class T, bool ONCE>
+template <class T, bool ONCE, bool WHOLE, int ACTIVE>
 __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps, float4v (&acc)[T::TP][T::TQ]) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x & 63, g = lane / 16, r = lane % 16;
@@ -246,12 +250,13 @@ __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps
     issue<T, ONCE>(src, lds0 + next * T::kStage, wave, kb + T::STAGES - 1, steps);
     const uint8_t *P = lds + slot * T::kStage, *Q = P + T::kBytesP;
     const float *S = reinterpret_cast<const float *>(Q + T::kBytesQ);
-    int8v q[T::TQ];
-    float sq[T::TQ];
+    std::conditional_t<WHOLE, Half32, int8v> q[ACTIVE];
+    float sq[ACTIVE];
 #pragma unroll
-    for (int j = 0; j < T::TQ; j++) {
+    for (int j = 0; j < ACTIVE; j++) {
       const int row = (wq * T::TQ + j) * 16 + r;
-      q[j] = fragment(Q, row, g);
+      if constexpr (WHOLE) q[j] = to_f16(fragment(Q, row, g));
+      else q[j] = fragment(Q, row, g);
       sq[j] = S[row];
     }
 #pragma unroll
@@ -259,13 +264,25 @@ __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps
       const int row0 = (i / T::kPerHalf) * kFp8Block + wp * (kFp8Block / T::WP) + (i % T::kPerHalf) * 16;
       const int8v p = fragment(P, row0 + r, g);
       const float sp = S[T::kScaleP + i / T::kPerHalf];
+      float4v v[ACTIVE];
+      if constexpr (WHOLE) {
+        const Half32 ph = to_f16(p);
 #pragma unroll
-      for (int j = 0; j < T::TQ; j++) {
-        const float4v t =
-            __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q[j], float4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+        for (int j = 0; j < ACTIVE; j++) v[j] = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 4; h++)
+#pragma unroll
+          for (int j = 0; j < ACTIVE; j++) v[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph.h[h], q[j].h[h], v[j], 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < ACTIVE; j++)
+          v[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q[j], float4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < ACTIVE; j++) {
         const float s = sp * sq[j];
 #pragma unroll
-        for (int c = 0; c < 4; c++) acc[i][j][c] = fmaf(t[c], s, acc[i][j][c]);
+        for (int c = 0; c < 4; c++) acc[i][j][c] = fmaf(v[j][c], s, acc[i][j][c]);
       }
     }
     slot = slot == T::STAGES - 1 ? 0 : slot + 1;
@@ -516,15 +533,26 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
   src.s = uniform(src.s);
 
   float4v acc[T::TP][T::TQ];
+  constexpr bool kWhole = MODE == kSwigluFp8;   // fp16 matrix core
   // the weights of a group of one chunk are read by this workgroup alone (measured at 32 rows per
   // expert, 805 MB of weights: 130 us past the caches, 138 us through them; with two chunks, whose
   // second one finds them in L2, 35 us against 24 us for 77 MB)
-  if (g.total == 1 && P.stream_weights) {
-    if constexpr (T::kLarge) contract_large<T, true>(src, lds, kb_n, count, acc);
-    else contract<T, true>(src, lds, kb_n, acc);
+  const bool once = g.total == 1 && P.stream_weights;
+  if constexpr (T::kLarge) {
+    if (once) contract_large<T, true>(src, lds, kb_n, count, acc);
+    else contract_large<T, false>(src, lds, kb_n, count, acc);
   } else {
-    if constexpr (T::kLarge) contract_large<T, false>(src, lds, kb_n, count, acc);
-    else contract<T, false>(src, lds, kb_n, acc);
+    // Q tiles behind the last row are left out
+    auto run = [&](auto active) {
+      constexpr int kActive = decltype(active)::value;
+      if (once) contract<T, true, kWhole, kActive>(src, lds, kb_n, acc);
+      else contract<T, false, kWhole, kActive>(src, lds, kb_n, acc);
+    };
+    const int active = T::WQ == 1 ? (count + 15) / 16 : T::TQ;
+    if (T::TQ >= 4 && active == 3) run(std::integral_constant<int, T::TQ >= 4 ? 3 : T::TQ>());
+    else if (T::TQ >= 4 && active == 2) run(std::integral_constant<int, T::TQ >= 4 ? 2 : T::TQ>());
+    else if (T::TQ >= 2 && active == 1) run(std::integral_constant<int, T::TQ >= 2 ? 1 : T::TQ>());
+    else run(std::integral_constant<int, T::TQ>());
   }
 
   const int wp = wave % T::WP, wq = wave / T::WP;
