@@ -146,8 +146,10 @@ def _at(t):
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return C.c_void_p(stream.cuda_stream)
+        # the handle of torch.cuda.current_stream() without the Python object around it (0.3 us
+        # instead of 3 us, a third of a small call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _ws(nbytes: int, device) -> torch.Tensor:
