@@ -13,6 +13,7 @@ MoE layer's buffers and sequences its six calls.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from dataclasses import dataclass
@@ -150,6 +151,14 @@ def _stream(stream):
         # instead of 3 us, a third of a small call)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
+
+
+_NO_STREAM = contextlib.nullcontext()
+
+
+def _allocating(stream):
+    """Allocations inside belong to `stream`, the one whose kernels use them (None: the current one)."""
+    return _NO_STREAM if stream is None else torch.cuda.stream(stream)
 
 
 def _ws(nbytes: int, device) -> torch.Tensor:
@@ -384,7 +393,8 @@ def moe_balance_loss(logits, topk_ids, counts, coef, loss, seq_offsets=None, tok
            and loss.numel() >= 1 and (token_mask is None or token_mask.numel() == T), "operand sizes do not agree")
     _current("moe_balance_loss", logits)
     if ws is None:
-        ws = _ws(moe_balance_loss_workspace(T, E, k, S), logits.device)
+        with _allocating(stream):
+            ws = _ws(moe_balance_loss_workspace(T, E, k, S), logits.device)
     _check("moe_balance_loss", lib().moe_balance_loss(
         _at(logits), _at(topk_ids), T, E, k, _at(seq_offsets), S, _at(token_mask), _at(counts), _at(coef), _at(loss),
         _at(ws), ws.numel(), _stream(stream)))
@@ -601,8 +611,9 @@ class FP8Tensor:
 
 def quantize_fp8_alloc(x: torch.Tensor, stream=None) -> FP8Tensor:
     rows, cols = x.shape
-    out = FP8Tensor(torch.empty(rows, cols, dtype=torch.uint8, device=x.device),
-                    torch.empty(rows, _fp8_blocks(cols), dtype=torch.float32, device=x.device))
+    with _allocating(stream):
+        out = FP8Tensor(torch.empty(rows, cols, dtype=torch.uint8, device=x.device),
+                        torch.empty(rows, _fp8_blocks(cols), dtype=torch.float32, device=x.device))
     moe_quantize_fp8(x, out.q, out.sf, stream)
     return out
 
@@ -612,19 +623,20 @@ def quantize_fp8_weights_alloc(w: torch.Tensor, transposed=False, stream=None):
     E, N, K = w.shape
     z = lambda a, b: FP8Tensor(torch.empty(E, a, b, dtype=torch.uint8, device=w.device),
                                torch.empty(E, _fp8_blocks(a), _fp8_blocks(b), dtype=torch.float32, device=w.device))
-    out = z(N, K)
+    with _allocating(stream):
+        out, t = z(N, K), z(K, N) if transposed else None
     if not transposed:
         moe_quantize_fp8_weights(w, out.q, out.sf, stream=stream)
         return out
-    t = z(K, N)
     moe_quantize_fp8_weights(w, out.q, out.sf, t.q, t.sf, stream)
     return out, t
 
 
 def quantize_fp8_tokens_alloc(x: torch.Tensor, expert_offsets, R, rows=None, stream=None) -> FP8Tensor:
     blocks = moe_fp8_token_blocks(R, expert_offsets.numel() - 1)
-    out = FP8Tensor(torch.empty(blocks, x.shape[1], 128, dtype=torch.uint8, device=x.device),
-                    torch.empty(blocks, x.shape[1], dtype=torch.float32, device=x.device))
+    with _allocating(stream):
+        out = FP8Tensor(torch.empty(blocks, x.shape[1], 128, dtype=torch.uint8, device=x.device),
+                        torch.empty(blocks, x.shape[1], dtype=torch.float32, device=x.device))
     moe_quantize_fp8_tokens(x, expert_offsets, R, out.q, out.sf, rows, stream)
     return out
 
@@ -632,13 +644,14 @@ def quantize_fp8_tokens_alloc(x: torch.Tensor, expert_offsets, R, rows=None, str
 def grouped_gemm_fp8_alloc(A: FP8Tensor, B: FP8Tensor, expert_offsets, R, epilogue=MOE_EPI_NONE, A_rows=None, stream=None):
     """D bf16 [R, N] (NONE) or the FP8Tensor act [R, N/2] (SWIGLU_FP8)."""
     N, R, dev = B.q.shape[1], int(R), A.q.device
-    if epilogue == MOE_EPI_SWIGLU_FP8:
-        out = FP8Tensor(torch.empty(R, N // 2, dtype=torch.uint8, device=dev),
-                        torch.empty(R, N // 256, dtype=torch.float32, device=dev))
-        D, D_sf = out.q, out.sf
-    else:
-        out = D = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
-        D_sf = None
+    with _allocating(stream):
+        if epilogue == MOE_EPI_SWIGLU_FP8:
+            out = FP8Tensor(torch.empty(R, N // 2, dtype=torch.uint8, device=dev),
+                            torch.empty(R, N // 256, dtype=torch.float32, device=dev))
+            D, D_sf = out.q, out.sf
+        else:
+            out = D = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
+            D_sf = None
     moe_grouped_gemm_fp8(make_gemm_fp8_args(A.q, A.sf, B.q, B.sf, expert_offsets, R, epilogue, D, D_sf, A_rows), stream)
     return out
 
@@ -646,7 +659,8 @@ def grouped_gemm_fp8_alloc(A: FP8Tensor, B: FP8Tensor, expert_offsets, R, epilog
 def grouped_wgrad_fp8_alloc(dY: FP8Tensor, X: FP8Tensor, expert_offsets, R, dtype=torch.float32, stream=None):
     """dW [E, N, K] from quantize_fp8_tokens_alloc of the output gradients and of the rows."""
     E, N, K = expert_offsets.numel() - 1, dY.q.shape[1], X.q.shape[1]
-    D = torch.empty(E, N, K, dtype=dtype, device=dY.q.device)
+    with _allocating(stream):
+        D = torch.empty(E, N, K, dtype=dtype, device=dY.q.device)
     moe_grouped_wgrad_fp8(make_wgrad_fp8_args(dY.q, dY.sf, X.q, X.sf, expert_offsets, R, D), stream)
     return D
 
@@ -654,9 +668,10 @@ def grouped_wgrad_fp8_alloc(dY: FP8Tensor, X: FP8Tensor, expert_offsets, R, dtyp
 def balance_loss_alloc(logits: torch.Tensor, topk_ids: torch.Tensor, seq_offsets=None, token_mask=None, stream=None):
     """(loss [1], counts [S, E], coef [S, E]); coef goes to moe_balance_loss_backward."""
     S, E = 1 if seq_offsets is None else seq_offsets.numel() - 1, logits.shape[1]
-    counts = torch.empty(S, E, dtype=torch.int32, device=logits.device)
-    coef = torch.empty(S, E, dtype=torch.float32, device=logits.device)
-    loss = torch.empty(1, dtype=torch.float32, device=logits.device)
+    with _allocating(stream):
+        counts = torch.empty(S, E, dtype=torch.int32, device=logits.device)
+        coef = torch.empty(S, E, dtype=torch.float32, device=logits.device)
+        loss = torch.empty(1, dtype=torch.float32, device=logits.device)
     moe_balance_loss(logits, topk_ids, counts, coef, loss, seq_offsets, token_mask, stream=stream)
     return loss, counts, coef
 

@@ -189,3 +189,19 @@ def test_sizes_behind_every_variant(T, E, k, S):
     cuts = np.sort(rng.integers(0, T + 1, S - 1))
     mask = (rng.random(T) < 0.8).astype(np.uint8)
     _check(z, ids, None if S == 1 else [0, *cuts, T], mask, routed=True)
+
+
+def test_bool_mask_and_views():
+    """A bool mask, and logits that start inside a buffer (4-byte alignment is enough)."""
+    z, ids = _inputs(50, 33, 3, 11)
+    mask = np.arange(50) % 4 != 1
+    want = _run(z, ids, None, mask.astype(np.uint8), 1.0, False)
+    buf = torch.empty(50 * 33 + 1, device="cuda")
+    buf[1:] = dev(z).flatten()
+    logits = buf[1:].view(50, 33)
+    assert logits.data_ptr() % 16 == 4
+    loss, counts, coef = moe.balance_loss_alloc(logits, dev(ids), token_mask=dev(mask))
+    dl = torch.empty_like(logits)
+    moe.moe_balance_loss_backward(logits, coef, torch.ones(1, device="cuda"), dl, token_mask=dev(mask))
+    for a, b in zip((loss, counts, coef, dl), want):
+        assert torch.equal(a.view(torch.int32), b.view(torch.int32))

@@ -145,6 +145,39 @@ def test_work_on_another_stream():
     torch.cuda.synchronize()
 
 
+def test_stream_argument():
+    """The allocating helpers given a stream: what they allocate belongs to that stream, so memory that
+    the current stream's queued work still holds is not written."""
+    a = _training_inputs(6)
+    want, _ = _training_step(**a)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        junk = [torch.randn(1 << 20, device="cuda") for _ in range(8)]
+        held = [(j * 2).sum() for j in junk]
+        del junk
+        W = moe.quantize_fp8_weights_alloc(a["w"], stream=side)
+        y = moe.grouped_gemm_fp8_alloc(moe.quantize_fp8_alloc(a["x"], side), W, a["off"], a["R"], A_rows=a["src"], stream=side)
+        loss, counts, coef = moe.balance_loss_alloc(a["logits"], a["ids"], stream=side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(y.view(torch.int16), want["y"].view(torch.int16))
+        assert torch.equal(loss, want["loss"]) and torch.equal(counts, want["counts"])
+        del held
+
+
+def test_token_gradient_is_finalize_with_unit_weights():
+    """A token's rows of dx, summed by moe_finalize with weights of one."""
+    a = _training_inputs(9)
+    T, k, H = a["x"].shape[0], 2, a["x"].shape[1]
+    *_, tsr = moe.route_permute_alloc(a["logits"], k)
+    dx = _training_step(**a)[0]["dx"]
+    out = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    moe.moe_finalize(dx, torch.ones(T, k, device="cuda"), tsr, out)
+    rows = dx.double()[tsr.view(T, k).long()]
+    assert ((out.double() - rows.sum(1)).abs() <= U16 * rows.sum(1).abs() + 2 * k * U32 * rows.abs().sum(1)).all()
+
+
 def test_two_streams_at_once():
     """Two independent steps on two streams do not touch each other (each has its own workspace)."""
     ins = [_training_inputs(s, T=400) for s in (7, 8)]
