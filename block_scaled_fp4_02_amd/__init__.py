@@ -9,7 +9,10 @@ import of any entry point fails loudly.
 Functions with the C names take caller-allocated tensors exactly like the C calls.  The
 ``*_alloc`` helpers allocate outputs and workspaces with torch; :func:`pack_weights` turns
 an NVFP4 weight tensor into the packed layout once; :class:`MoELayerPlan` pre-allocates one
-MoE layer's buffers and sequences its six calls.
+MoE layer's buffers and sequences its six calls.  The FP8 operators (:func:`moe_quantize_fp8` and its
+kin, :func:`moe_grouped_gemm_fp8`, :func:`moe_grouped_wgrad_fp8`, :class:`MoEFP8LayerPlan`) and the
+router's balance loss (:func:`moe_balance_loss`) check their tensors (dtype, strides, sizes,
+device) before they pass the pointers on.
 """
 from __future__ import annotations
 

@@ -13,6 +13,8 @@
  *   5. moe_grouped_gemm_nvfp4 (MOE_EPI_NONE)  down GEMM into a bf16 workspace;
  *   6. moe_finalize        router-weighted gather-reduce of each token's k rows
  *                          into the bf16 output.
+ * The same layer with FP8 experts, their training step and the router's balance
+ * term are sections 5 to 8.
  *
  * Sources (web pages cited by title and section):
  *  - Operands are FP4 E2M1 with one FP8 scale per 16 elements along the
