@@ -474,13 +474,9 @@ __device__ __forceinline__ int64_t row_of_a(const GemmParams &P, int p) {
   return a < 0 ? 0 : (a >= P.rows_A ? P.rows_A - 1 : a);
 }
 
+// One tile: up to BQ rows from `first` of group g, n tile `nt`.
 template <class T, Mode MODE>
-__global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) {
-  __shared__ __align__(1024) uint8_t lds[T::kLds];
-  groups::Chunk g;
-  int chunk, nt;
-  if (!find_item(P, T::BQ, g, chunk, nt)) return;
-  const int first = g.lo + chunk * T::BQ, count = min(T::BQ, g.hi - first);
+__device__ __forceinline__ void gemm_tile(const GemmParams &P, uint8_t *lds, const groups::Chunk &g, int first, int count, int nt) {
   const int half_n = P.N / 2;                       // SWIGLU: gate rows, then up rows
   const int n0 = nt * (MODE == kSwigluFp8 ? kFp8Block : T::BP);
 
@@ -627,17 +623,33 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
   }
 }
 
+template <class T, Mode MODE, int TILES>
+__global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) {
+  __shared__ __align__(1024) uint8_t lds[T::kLds];
+  groups::Chunk g;
+  int chunk, nt;
+  if (!find_item(P, T::BQ, g, chunk, nt)) return;
+  const int first = g.lo + chunk * T::BQ, count = min(T::BQ, g.hi - first);
+  gemm_tile<T, MODE>(P, lds, g, first, count, TILES * nt);
+#pragma unroll 1
+  for (int i = 1; i < TILES; i++) {
+    if ((TILES * nt + i) * T::BP >= P.N) return;
+    __syncthreads();   // the tile before is out of LDS
+    gemm_tile<T, MODE>(P, lds, g, first, count, TILES * nt + i);
+  }
+}
+
 // ---- few items ------------------------------------------------------------------------------
 //
 // When 128-column tiles are fewer than the CUs (a single token: k experts' weights, each a few
 // hundred rows), the contraction is dealt to the eight waves of a workgroup: wave w takes the
-// scale blocks w, w + 8, ... of a tile of 32 columns and 16 rows, with a ring of its own and no
-// barrier before the end, and the eight partial tiles are added in order through LDS.  Bound by
+// scale blocks w, w + 8, ... of a tile of 32 columns (16 where tiles are very few: 7.9 us against 8.4
+// for the token below) and 16 rows, with a ring of its own and no barrier before the end, and the eight partial tiles are added in order through LDS.  Bound by
 // latency: the item lookup, about two round trips to HBM and the sum.  One token, eight experts of
-// 512 x 6144: 9.7 us (28 us in 64 x 128 tiles).
-template <int Q_, int WAVES_, int STAGES_>
+// 512 x 6144: 7.9 us (28 us in 64 x 128 tiles).
+template <int Q_, int P_, int WAVES_, int STAGES_>
 struct Split {
-  static constexpr int Q = Q_, P = 32, WAVES = WAVES_, STAGES = STAGES_;
+  static constexpr int Q = Q_, P = P_, WAVES = WAVES_, STAGES = STAGES_;
   static constexpr int TQ = Q / 16, TP = P / 16;
   static constexpr int kCopies = (P + Q) / 8 + 2;
   static constexpr int kStage = (P + Q) * kFp8Block + 2 * kWave * 4;
@@ -894,13 +906,15 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
   }
 }
 
-template <class T, Mode MODE>
+// TILES: n tiles that a workgroup does one after the other.
+template <class T, Mode MODE, int TILES = 1>
 hipError_t run_gemm(GemmParams p, hipStream_t stream) {
-  p.n_tiles = MODE == kSwigluFp8 ? p.N / 2 / kFp8Block : (p.N + T::BP - 1) / T::BP;
+  static_assert(MODE != kSwigluFp8 || TILES == 1, "an n tile is 128 columns of act");
+  p.n_tiles = MODE == kSwigluFp8 ? p.N / 2 / kFp8Block : (p.N + TILES * T::BP - 1) / (TILES * T::BP);
   const int64_t items = groups::max_chunks(p.R, p.E, T::BQ) * p.n_tiles;
   const int64_t grid = (items + kXcds - 1) / kXcds * kXcds;
   if (grid > 0)
-    hipLaunchKernelGGL((gemm_kernel<T, MODE>), dim3(static_cast<uint32_t>(grid)), dim3(T::kThreadsT), 0, stream, p);
+    hipLaunchKernelGGL((gemm_kernel<T, MODE, TILES>), dim3(static_cast<uint32_t>(grid)), dim3(T::kThreadsT), 0, stream, p);
   return hipGetLastError();
 }
 
@@ -943,11 +957,15 @@ hipError_t launch_gemm(GemmParams p, bool swiglu, hipStream_t stream) {
   }
   if (large) return run_gemm<Large, kNone>(p, stream);
   if (tiles(64, 128) < kManyTiles && p.K >= 4 * kFp8Block) {
-    if (mean <= 16) return run_split<Split<16, 8, 3>>(p, stream);
-    if (mean <= 32) return run_split<Split<32, 8, 2>>(p, stream);
-    return run_split<Split<64, 4, 3>>(p, stream);
+    if (mean > 32) return run_split<Split<64, 32, 4, 3>>(p, stream);
+    if (mean > 16) return run_split<Split<32, 32, 8, 2>>(p, stream);
+    if (tiles(16, 32) >= kManyTiles) return run_split<Split<16, 32, 8, 3>>(p, stream);
+    return run_split<Split<16, 16, 8, 3>>(p, stream);
   }
   if (mean > 2 * kLargeRows && tiles(128, 128) >= kManyTiles) return run_gemm<Tile<128, 128, 2, 2, 2>, kNone>(p, stream);
+  // two steps a tile: looking the item up takes as long (256 experts of 32 rows, N 6144, K 256: 119 us, one
+  // tile a workgroup 136; with K 512 no difference)
+  if (p.K <= 2 * kFp8Block && tiles(64, 512) >= 4 * kManyTiles) return run_gemm<Tile<64, 128, 1, 4, 2>, kNone, 4>(p, stream);
   if (p.K <= 4 * kFp8Block) return run_gemm<Tile<64, 128, 1, 4, 2>, kNone>(p, stream);
   return run_gemm<Tile<64, 128, 1, 4, 3>, kNone>(p, stream);
 }
