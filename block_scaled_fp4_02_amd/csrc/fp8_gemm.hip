@@ -17,7 +17,7 @@
 // and sums are whole, takes them: in wgrad_kernel, whose D may be binary32, and in the SwiGLU
 // epilogue's smaller tiles, whose act is rounded again to E4M3 (a code next to a border falls the
 // other way for the least difference: 1.3 to 1.6 times the error of the down projection's result,
-// against 4 % of a decode batch's time; the large tile, at half its rate with fp16, keeps FP8).  
+// against 4 % of a decode batch's time; the large tile, at half its rate with fp16, keeps FP8).
 //
 // Both products have the same inner form.  The "row" operand P (weight rows; columns k of x)
 // gives the MFMA's rows, of which a lane holds 4 consecutive ones, so results are contiguous
@@ -306,7 +306,11 @@ __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps
 // step.  The last group of a row that has no whole number of groups starts at its fourth scale
 // from the end (a large tile has at least four steps).
 //
-// Measured, one group of 8192 rows, N = K = 8192 (1.1 TFLOP): 480 us, 2.3 PFLOP/s (128 x 128 tiles: 680 us); the same data of zeros 420 us: the card lowers its clock under this load, and a loop of these MFMAs and fmas alone runs at 3.4 PFLOP/s on random data, 4.5 on constants.
+// Measured, one group of 8192 rows, N = K = 8192 (1.1 TFLOP): 480 us, 2.3 PFLOP/s (128 x 128 tiles
+// 680 us).  What bounds it: the matrix cores are busy for half of the cycles at a clock that this
+// load holds near 2.0 GHz (the same launch on zeros takes 420 us; a loop of these MFMAs and fmas
+// alone runs at 3.5 PFLOP/s on random data, 4.5 on constants); writing D costs 25 us, the copies
+// from L2 some 30.
 constexpr int kLag = 4;   // an MFMA's result is read that many MFMAs later (3: the same within 1 %; 2: 3 % slower)
 
 template <class T, bool ONCE>
@@ -644,9 +648,10 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
 // When 128-column tiles are fewer than the CUs (a single token: k experts' weights, each a few
 // hundred rows), the contraction is dealt to the eight waves of a workgroup: wave w takes the
 // scale blocks w, w + 8, ... of a tile of 32 columns (16 where tiles are very few: 7.9 us against 8.4
-// for the token below) and 16 rows, with a ring of its own and no barrier before the end, and the eight partial tiles are added in order through LDS.  Bound by
-// latency: the item lookup, about two round trips to HBM and the sum.  One token, eight experts of
-// 512 x 6144: 7.9 us (28 us in 64 x 128 tiles).
+// for the token below) and 16 rows, with a ring of its own and no barrier before the end, and the
+// eight partial tiles are added in order through LDS.  Bound by latency: the item lookup, about two
+// round trips to HBM and the sum.  One token, eight experts of 512 x 6144: 7.9 us (28 us in 64 x 128
+// tiles).
 template <int Q_, int P_, int WAVES_, int STAGES_>
 struct Split {
   static constexpr int Q = Q_, P = P_, WAVES = WAVES_, STAGES = STAGES_;
@@ -929,7 +934,12 @@ hipError_t run_split(GemmParams p, hipStream_t stream) {
 
 using Large = Tile<256, 256, 4, 2, 2>;
 constexpr int64_t kCacheBytes = 256 << 20;   // MI355X's memory-side cache
-constexpr int kManyTiles = 192;              // three quarters of the CUs
+// Fewer tiles leave CUs without one.  One group, N = K = 4096: of 1024 rows, 64 large tiles 55 us, 512
+// 64-row tiles 31; of 2048, 128 large tiles 59 us, 256 128-row tiles 46; of 64 rows, 32 64-row tiles
+// 23 us, the contraction split over waves 11.
+constexpr int kManyTiles = 192;
+// Rows per expert above which 64-row tiles read weights twice too often.  32 experts, N 4096, K 6144: of
+// 32 rows, 64-row tiles 136 us, large ones 140; of 50 rows 161 and 146; of 64 rows 215 and 149.
 constexpr int kLargeRows = 44;
 
 template <class T, Mode MODE>
