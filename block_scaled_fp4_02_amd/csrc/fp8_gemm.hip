@@ -767,13 +767,13 @@ __global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams
 // ---- the weight gradient -----------------------------------------------------------------------
 //
 // A tile of D has a few steps (one per 128 tokens of its expert).  Measured, 16 experts of 512 rows, N
-// 4096, K 6144, binary32 D (412 GFLOP, 1.6 GB written): 605 us; 64 rows each: 284 us, 5.7 TB/s
+// 4096, K 6144, binary32 D (412 GFLOP, 1.6 GB written): 600 us; 64 rows each: 300 us, 5.4 TB/s
 // written.  Per step and wave 64 MFMAs (1024 cycles) stand against 128 conversions and 128
 // scalings (1024), which the MFMAs hide in part only.  One pipeline through several tiles, the
 // next one's first stage copied during the last step: 620 to 710 us.
 struct GradTile {
   Buf p, q, s;     // this wave's stages: X codes, Y codes, scales of one of them
-  int steps;       // token blocks
+  int steps, last; // token blocks, tokens of the last one
   int e, n0, k0;
 };
 
@@ -791,6 +791,7 @@ __device__ __forceinline__ bool grad_tile(const WgradParams &P, int wave, GradTi
   int lo = __builtin_amdgcn_readfirstlane(P.offsets[t.e]), hi = __builtin_amdgcn_readfirstlane(P.offsets[t.e + 1]);
   groups::clamp_pair(lo, hi, P.R);
   t.steps = (hi - lo + kFp8Block - 1) / kFp8Block;
+  t.last = hi - lo - (t.steps - 1) * kFp8Block;
   t.steps = max(0, min(t.steps, P.blocks - b0));   // offsets that are not monotone stay inside the buffers
   const bool of_q = wave * kWave < T::BQ;
   const uint32_t rows_p = min(T::BP, P.K - t.k0), rows_q = min(T::BQ, P.N - t.n0);
@@ -852,7 +853,13 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
 #pragma unroll
     for (int j = 0; j < T::TQ; j++) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
   issue_stage(0);
-  for (int kb = 0; kb < t.steps; kb++) {
+  // One token block.  kPieces 2: the block has up to 64 tokens (pieces 0 and 1 of a lane's 32 bytes are
+  // the block's first 64), so half its MFMAs and conversions would work on padding.  Measured, 16
+  // experts of about 512 rows, N 4096, K 6144: 616 -> 600 us, 175 rows: 385 -> 369, 2048 rows (bf16 D):
+  // 1694 -> 1659; 64 experts of 128 rows, N 1024, K 4096: 238 -> 226; 16 of 64 rows, where writing D
+  // is the bound: 294 -> 300.
+  auto step = [&](int kb, auto pieces) {
+    constexpr int kPieces = decltype(pieces)::value;
     arrive<0>();
     issue_stage(kb + 1);
     const uint8_t *Ps = lds + (kb & 1) * T::kStage, *Qs = Ps + T::kBytesP;
@@ -875,7 +882,7 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
       for (int j = 0; j < T::TQ; j++) v[j] = float4v{0.f, 0.f, 0.f, 0.f};
       // piece by piece over all columns: neighbouring MFMAs do not wait for each other
 #pragma unroll
-      for (int h = 0; h < 4; h++)
+      for (int h = 0; h < kPieces; h++)
 #pragma unroll
         for (int j = 0; j < T::TQ; j++) v[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(p.h[h], q[j].h[h], v[j], 0, 0, 0);
 #pragma unroll
@@ -883,6 +890,11 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
 #pragma unroll
         for (int c = 0; c < 4; c++) acc[i][j][c] = fmaf(v[j][c], sp[c] * sq[j], acc[i][j][c]);
     }
+  };
+  for (int kb = 0; kb + 1 < t.steps; kb++) step(kb, std::integral_constant<int, 4>());
+  if (t.steps > 0) {
+    if (t.last <= kFp8Block / 2) step(t.steps - 1, std::integral_constant<int, 2>());
+    else step(t.steps - 1, std::integral_constant<int, 4>());
   }
   arrive<0>();   // the copies past the end (zeros) are in before the buffers serve anything else
   // each wave turns 16 rows of its tile at a time in LDS and stores whole pieces of them (16 rows

@@ -248,6 +248,21 @@ def test_weight_gradient(groups, N, K, dtype):
     _near(D.float().cpu().numpy(), want, half * np.abs(want) + (1 + half) * ref.sum_error(max(sizes)) * mag, groups)
 
 
+def test_weight_gradient_of_half_blocks():
+    """Groups whose last token block is up to half full, just over and full."""
+    rng = np.random.default_rng(12)
+    N, K, sizes = 144, 272, [1, 63, 64, 65, 127, 128, 129, 191, 192, 193, 0, 256]
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    R = int(off[-1])
+    o = dev(off)
+    Y, X = (moe.quantize_fp8_tokens_alloc(torch.from_numpy(rng.standard_normal((R, C)).astype(np.float32)).cuda(), o, R) for C in (N, K))
+    D = moe.grouped_wgrad_fp8_alloc(Y, X, o, R)
+    n = sum(-(-s // 128) for s in sizes)
+    yv, xv = (ref.tokens_value(t.q[:n].cpu().numpy(), t.sf[:n].cpu().numpy()) for t in (Y, X))
+    want, mag = ref.wgrad(yv, xv, off)
+    _near(D.float().cpu().numpy(), want, U32 * np.abs(want) + (1 + U32) * ref.sum_error(max(sizes)) * mag, "half blocks")
+
+
 def test_input_gradient_is_the_transposed_product():
     rng = np.random.default_rng(11)
     N, K, sizes = 272, 144, [50, 0, 7, 140]
