@@ -303,7 +303,8 @@ moe_status moe_finalize(const uint16_t *Y, int64_t R, const float *topk_w,
  *     moe_fp8_token_blocks(R, E) is the most there can be; blocks past the last one in use
  *     are not written.
  * Limits: rows, R >= 0; C, N, K multiples of 16 (of x in 5a and 5c: C >= 16) up to 2^20;
- * 1 <= E <= 1024; R < 2^31; fewer than 2^31 blocks.
+ * 1 <= E <= 1024; R <= 2^30; fewer than 2^28 blocks of rows, and 2^24 - 8 tiles or blocks of 128 rows
+ * by 128 columns.
  * ------------------------------------------------------------------------- */
 moe_status moe_quantize_fp8(const void *x, int x_dtype, int64_t rows, int64_t C, uint8_t *q, float *sf,
                             hipStream_t stream);
@@ -332,7 +333,7 @@ moe_status moe_quantize_fp8_tokens(const void *x, int x_dtype, int64_t rows_x, c
  * dY[p, n] W[e, n, k], is the same product: A = dY quantised by 5a, B = qt, B_sf = sft of
  * 5b, with N and K exchanged (moe_finalize with unit weights sums a token's rows).
  * Supported: N % 16 == 0, K % 16 == 0, N, K <= 2^20, N * K <= 2^31 - 4096, 1 <= E <= 1024,
- * 0 <= R < 2^31; SWIGLU_FP8: N % 256 == 0; with A_rows: rows_A * K <= 2^31 - 4096;
+ * (R / 64 + E) * ceil(N / 128) < 2^24 - 8; SWIGLU_FP8: N % 256 == 0; with A_rows: rows_A * K <= 2^31 - 4096;
  * MOE_ERR_UNSUPPORTED otherwise.  Without A_rows, rows_A >= R.  No workspace: every
  * workgroup derives its work item from the offsets.
  * moe_grouped_gemm_fp8_can_implement() returns MOE_OK exactly when the launch is supported.
@@ -364,7 +365,8 @@ moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args *args, hipStream_t strea
  *   D[e, n, k] = sum_b sY[b, n] sX[b, k] sum_{t<128} y[b, n, t] x[b, k, t]
  * over the blocks b of group e; products are exact and all sums binary32.  D [E, N, K] in D_dtype
  * (MOE_DTYPE_F32, or MOE_DTYPE_BF16: rounded once); every element is written, zeros for an
- * expert without rows.  Limits: as section 6.
+ * expert without rows.  Limits: N, K and E as in section 6, R <= 2^30, E * ceil(N / 128) *
+ * ceil(K / 128) < 2^24 - 8.
  * ------------------------------------------------------------------------- */
 typedef struct moe_wgrad_fp8_args {
   const uint8_t *Y;               /* [blocks, N, 128] */
@@ -405,9 +407,9 @@ moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args *args, hipStream_t str
  * gradient of the routing weights topk_w of section 1 in the same pass:
  *   dlogits[t, topk_ids[t, j]] += topk_w[t, j] (d_topk_w[t, j] - sum_i topk_w[t, i] d_topk_w[t, i])
  * A masked token's row is 0.  Rows of dlogits outside every sequence are not written.
- * Limits: T >= 0, 1 <= E <= 1024, 1 <= k <= min(E, 32), 1 <= S <= 65536, T*k < 2^31;
+ * Limits: 0 <= T <= 2^26, 1 <= E <= 1024, 1 <= k <= min(E, 32), 1 <= S <= 65536, T*k < 2^31;
  * seq_offsets NULL with S != 1 is MOE_ERR_NULL.  ws: moe_balance_loss_workspace(T, E, k, S)
- * bytes (contents on entry irrelevant; calls that may overlap need one each).
+ * bytes, 16-byte aligned (contents on entry irrelevant; calls that may overlap need one each).
  * ------------------------------------------------------------------------- */
 size_t moe_balance_loss_workspace(int T, int E, int k, int S);
 moe_status moe_balance_loss(const float *logits, const int32_t *topk_ids, int T, int E, int k,

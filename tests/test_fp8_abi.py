@@ -131,6 +131,35 @@ def test_balance_backward_refusals(kw, want):
                                                a["w"], a["dw"], a["k"], a["dlogits"], None) == want
 
 
+def test_most_rows():
+    """Row numbers and the rows past a tile's end stay in 31 bits, and a launch has fewer than 2^32
+    threads: more rows are refused before the launch."""
+    L = moe.lib()
+    for R, want in ((1 << 30, OK), ((1 << 30) + 1, UNSUPPORTED), ((1 << 31) - 1, UNSUPPORTED)):
+        w = moe.moe_wgrad_fp8_args()
+        for f, x in dict(Y=FAKE, Y_sf=FAKE, X=FAKE, X_sf=FAKE, expert_offsets=FAKE, E=3, N=48, K=80, D_dtype=1, R=R, D=FAKE).items():
+            setattr(w, f, x)
+        assert L.moe_grouped_wgrad_fp8_can_implement(C.byref(w)) == want
+        # (a null pointer stands for a call that would be launched)
+        assert L.moe_quantize_fp8_tokens(None, 0, R, None, FAKE, 2, R, 16, FAKE, FAKE, None) == (want or NULL)
+    for R, N, want in (((1 << 30) - 2048, 16, OK), (1 << 30, 16, UNSUPPORTED), ((1 << 24) - 2048, 8192, OK), (1 << 24, 8192, UNSUPPORTED)):
+        g = gemm_args(R=R, rows_A=1 << 31, N=N, K=16)
+        assert L.moe_grouped_gemm_fp8_can_implement(C.byref(g)) == want
+    for rows, C_, want in (((1 << 28) - 1, 16, NULL), (1 << 28, 16, UNSUPPORTED), (1 << 24, 2048, UNSUPPORTED)):
+        assert L.moe_quantize_fp8(None, 0, rows, C_, FAKE, FAKE, None) == want
+    for T, want in ((1 << 26, NULL), ((1 << 26) + 1, SHAPE)):
+        assert (L.moe_balance_loss_workspace(T, 4, 1, 1) != 0) == (want == NULL)
+        assert L.moe_balance_loss_backward(None, T, 4, None, 1, None, FAKE, FAKE, None, None, None, 1, FAKE, None) == want
+
+
+def test_balance_workspace_alignment():
+    """The workspace holds binary64 partial sums behind its first 16 bytes."""
+    L = moe.lib()
+    need = L.moe_balance_loss_workspace(100, 4, 2, 3)
+    call = lambda ws: L.moe_balance_loss(FAKE, FAKE, 100, 4, 2, FAKE, 3, None, FAKE, FAKE, FAKE, C.c_void_p(ws), need, None)
+    assert call(0x1004) == call(0x1008) == WS
+
+
 def test_binding_refuses_what_kernels_cannot_read():
     """Wrong dtypes, strides, sizes, unaligned views and host tensors are refused before any launch."""
     bf, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
