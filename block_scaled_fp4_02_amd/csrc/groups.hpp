@@ -1,8 +1,9 @@
 // Groups of consecutive rows given by offsets on the device (expert groups, sequences), cut
 // into chunks: which group and rows does chunk number `i` hold?  Every wave works it out for
 // itself, 256 groups per round (four per lane, their offsets loaded together), and the result
-// is uniform over the wave.  Offsets are clamped to [0, limit] and made monotone pairwise, so
-// bad values give wrong groups but never a row outside [0, limit).
+// is uniform over the wave.  Offsets are clamped to [0, limit] and made monotone pairwise, and
+// numbers of chunks stop at 2^30, more than monotone offsets can give, so bad values give wrong
+// groups but never a row outside [0, limit).
 #pragma once
 
 #include "common.hpp"
@@ -23,6 +24,22 @@ __device__ __forceinline__ int wave_inclusive_sum(int v) {
   for (int o = 1; o < kWave; o <<= 1) {
     const int u = __shfl_up(v, o, kWave);
     if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// The sum of two numbers of chunks, each up to 2^30.
+constexpr uint32_t kMostChunks = 1u << 30;
+__device__ __forceinline__ int plus(int a, int b) {
+  return static_cast<int>(min(static_cast<uint32_t>(a) + static_cast<uint32_t>(b), kMostChunks));
+}
+
+__device__ __forceinline__ int wave_inclusive_chunks(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int u = __shfl_up(v, o, kWave);
+    if (lane >= o) v = plus(v, u);
   }
   return v;
 }
@@ -52,14 +69,15 @@ __device__ __forceinline__ Round round_of(const int32_t *off, int G, int limit, 
     r.hi[q] = o[q + 1];
     clamp_pair(r.lo[q], r.hi[q], limit);
     r.n[q] = g0 + q < G ? (r.hi[q] - r.lo[q] + size - 1) / size : 0;
-    r.mine += r.n[q];
+    r.mine = plus(r.mine, r.n[q]);
   }
-  r.incl = wave_inclusive_sum(r.mine);
+  r.incl = wave_inclusive_chunks(r.mine);
   r.sum = __builtin_amdgcn_readlane(r.incl, kWave - 1);
   return r;
 }
 
-// Chunk `i` of a round's (i < r.sum), read out of the lane that has it.
+// Chunk `i` of a round's (i < r.sum), read out of the lane that has it (the first one, where sums stopped
+// at 2^30; its index is one of the lane's chunks all the same).
 __device__ __forceinline__ Chunk pick(const Round &r, int base, int i) {
   const int local = i - (r.incl - r.mine);
   const int src = __builtin_ctzll(__ballot(local >= 0 && local < r.mine));
@@ -90,9 +108,9 @@ __device__ __forceinline__ int chunks_before(const int32_t *off, int g, int G, i
     const int g0 = base + 4 * static_cast<int>(threadIdx.x & 63);
 #pragma unroll
     for (int q = 0; q < 4; q++)
-      if (g0 + q < g) sum += r.n[q];
+      if (g0 + q < g) sum = plus(sum, r.n[q]);
   }
-  return __builtin_amdgcn_readlane(wave_inclusive_sum(sum), kWave - 1);
+  return __builtin_amdgcn_readlane(wave_inclusive_chunks(sum), kWave - 1);
 }
 
 // Chunk `i` of the concatenated chunks of all groups; false if there are not that many.
@@ -114,7 +132,7 @@ template <class F>
 __device__ __forceinline__ bool find_chunk_of_all(const int32_t *off, int G, int limit, int size, F index, int &i, Chunk &c) {
   const Round first = round_of(off, G, limit, size, 0);
   int total = first.sum;
-  for (int base = 4 * kWave; base < G; base += 4 * kWave) total += round_of(off, G, limit, size, base).sum;
+  for (int base = 4 * kWave; base < G; base += 4 * kWave) total = plus(total, round_of(off, G, limit, size, base).sum);
   i = index(total);
   if (i < 0) return false;
   if (i < first.sum) {

@@ -205,3 +205,22 @@ def test_bool_mask_and_views():
     moe.moe_balance_loss_backward(logits, coef, torch.ones(1, device="cuda"), dl, token_mask=dev(mask))
     for a, b in zip((loss, counts, coef, dl), want):
         assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+
+
+def test_offsets_that_are_not_monotone_stay_in_range():
+    """2^16 sequences that claim all tokens in turn: 2^31 chunks and more, past what 32 bits hold.  The
+    values mean nothing, rows in front of and behind the tensors stay."""
+    T, E, S = 1 << 19, 1, 1 << 16
+    off = torch.zeros(S + 1, dtype=torch.int32, device="cuda")
+    off[1::2] = T
+    pad = 1 << 12
+    buf = torch.full((T + 2 * pad,), 7.0, device="cuda")
+    dl = buf[pad:pad + T].view(T, E)
+    z = torch.zeros(T, E, device="cuda")
+    loss, counts, coef = moe.balance_loss_alloc(z, torch.zeros(T, 1, dtype=torch.int32, device="cuda"), off)
+    moe.moe_balance_loss_backward(z, coef, torch.ones(1, device="cuda"), dl, off)
+    assert (buf[:pad] == 7).all() and (buf[pad + T:] == 7).all()
+    # and the same call with good offsets afterwards
+    good = torch.linspace(0, T, S + 1, device="cuda").round().int()
+    loss, counts, coef = moe.balance_loss_alloc(z, torch.zeros(T, 1, dtype=torch.int32, device="cuda"), good)
+    assert abs(loss.item() - 1) <= 64 * U32 and (counts.flatten() == good.diff()).all()
