@@ -275,11 +275,10 @@ def _dense(fn: str, *tensors):
                            f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
-def _current(fn: str, t):
-    """Kernels are launched on the current device: its tensors only."""
-    at = t.get_device()
-    if at < 0 or at != torch.cuda.current_device():
-        raise MoeError(fn, MOE_ERR_UNSUPPORTED, f"tensors of the current device are needed, got {t.device}")
+def _current(fn: str, at: int, stream=None):
+    """Kernels are launched on the current device: its tensors (device index `at`) and streams only."""
+    if at < 0 or at != torch.cuda.current_device() or (stream is not None and stream.device_index != at):
+        raise MoeError(fn, MOE_ERR_UNSUPPORTED, f"tensors and a stream of the current device are needed, got tensors of device {at}")
 
 
 _U8, _MASK, _I32, _F32 = (torch.uint8,), (torch.uint8, torch.bool), (torch.int32,), (torch.float32,)
@@ -297,7 +296,7 @@ def moe_quantize_fp8(x, q, sf, stream=None):
     _dense("moe_quantize_fp8", ("x", x, _REAL), ("q", q, _U8), ("sf", sf, _F32))
     rows, cols = x.shape
     _sized("moe_quantize_fp8", q.numel() == rows * cols and sf.numel() == rows * _fp8_blocks(cols), "q or sf size")
-    _current("moe_quantize_fp8", x)
+    _current("moe_quantize_fp8", x.get_device(), stream)
     _check("moe_quantize_fp8", lib().moe_quantize_fp8(_at(x), _DTYPES[x.dtype], rows, cols, _at(q), _at(sf), _stream(stream)))
 
 
@@ -309,7 +308,7 @@ def moe_quantize_fp8_weights(w, q, sf, qt=None, sft=None, stream=None):
     tiles = E * _fp8_blocks(N) * _fp8_blocks(K)
     _sized("moe_quantize_fp8_weights", all(t is None or t.numel() == n for t, n in (
         (q, w.numel()), (sf, tiles), (qt, w.numel()), (sft, tiles))), "an output's size")
-    _current("moe_quantize_fp8_weights", w)
+    _current("moe_quantize_fp8_weights", w.get_device(), stream)
     _check("moe_quantize_fp8_weights", lib().moe_quantize_fp8_weights(
         _at(w), _DTYPES[w.dtype], E, N, K, _at(q), _at(sf), _at(qt), _at(sft), _stream(stream)))
 
@@ -327,7 +326,7 @@ def moe_quantize_fp8_tokens(x, expert_offsets, R, q, sf, rows=None, stream=None)
     blocks = moe_fp8_token_blocks(R, E)
     _sized("moe_quantize_fp8_tokens", q.numel() >= blocks * cols * 128 and sf.numel() >= blocks * cols
            and (rows is None or rows.numel() >= R), "q, sf or rows size")
-    _current("moe_quantize_fp8_tokens", x)
+    _current("moe_quantize_fp8_tokens", x.get_device(), stream)
     _check("moe_quantize_fp8_tokens", lib().moe_quantize_fp8_tokens(
         _at(x), _DTYPES[x.dtype], rows_x, _at(rows), _at(expert_offsets), E, int(R), cols, _at(q), _at(sf), _stream(stream)))
 
@@ -345,10 +344,12 @@ def make_gemm_fp8_args(A, A_sf, B, B_sf, expert_offsets, R, epilogue, D=None, D_
            and expert_offsets.numel() == E + 1 and (A_rows is None or A_rows.numel() >= R)
            and (D is None or D.numel() >= R * (N // 2 if fp8_act else N))
            and (D_sf is None or D_sf.numel() >= R * (N // 256)), "operand sizes do not agree")
-    _current("make_gemm_fp8_args", A)
-    return moe_gemm_fp8_args(A.data_ptr(), A_sf.data_ptr(), A_rows.data_ptr() if A_rows is not None else None, rows_A,
+    _current("make_gemm_fp8_args", A.get_device())
+    args = moe_gemm_fp8_args(A.data_ptr(), A_sf.data_ptr(), A_rows.data_ptr() if A_rows is not None else None, rows_A,
                              B.data_ptr(), B_sf.data_ptr(), expert_offsets.data_ptr(), E, N, K, epilogue, R,
                              D.data_ptr() if D is not None else None, D_sf.data_ptr() if D_sf is not None else None)
+    args.device = A.get_device()
+    return args
 
 
 def moe_grouped_gemm_fp8_can_implement(args: moe_gemm_fp8_args) -> int:
@@ -356,6 +357,8 @@ def moe_grouped_gemm_fp8_can_implement(args: moe_gemm_fp8_args) -> int:
 
 
 def moe_grouped_gemm_fp8(args: moe_gemm_fp8_args, stream=None):
+    if (at := getattr(args, "device", None)) is not None:   # (a caller may fill the structure without make_gemm_fp8_args)
+        _current("moe_grouped_gemm_fp8", at, stream)
     _check("moe_grouped_gemm_fp8", lib().moe_grouped_gemm_fp8(C.byref(args), _stream(stream)))
 
 
@@ -368,9 +371,11 @@ def make_wgrad_fp8_args(Y, Y_sf, X, X_sf, expert_offsets, R, D) -> moe_wgrad_fp8
     _sized("make_wgrad_fp8_args", expert_offsets.numel() == E + 1 and Y.numel() >= blocks * N * 128
            and Y_sf.numel() >= blocks * N and X.numel() >= blocks * K * 128 and X_sf.numel() >= blocks * K,
            "operand sizes do not agree")
-    _current("make_wgrad_fp8_args", D)
-    return moe_wgrad_fp8_args(Y.data_ptr(), Y_sf.data_ptr(), X.data_ptr(), X_sf.data_ptr(), expert_offsets.data_ptr(),
+    _current("make_wgrad_fp8_args", D.get_device())
+    args = moe_wgrad_fp8_args(Y.data_ptr(), Y_sf.data_ptr(), X.data_ptr(), X_sf.data_ptr(), expert_offsets.data_ptr(),
                               E, N, K, _DTYPES[D.dtype], int(R), D.data_ptr())
+    args.device = D.get_device()
+    return args
 
 
 def moe_grouped_wgrad_fp8_can_implement(args: moe_wgrad_fp8_args) -> int:
@@ -378,6 +383,8 @@ def moe_grouped_wgrad_fp8_can_implement(args: moe_wgrad_fp8_args) -> int:
 
 
 def moe_grouped_wgrad_fp8(args: moe_wgrad_fp8_args, stream=None):
+    if (at := getattr(args, "device", None)) is not None:   # (a caller may fill the structure without make_wgrad_fp8_args)
+        _current("moe_grouped_wgrad_fp8", at, stream)
     _check("moe_grouped_wgrad_fp8", lib().moe_grouped_wgrad_fp8(C.byref(args), _stream(stream)))
 
 
@@ -389,12 +396,12 @@ def moe_balance_loss(logits, topk_ids, counts, coef, loss, seq_offsets=None, tok
     """logits [T, E] f32, topk_ids [T, k] i32, seq_offsets [S+1] i32 or None (S = 1), token_mask [T] u8
     or None -> counts [S, E] i32, coef [S, E] f32 (for the backward pass), loss [1] f32."""
     _dense("moe_balance_loss", ("logits", logits, _F32), ("topk_ids", topk_ids, _I32), ("counts", counts, _I32), ("coef", coef, _F32), ("loss", loss, _F32),
-           ("seq_offsets", seq_offsets, _I32), ("token_mask", token_mask, _MASK))
+           ("seq_offsets", seq_offsets, _I32), ("token_mask", token_mask, _MASK), ("ws", ws, _U8))
     (T, E), k = logits.shape, topk_ids.shape[1]
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
     _sized("moe_balance_loss", topk_ids.shape[0] == T and counts.numel() == S * E and coef.numel() == S * E
            and loss.numel() >= 1 and (token_mask is None or token_mask.numel() == T), "operand sizes do not agree")
-    _current("moe_balance_loss", logits)
+    _current("moe_balance_loss", logits.get_device(), stream)
     if ws is None:
         with _allocating(stream):
             ws = _ws(moe_balance_loss_workspace(T, E, k, S), logits.device)
@@ -417,7 +424,7 @@ def moe_balance_loss_backward(logits, coef, grad_loss, dlogits, seq_offsets=None
            and (token_mask is None or token_mask.numel() == T)
            and (d_topk_w is None or all(t is not None and t.shape == (T, k) for t in (topk_ids, topk_w, d_topk_w))),
            "operand sizes do not agree")
-    _current("moe_balance_loss_backward", logits)
+    _current("moe_balance_loss_backward", logits.get_device(), stream)
     _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
         _at(logits), T, E, _at(seq_offsets), S, _at(token_mask), _at(coef), _at(grad_loss), _at(topk_ids), _at(topk_w),
         _at(d_topk_w), k, _at(dlogits), _stream(stream)))
@@ -694,6 +701,7 @@ class MoEFP8LayerPlan:
         self.xq = FP8Tensor(z(T, H, dt=torch.uint8), z(T, _fp8_blocks(H), dt=torch.float32))
         self.actq = FP8Tensor(z(R, I, dt=torch.uint8), z(R, _fp8_blocks(I), dt=torch.float32))
         self.Y, self.out = z(R, H, dt=torch.bfloat16), z(T, H, dt=torch.bfloat16)
+        _sized("MoEFP8LayerPlan", W1.q.shape == (E, 2 * I, H) and W2.q.shape == (E, H, I), "W1 [E, 2I, H] and W2 [E, H, I] are needed")
         self.W1, self.W2 = W1, W2
         self.args1 = make_gemm_fp8_args(self.xq.q, self.xq.sf, W1.q, W1.sf, self.off, R, MOE_EPI_SWIGLU_FP8,
                                         self.actq.q, self.actq.sf, self.row_src)
@@ -703,6 +711,8 @@ class MoEFP8LayerPlan:
         self.ws_route = _ws(lib().moe_route_permute_workspace(T, E, k), dev)
 
     def forward(self, logits, x, stream=None):
+        _dense("MoEFP8LayerPlan.forward", ("logits", logits, _F32), ("x", x, _REAL), ("out", self.out, _BF16))
+        _sized("MoEFP8LayerPlan.forward", logits.shape == (self.T, self.E) and x.shape == (self.T, self.H), "logits [T, E] and x [T, H] are needed")
         main = stream if stream is not None else torch.cuda.current_stream()
         moe_route_permute(logits, self.k, self.ids, self.w, self.off, self.row_src, self.tsr, self.ws_route, main)
         moe_quantize_fp8(x, self.xq.q, self.xq.sf, main)

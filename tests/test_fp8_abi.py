@@ -259,3 +259,25 @@ def test_reference_products_and_gradients():
             zm[t, j] -= h
             f = lambda v: 1.7 * (coef[[0] * 4 + [2] * 5] * mask[:, None] * ref.softmax(v)).sum() + (rw(v) * dw).sum()
             assert abs((f(zp) - f(zm)) / (2 * h) - d[t, j]) < 1e-7, (t, j)
+
+
+def test_binding_refuses_another_device_and_wrong_layer_shapes():
+    g = gemm_args()
+    g.device = -1
+    w = moe.moe_wgrad_fp8_args()
+    w.device = -1
+    for call, a in ((moe.moe_grouped_gemm_fp8, g), (moe.moe_grouped_wgrad_fp8, w)):
+        with pytest.raises(moe.MoeError) as e:
+            call(a)
+        assert e.value.status == UNSUPPORTED
+    E, H, I = 2, 256, 128
+    z = lambda *s: moe.FP8Tensor(torch.zeros(*s, dtype=torch.uint8), torch.zeros(s[0], -(-s[1] // 128), -(-s[2] // 128)))
+    for w1, w2 in ((z(E, I, H), z(E, H, I)), (z(E, 2 * I, H), z(E, I, I)), (z(E + 1, 2 * I, H), z(E, H, I))):
+        with pytest.raises(moe.MoeError) as e:
+            moe.MoEFP8LayerPlan(4, E, 1, H, I, w1, w2, device="cpu")
+        assert e.value.status == SHAPE
+    ws = torch.zeros(1 << 12)   # not bytes
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_balance_loss(torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(1, 8, dtype=torch.int32),
+                             torch.zeros(1, 8), torch.zeros(1), ws=ws)
+    assert e.value.status == UNSUPPORTED

@@ -251,3 +251,30 @@ def test_binding_refuses_mixed_devices_and_host_tensors():
     for bad in ((x.cpu(), q, sf), (x, q.cpu(), sf), (x, q, sf.cpu()), (x.cpu(), q.cpu(), sf.cpu())):
         with pytest.raises(moe.MoeError):
             moe.moe_quantize_fp8(*bad)
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    class Elsewhere:
+        device_index, cuda_stream = 1, 0
+    a = _training_inputs(3)
+    X, W = moe.quantize_fp8_alloc(a["x"]), moe.quantize_fp8_weights_alloc(a["w"])
+    D = torch.empty(a["R"], a["w"].shape[1], dtype=torch.bfloat16, device="cuda")
+    args = moe.make_gemm_fp8_args(X.q, X.sf, W.q, W.sf, a["off"], a["R"], moe.MOE_EPI_NONE, D, A_rows=a["src"])
+    calls = [lambda s: moe.moe_grouped_gemm_fp8(args, s), lambda s: moe.moe_quantize_fp8(a["x"], X.q, X.sf, s),
+             lambda s: moe.moe_quantize_fp8_weights(a["w"], W.q, W.sf, stream=s)]
+    for call in calls:
+        with pytest.raises(moe.MoeError):
+            call(Elsewhere())
+        call(torch.cuda.current_stream())
+
+
+def test_layer_refuses_other_shapes():
+    T, E, k, H, I = 20, 32, 2, 272, 128
+    g = _gen(31)
+    plan = moe.MoEFP8LayerPlan(T, E, k, H, I, *_weights(g, E, H, I))
+    logits, x = _randn(g, T, E, dt=torch.float32), _randn(g, T, H)
+    want = plan.forward(logits, x).clone()
+    for l, y in ((logits[:-1], x), (logits, x[:-1]), (logits[:, :-16].contiguous(), x), (logits.double(), x), (logits.T, x)):
+        with pytest.raises(moe.MoeError):
+            plan.forward(l, y)
+    assert torch.equal(plan.forward(logits, x).view(torch.int16), want.view(torch.int16))
