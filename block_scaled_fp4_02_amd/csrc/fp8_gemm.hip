@@ -111,6 +111,15 @@ __device__ __forceinline__ void arrive() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(LATER) : "memory");
 }
 
+// Between LDS writes and reads of different lanes of one wave, either way round.  LDS serves a wave in
+// order, so no instruction is needed; the compiler, to which the lanes' addresses need not overlap,
+// has to keep the order as well.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---- one tile -----------------------------------------------------------------------------
 
 template <int BQ_, int BP_, int WQ_, int WP_, int STAGES_>
@@ -573,6 +582,7 @@ __device__ __forceinline__ void gemm_tile(const GemmParams &P, uint8_t *lds, con
 #pragma unroll
         for (int ti = 0; ti < T::TP; ti++)
           *reinterpret_cast<uint2 *>(mine + (j * 16 + r) * kStride + ti * 32 + lg * 8) = bf16x4(acc[ti][j0 + j]);
+      wave_order();
 #pragma unroll
       for (int c = 0; c < kPieces; c++) {
         const int at = c * kWave + lane, row = at / (kRow / 16), col = at % (kRow / 16) * 8;   // col: of the wave's columns
@@ -582,6 +592,7 @@ __device__ __forceinline__ void gemm_tile(const GemmParams &P, uint8_t *lds, con
         if (t >= count || n >= P.N) continue;
         store16<T::kLarge>(D + static_cast<int64_t>(first + t) * P.N + n, v);
       }
+      wave_order();
     }
   } else {
     // act = silu(gate) up in binary32 (hardware exp2 and reciprocal); its maximum over the 128
@@ -911,6 +922,7 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
       if (MODE == kWgradF32) *reinterpret_cast<float4v *>(at) = acc[ti][j];
       else *reinterpret_cast<uint2 *>(at) = bf16x4(acc[ti][j]);
     }
+    wave_order();
 #pragma unroll
     for (int c = 0; c < kPieces; c++) {
       const int at = c * kWave + lane, row = at / (kRow / 16), col = at % (kRow / 16) * kPer;   // col: of the wave's columns
@@ -920,6 +932,7 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
       if (n >= P.N || k >= P.K) continue;
       store16<true>(static_cast<uint8_t *>(P.D) + ((static_cast<int64_t>(t.e) * P.N + n) * P.K + k) * kElem, v);
     }
+    wave_order();
   }
 }
 
