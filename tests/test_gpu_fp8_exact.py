@@ -1,0 +1,99 @@
+"""The FP8 products on operands for which every sum is exact in any order, so a single lost, doubled
+or misplaced element shows in every kernel behind moe_grouped_gemm_fp8."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_fp4_02_amd as moe
+from tests import fp8_ref as ref
+from tests.fp8_ref import dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    moe.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def kernel_of(R, E, N, K, swiglu=False):
+    """The kernel that the library's rule takes, which follows the sizes alone."""
+    hit = min(R, E)
+    mean = R // hit
+    tiles = lambda q, c: (R // q + hit) * -(-N // c)
+    large = mean > 44 and K > 384 and tiles(256, 256) >= 192
+    if swiglu:
+        return "256 x 256" if large else "32 rows" if tiles(64, 256) < 192 else "64 rows"
+    if large:
+        return "256 x 256"
+    if tiles(64, 128) < 192 and K >= 512:
+        return "split 64" if mean > 32 else "split 32" if mean > 16 else "split 16" if tiles(16, 32) >= 192 else "split 16, 16 columns"
+    if mean > 88 and tiles(128, 128) >= 192:
+        return "128 x 128"
+    if K <= 256 and tiles(64, 512) >= 768:
+        return "64 rows, four tiles"
+    return "64 rows, two stages" if K <= 512 else "64 rows"
+
+
+def _sizes(E, mean):
+    """E groups with an empty one, a short one and a long one, `mean` rows each in all."""
+    sizes = np.full(E, mean)
+    if E >= 3 and mean > 1:
+        sizes[0], sizes[1], sizes[E // 2] = 0, 1, mean + mean + mean - 1
+    return sizes
+
+
+def _integers(E, mean, N, K, gather, wide):
+    """Codes of -1, 0, 1 (wide: with two products of +-100352 that cancel in front of every sum) and scales
+    of 1 and 2, 1/2 and 1: (offsets, R, A, B, rows, a's values, a function of e for B's values)."""
+    g = torch.Generator(device="cuda").manual_seed(E * N + K)
+    off = np.concatenate([[0], np.cumsum(_sizes(E, mean))]).astype(np.int32)
+    R = int(off[-1])
+    rows_A = R // 2 + 1 if gather else R
+    code = {v: int(ref.e4m3_codes(np.float64(v))) for v in (-1, 0, 1, 448, 224, -224)}
+    small = torch.tensor([code[-1], code[0], code[1]], dtype=torch.uint8, device="cuda")
+    pick = lambda *s: small[torch.randint(0, 3, s, generator=g, device="cuda")]
+    kb, nb = -(-K // 128), -(-N // 128)
+    power = lambda lo, *s: 2.0 ** torch.randint(lo, lo + 2, s, generator=g, device="cuda").float()
+    A, B = moe.FP8Tensor(pick(rows_A, K), power(0, rows_A, kb)), moe.FP8Tensor(pick(E, N, K), power(-1, E, nb, kb))
+    if wide:
+        A.q[:, :2] = code[448]
+        B.q[..., 0], B.q[..., 1] = code[224], code[-224]
+    rows = torch.randint(0, rows_A, (R,), generator=g, device="cuda", dtype=torch.int32) if gather else None
+    table = torch.from_numpy(ref.e4m3_values()).cuda()
+    up = lambda s, n, d: s.double().repeat_interleave(128, d).narrow(d, 0, n)
+    a = table[A.q.long()] * up(A.sf, K, 1)
+    return off, R, A, B, rows, a if rows is None else a[rows.long()], lambda e: table[B.q[e].long()] * up(up(B.sf[e], N, 0), K, 1)
+
+
+PRODUCTS = {
+    "split 16, 16 columns": [(6, 9, 272, 2064), (1, 1, 16, 528)],
+    "split 16": [(8, 10, 784, 1040), (8, 16, 1040, 512)],
+    "split 32": [(4, 26, 240, 1104), (9, 17, 528, 2064)],
+    "split 64": [(3, 80, 400, 656), (2, 33, 1040, 1040)],
+    "64 rows, four tiles": [(200, 12, 1616, 240), (256, 3, 2576, 16), (200, 70, 1024, 144)],
+    "64 rows, two stages": [(90, 12, 528, 400), (5, 7, 48, 272)],
+    "64 rows": [(90, 20, 528, 1552), (40, 6, 2048, 2064)],      # the second one past the caches
+    "128 x 128": [(8, 220, 1648, 368), (20, 130, 1040, 144)],
+    "256 x 256": [(70, 70, 1040, 528), (64, 200, 1024, 1024), (72, 90, 2048, 1040), (30, 300, 1296, 400)],
+}
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("kernel, size", [(k, s) for k, sizes in PRODUCTS.items() for s in sizes])
+def test_product(kernel, size, gather):
+    E, mean, N, K = size
+    off, R, A, B, rows, a, b = _integers(E, mean, N, K, gather, False)
+    assert kernel_of(R, E, N, K) == kernel
+    D = torch.full((R + 3, N), 7.5, dtype=torch.bfloat16, device="cuda")
+    moe.moe_grouped_gemm_fp8(moe.make_gemm_fp8_args(A.q, A.sf, B.q, B.sf, dev(off), R, moe.MOE_EPI_NONE, D, A_rows=rows))
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        assert torch.equal(D[lo:hi].double(), (a[lo:hi] @ b(e).T).bfloat16().double()), e
+    assert (D[R:] == 7.5).all()
