@@ -8,7 +8,7 @@ import torch
 
 import block_scaled_fp4_02_amd as moe
 from tests import fp8_ref as ref
-from tests.fp8_ref import dev
+from tests.fp8_ref import U32, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +97,41 @@ def test_product(kernel, size, gather):
         lo, hi = int(off[e]), int(off[e + 1])
         assert torch.equal(D[lo:hi].double(), (a[lo:hi] @ b(e).T).bfloat16().double()), e
     assert (D[R:] == 7.5).all()
+
+
+def _check_act(act, y, what):
+    """act = silu(gate) up of exact sums y: 8 steps for exp2, the reciprocal and the products, the rounded
+    exponent's |gate| 2^-24, and the code's half step, 2^-4 of the value or 2^-10 of the scale."""
+    I = y.shape[1] // 2
+    gate, up = y[:, :I], y[:, I:]
+    want = gate / (1 + torch.exp(-gate)) * up
+    err = (8 + 2 * gate.abs()) * 2 * U32 * want.abs()
+    s = act.sf.double()
+    peak, tol = want.abs().unflatten(1, (I // 128, 128)).amax(2), err.unflatten(1, (I // 128, 128)).amax(2)
+    assert ((s * 448 - peak).abs() <= tol + 4 * U32 * (peak + tol)).all(), what
+    table = torch.from_numpy(ref.e4m3_values()).cuda()
+    s = s.repeat_interleave(128, 1)
+    lim = (want.abs() + err) * 2.0 ** -4 + s * 2.0 ** -10 + err + 4 * U32 * want.abs()
+    assert ((table[act.q.long()] * s - want).abs() <= lim).all(), what
+
+
+SWIGLU = {
+    "32 rows": [(8, 5, 512, 1040), (3, 20, 256, 144), (1, 1, 256, 16)],
+    "64 rows": [(90, 20, 512, 528), (40, 6, 2048, 2064)],
+    "256 x 256": [(70, 70, 1024, 528), (64, 200, 1024, 1024), (72, 90, 2048, 1040)],
+}
+
+
+@pytest.mark.parametrize("kernel, size, wide", [(k, s, w) for k, sizes in SWIGLU.items() for s in sizes for w in (False, True)
+                                                if not (w and k == "256 x 256")])
+def test_swiglu(kernel, size, wide):
+    """wide: the smaller tiles sum whole products, so two that cancel leave the small ones as they are (the
+    256 x 256 tile may cut them at 2^-13 of the large ones: not asked of it)."""
+    E, mean, N, K = size
+    off, R, A, B, rows, a, b = _integers(E, mean, N, K, True, wide)
+    assert kernel_of(R, E, N, K, True) == kernel
+    act = moe.grouped_gemm_fp8_alloc(A, B, dev(off), R, moe.MOE_EPI_SWIGLU_FP8, rows)
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if hi > lo:
+            _check_act(moe.FP8Tensor(act.q[lo:hi], act.sf[lo:hi]), a[lo:hi] @ b(e).T, e)
