@@ -1,5 +1,6 @@
 """The FP8 products on operands for which every sum is exact in any order, so a single lost, doubled
-or misplaced element shows in every kernel behind moe_grouped_gemm_fp8."""
+or misplaced element shows in every kernel behind moe_grouped_gemm_fp8, and the gradients against
+differences without a tolerance."""
 from __future__ import annotations
 
 import numpy as np
@@ -135,3 +136,45 @@ def test_swiglu(kernel, size, wide):
         lo, hi = int(off[e]), int(off[e + 1])
         if hi > lo:
             _check_act(moe.FP8Tensor(act.q[lo:hi], act.sf[lo:hi]), a[lo:hi] @ b(e).T, e)
+
+
+def test_gradients_equal_differences():
+    """f = sum c . y over operands that FP8 holds exactly (-1, 0, 1 and a 7 in every block, so every scale is
+    2^-6) and results that bf16 holds exactly (whole numbers up to 256): f's differences in x and in w
+    are dx and dw without any rounding, and dx is c w."""
+    rng = np.random.default_rng(41)
+    N, K, sizes = 48, 144, [5, 0, 9]
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    R, o, e_of = int(off[-1]), dev(off), np.repeat(np.arange(3), sizes)
+    whole = lambda *s: torch.from_numpy(rng.integers(-1, 2, s).astype(np.float32))
+    x, w, c = whole(R, K), whole(3, N, K), whole(R, N)
+    x[:, 0] = x[:, 128] = w[..., 0] = c[:, 0] = 7.0
+    w[..., 128] = -7.0
+    xc, cc = x.clone(), c.clone()
+    first = [int(off[e]) for e in range(3) if sizes[e]]
+    xc[first], cc[first] = 7.0, 7.0                       # a 7 in every column of every group
+    exact = lambda x, w: torch.stack([w[e_of[p]].double() @ x[p].double() for p in range(R)])
+
+    def y(x, w):
+        got = moe.grouped_gemm_fp8_alloc(moe.quantize_fp8_alloc(x.cuda()), moe.quantize_fp8_weights_alloc(w.cuda()), o, R).double().cpu()
+        want = exact(x, w)
+        assert want.abs().max() <= 256 and torch.equal(got, want)
+        return got
+
+    dx = moe.grouped_gemm_fp8_alloc(moe.quantize_fp8_alloc(c.cuda()), moe.quantize_fp8_weights_alloc(w.cuda(), True)[1], o, R).double().cpu()
+    assert torch.equal(dx, torch.stack([c[p].double() @ w[e_of[p]].double() for p in range(R)]).bfloat16().double())
+    changed = 0
+    for p in range(R):
+        for k in rng.choice(np.arange(1, 128), 3, replace=False):
+            up = x.clone()
+            up[p, k] += 2 if x[p, k] < 1 else -2
+            slope = (((y(up, w) - y(x, w)) * c).sum() / (up[p, k] - x[p, k])).item()
+            assert slope == dx[p, k].item()
+            changed += slope != 0
+    assert changed > R
+    dw = moe.grouped_wgrad_fp8_alloc(moe.quantize_fp8_tokens_alloc(cc.cuda(), o, R), moe.quantize_fp8_tokens_alloc(xc.cuda(), o, R), o, R).double().cpu()
+    assert (dw[1] == 0).all()
+    for e, n, k in [(0, 3, 5), (2, 47, 143), (0, 0, 7), (1, 5, 5), (2, 0, 127), (0, 47, 129)]:
+        up = w.clone()
+        up[e, n, k] += 2 if w[e, n, k] < 1 else -2
+        assert (((y(xc, up) - y(xc, w)) * cc).sum() / (up[e, n, k] - w[e, n, k])).item() == dw[e, n, k].item()
