@@ -283,7 +283,8 @@ def _current(fn: str, at: int, stream=None):
 
 _U8, _MASK, _I32, _F32 = (torch.uint8,), (torch.uint8, torch.bool), (torch.int32,), (torch.float32,)
 _BF16, _REAL = (torch.bfloat16,), (torch.bfloat16, torch.float32)
-_WIDE = (_U8, _BF16, _REAL)
+_CODES = (torch.uint8, torch.float8_e4m3fn)   # E4M3 codes as bytes, or as the type that checkpoints hold them in
+_WIDE = (_U8, _BF16, _REAL, _CODES)
 
 
 def _sized(fn: str, ok: bool, what: str):
@@ -292,8 +293,9 @@ def _sized(fn: str, ok: bool, what: str):
 
 
 def moe_quantize_fp8(x, q, sf, stream=None):
-    """x [rows, C] bf16 or f32 -> q [rows, C] u8 E4M3 codes, sf [rows, ceil(C/128)] f32 scales."""
-    _dense("moe_quantize_fp8", ("x", x, _REAL), ("q", q, _U8), ("sf", sf, _F32))
+    """x [rows, C] bf16 or f32 -> q [rows, C] E4M3 codes, sf [rows, ceil(C/128)] f32 scales.  Codes are u8
+    or float8_e4m3fn, here and in the functions below."""
+    _dense("moe_quantize_fp8", ("x", x, _REAL), ("q", q, _CODES), ("sf", sf, _F32))
     rows, cols = x.shape
     _sized("moe_quantize_fp8", q.numel() == rows * cols and sf.numel() == rows * _fp8_blocks(cols), "q or sf size")
     _current("moe_quantize_fp8", x.get_device(), stream)
@@ -303,7 +305,7 @@ def moe_quantize_fp8(x, q, sf, stream=None):
 def moe_quantize_fp8_weights(w, q, sf, qt=None, sft=None, stream=None):
     """w [E, N, K] bf16 or f32 -> q, sf with one scale per 128 x 128 tile; qt [E, K, N] and sft
     receive the transposed copy."""
-    _dense("moe_quantize_fp8_weights", ("w", w, _REAL), ("q", q, _U8), ("sf", sf, _F32), ("qt", qt, _U8), ("sft", sft, _F32))
+    _dense("moe_quantize_fp8_weights", ("w", w, _REAL), ("q", q, _CODES), ("sf", sf, _F32), ("qt", qt, _CODES), ("sft", sft, _F32))
     E, N, K = w.shape
     tiles = E * _fp8_blocks(N) * _fp8_blocks(K)
     _sized("moe_quantize_fp8_weights", all(t is None or t.numel() == n for t, n in (
@@ -320,7 +322,7 @@ def moe_fp8_token_blocks(R: int, E: int) -> int:
 def moe_quantize_fp8_tokens(x, expert_offsets, R, q, sf, rows=None, stream=None):
     """x [rows_x, C] -> q [blocks, C, 128], sf [blocks, C]: blocks of 128 permuted rows of a group,
     one scale per column (blocks = moe_fp8_token_blocks(R, E))."""
-    _dense("moe_quantize_fp8_tokens", ("x", x, _REAL), ("expert_offsets", expert_offsets, _I32), ("q", q, _U8), ("sf", sf, _F32), ("rows", rows, _I32))
+    _dense("moe_quantize_fp8_tokens", ("x", x, _REAL), ("expert_offsets", expert_offsets, _I32), ("q", q, _CODES), ("sf", sf, _F32), ("rows", rows, _I32))
     rows_x, cols = x.shape
     E = expert_offsets.numel() - 1
     blocks = moe_fp8_token_blocks(R, E)
@@ -333,11 +335,11 @@ def moe_quantize_fp8_tokens(x, expert_offsets, R, q, sf, rows=None, stream=None)
 
 def make_gemm_fp8_args(A, A_sf, B, B_sf, expert_offsets, R, epilogue, D=None, D_sf=None, A_rows=None) -> moe_gemm_fp8_args:
     """A [rows_A, K] / A_sf from moe_quantize_fp8, B [E, N, K] / B_sf from moe_quantize_fp8_weights;
-    D bf16 [R, N] (NONE), or u8 [R, N/2] with D_sf f32 [R, N/256] (SWIGLU_FP8).  The tensors must
+    D bf16 [R, N] (NONE), or codes [R, N/2] with D_sf f32 [R, N/256] (SWIGLU_FP8).  The tensors must
     outlive the arguments' use."""
     fp8_act = epilogue == MOE_EPI_SWIGLU_FP8
-    _dense("make_gemm_fp8_args", ("A", A, _U8), ("A_sf", A_sf, _F32), ("B", B, _U8), ("B_sf", B_sf, _F32), ("expert_offsets", expert_offsets, _I32),
-           ("D", D, _U8 if fp8_act else _BF16), ("D_sf", D_sf, _F32), ("A_rows", A_rows, _I32))
+    _dense("make_gemm_fp8_args", ("A", A, _CODES), ("A_sf", A_sf, _F32), ("B", B, _CODES), ("B_sf", B_sf, _F32), ("expert_offsets", expert_offsets, _I32),
+           ("D", D, _CODES if fp8_act else _BF16), ("D_sf", D_sf, _F32), ("A_rows", A_rows, _I32))
     E, N, K = B.shape
     rows_A, R, kb = A.shape[0], int(R), _fp8_blocks(K)
     _sized("make_gemm_fp8_args", A.shape[1] == K and A_sf.numel() == rows_A * kb and B_sf.numel() == E * _fp8_blocks(N) * kb
@@ -365,7 +367,7 @@ def moe_grouped_gemm_fp8(args: moe_gemm_fp8_args, stream=None):
 def make_wgrad_fp8_args(Y, Y_sf, X, X_sf, expert_offsets, R, D) -> moe_wgrad_fp8_args:
     """Y [blocks, N, 128] / Y_sf and X [blocks, K, 128] / X_sf from moe_quantize_fp8_tokens over the
     same expert_offsets and R; D [E, N, K] f32 or bf16."""
-    _dense("make_wgrad_fp8_args", ("Y", Y, _U8), ("Y_sf", Y_sf, _F32), ("X", X, _U8), ("X_sf", X_sf, _F32), ("expert_offsets", expert_offsets, _I32), ("D", D, _REAL))
+    _dense("make_wgrad_fp8_args", ("Y", Y, _CODES), ("Y_sf", Y_sf, _F32), ("X", X, _CODES), ("X_sf", X_sf, _F32), ("expert_offsets", expert_offsets, _I32), ("D", D, _REAL))
     E, N, K = D.shape
     blocks = moe_fp8_token_blocks(R, E)
     _sized("make_wgrad_fp8_args", expert_offsets.numel() == E + 1 and Y.numel() >= blocks * N * 128
@@ -612,7 +614,7 @@ class MoELayerPlan:
 
 @dataclass
 class FP8Tensor:
-    """Device FP8 tensor: E4M3 codes u8 and f32 scales, one per 128 elements of the contraction (rows
+    """Device FP8 tensor: E4M3 codes (u8 or float8_e4m3fn) and f32 scales, one per 128 elements of the contraction (rows
     [rows, C] / [rows, ceil(C/128)], weights [E, N, K] / one per 128 x 128 tile, or token blocks
     [blocks, C, 128] / [blocks, C])."""
     q: torch.Tensor

@@ -281,3 +281,20 @@ def test_binding_refuses_another_device_and_wrong_layer_shapes():
         moe.moe_balance_loss(torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(1, 8, dtype=torch.int32),
                              torch.zeros(1, 8), torch.zeros(1), ws=ws)
     assert e.value.status == UNSUPPORTED
+
+
+def test_binding_takes_codes_in_their_own_type():
+    """float8_e4m3fn beside uint8 (a wrong size is found behind the type); other 8-bit floats are refused."""
+    bf, u8, f8, i32 = torch.bfloat16, torch.uint8, torch.float8_e4m3fn, torch.int32
+    z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=torch.uint8 if dt.itemsize == 1 else dt).view(dt)
+    refused = lambda status, f, *a, **k: pytest.raises(moe.MoeError, f, *a, **k).value.status == status
+    x, w, off = z(4, 32, dt=bf), z(2, 32, 48, dt=bf), z(3, dt=i32)
+    act = moe.MOE_EPI_SWIGLU_FP8
+    calls = [lambda t: (moe.moe_quantize_fp8, x, z(3, 32, dt=t), z(4, 1)),
+             lambda t: (moe.moe_quantize_fp8_weights, w, z(2, 32, 48, dt=t), z(2, 1, 1), z(2, 48, 16, dt=t), z(2, 1, 1)),
+             lambda t: (moe.moe_quantize_fp8_tokens, x, off, 4, z(1, 32, 128, dt=t), z(2, 32)),
+             lambda t: (moe.make_gemm_fp8_args, z(4, 48, dt=t), z(4, 1), z(2, 256, 32, dt=t), z(2, 2, 1), off, 4, act, z(4, 128, dt=t), z(4, 1)),
+             lambda t: (moe.make_wgrad_fp8_args, z(1, 48, 128, dt=t), z(2, 48), z(2, 32, 128, dt=t), z(2, 32), off, 4, z(2, 48, 32))]
+    for call in calls:
+        assert refused(SHAPE, *call(u8)) and refused(SHAPE, *call(f8))
+        assert refused(UNSUPPORTED, *call(torch.float8_e4m3fnuz)) and refused(UNSUPPORTED, *call(torch.float8_e5m2))

@@ -178,3 +178,27 @@ def test_gradients_equal_differences():
         up = w.clone()
         up[e, n, k] += 2 if w[e, n, k] < 1 else -2
         assert (((y(xc, up) - y(xc, w)) * cc).sum() / (up[e, n, k] - w[e, n, k])).item() == dw[e, n, k].item()
+
+
+def test_codes_in_their_own_type():
+    """float8_e4m3fn codes in and out of every call: the bytes of the u8 ones."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    f8 = torch.float8_e4m3fn
+    R, E, I, K, o = 40, 2, 128, 144, dev(np.array([0, 15, 40], np.int32))
+    x, w = torch.randn(R, K, generator=g, device="cuda").bfloat16(), torch.randn(E, 2 * I, K, generator=g, device="cuda").bfloat16()
+    typed = lambda t: moe.FP8Tensor(torch.empty_like(t.q).view(f8), torch.empty_like(t.sf))
+    same = lambda a, b: torch.equal(a.q.view(torch.uint8), b.q) and torch.equal(a.sf, b.sf)
+    a, (b, bt), t = moe.quantize_fp8_alloc(x), moe.quantize_fp8_weights_alloc(w, True), moe.quantize_fp8_tokens_alloc(x, o, R)
+    a8, b8, bt8, t8 = typed(a), typed(b), typed(bt), typed(t)
+    t8.q.view(torch.uint8).copy_(t.q)      # (blocks that no group has are not written)
+    t8.sf.copy_(t.sf)
+    moe.moe_quantize_fp8(x, a8.q, a8.sf)
+    moe.moe_quantize_fp8_weights(w, b8.q, b8.sf, bt8.q, bt8.sf)
+    moe.moe_quantize_fp8_tokens(x, o, R, t8.q, t8.sf)
+    assert same(a8, a) and same(b8, b) and same(bt8, bt) and same(t8, t)
+    y, act = (moe.grouped_gemm_fp8_alloc(a, b, o, R, e) for e in (moe.MOE_EPI_NONE, moe.MOE_EPI_SWIGLU_FP8))
+    assert torch.equal(moe.grouped_gemm_fp8_alloc(a8, b8, o, R), y)
+    act8 = typed(act)
+    moe.moe_grouped_gemm_fp8(moe.make_gemm_fp8_args(a8.q, a8.sf, b8.q, b8.sf, o, R, moe.MOE_EPI_SWIGLU_FP8, act8.q, act8.sf))
+    assert same(act8, act)
+    assert torch.equal(moe.grouped_wgrad_fp8_alloc(t8, t8, o, R), moe.grouped_wgrad_fp8_alloc(t, t, o, R))
