@@ -296,6 +296,7 @@ def moe_quantize_fp8(x, q, sf, stream=None):
     """x [rows, C] bf16 or f32 -> q [rows, C] E4M3 codes, sf [rows, ceil(C/128)] f32 scales.  Codes are u8
     or float8_e4m3fn, here and in the functions below."""
     _dense("moe_quantize_fp8", ("x", x, _REAL), ("q", q, _CODES), ("sf", sf, _F32))
+    _sized("moe_quantize_fp8", x.dim() == 2, "x [rows, C] is needed")
     rows, cols = x.shape
     _sized("moe_quantize_fp8", q.numel() == rows * cols and sf.numel() == rows * _fp8_blocks(cols), "q or sf size")
     _current("moe_quantize_fp8", x.get_device(), stream)
@@ -306,6 +307,7 @@ def moe_quantize_fp8_weights(w, q, sf, qt=None, sft=None, stream=None):
     """w [E, N, K] bf16 or f32 -> q, sf with one scale per 128 x 128 tile; qt [E, K, N] and sft
     receive the transposed copy."""
     _dense("moe_quantize_fp8_weights", ("w", w, _REAL), ("q", q, _CODES), ("sf", sf, _F32), ("qt", qt, _CODES), ("sft", sft, _F32))
+    _sized("moe_quantize_fp8_weights", w.dim() == 3, "w [E, N, K] is needed")
     E, N, K = w.shape
     tiles = E * _fp8_blocks(N) * _fp8_blocks(K)
     _sized("moe_quantize_fp8_weights", all(t is None or t.numel() == n for t, n in (
@@ -323,6 +325,7 @@ def moe_quantize_fp8_tokens(x, expert_offsets, R, q, sf, rows=None, stream=None)
     """x [rows_x, C] -> q [blocks, C, 128], sf [blocks, C]: blocks of 128 permuted rows of a group,
     one scale per column (blocks = moe_fp8_token_blocks(R, E))."""
     _dense("moe_quantize_fp8_tokens", ("x", x, _REAL), ("expert_offsets", expert_offsets, _I32), ("q", q, _CODES), ("sf", sf, _F32), ("rows", rows, _I32))
+    _sized("moe_quantize_fp8_tokens", x.dim() == 2, "x [rows_x, C] is needed")
     rows_x, cols = x.shape
     E = expert_offsets.numel() - 1
     blocks = moe_fp8_token_blocks(R, E)
@@ -340,6 +343,7 @@ def make_gemm_fp8_args(A, A_sf, B, B_sf, expert_offsets, R, epilogue, D=None, D_
     fp8_act = epilogue == MOE_EPI_SWIGLU_FP8
     _dense("make_gemm_fp8_args", ("A", A, _CODES), ("A_sf", A_sf, _F32), ("B", B, _CODES), ("B_sf", B_sf, _F32), ("expert_offsets", expert_offsets, _I32),
            ("D", D, _CODES if fp8_act else _BF16), ("D_sf", D_sf, _F32), ("A_rows", A_rows, _I32))
+    _sized("make_gemm_fp8_args", A.dim() == 2 and B.dim() == 3, "A [rows_A, K] and B [E, N, K] are needed")
     E, N, K = B.shape
     rows_A, R, kb = A.shape[0], int(R), _fp8_blocks(K)
     _sized("make_gemm_fp8_args", A.shape[1] == K and A_sf.numel() == rows_A * kb and B_sf.numel() == E * _fp8_blocks(N) * kb
@@ -368,6 +372,7 @@ def make_wgrad_fp8_args(Y, Y_sf, X, X_sf, expert_offsets, R, D) -> moe_wgrad_fp8
     """Y [blocks, N, 128] / Y_sf and X [blocks, K, 128] / X_sf from moe_quantize_fp8_tokens over the
     same expert_offsets and R; D [E, N, K] f32 or bf16."""
     _dense("make_wgrad_fp8_args", ("Y", Y, _CODES), ("Y_sf", Y_sf, _F32), ("X", X, _CODES), ("X_sf", X_sf, _F32), ("expert_offsets", expert_offsets, _I32), ("D", D, _REAL))
+    _sized("make_wgrad_fp8_args", D.dim() == 3, "D [E, N, K] is needed")
     E, N, K = D.shape
     blocks = moe_fp8_token_blocks(R, E)
     _sized("make_wgrad_fp8_args", expert_offsets.numel() == E + 1 and Y.numel() >= blocks * N * 128
@@ -399,6 +404,7 @@ def moe_balance_loss(logits, topk_ids, counts, coef, loss, seq_offsets=None, tok
     or None -> counts [S, E] i32, coef [S, E] f32 (for the backward pass), loss [1] f32."""
     _dense("moe_balance_loss", ("logits", logits, _F32), ("topk_ids", topk_ids, _I32), ("counts", counts, _I32), ("coef", coef, _F32), ("loss", loss, _F32),
            ("seq_offsets", seq_offsets, _I32), ("token_mask", token_mask, _MASK), ("ws", ws, _U8))
+    _sized("moe_balance_loss", logits.dim() == 2 and topk_ids.dim() == 2, "logits [T, E] and topk_ids [T, k] are needed")
     (T, E), k = logits.shape, topk_ids.shape[1]
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
     _sized("moe_balance_loss", topk_ids.shape[0] == T and counts.numel() == S * E and coef.numel() == S * E
@@ -419,6 +425,7 @@ def moe_balance_loss_backward(logits, coef, grad_loss, dlogits, seq_offsets=None
     _dense("moe_balance_loss_backward", ("logits", logits, _F32), ("coef", coef, _F32), ("grad_loss", grad_loss, _F32), ("dlogits", dlogits, _F32),
            ("seq_offsets", seq_offsets, _I32), ("token_mask", token_mask, _MASK), ("topk_ids", topk_ids, _I32), ("topk_w", topk_w, _F32),
            ("d_topk_w", d_topk_w, _F32))
+    _sized("moe_balance_loss_backward", logits.dim() == 2 and (d_topk_w is None or d_topk_w.dim() == 2), "logits [T, E] and d_topk_w [T, k] are needed")
     T, E = logits.shape
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
     k = 1 if d_topk_w is None else d_topk_w.shape[1]

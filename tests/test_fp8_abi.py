@@ -298,3 +298,25 @@ def test_binding_takes_codes_in_their_own_type():
     for call in calls:
         assert refused(SHAPE, *call(u8)) and refused(SHAPE, *call(f8))
         assert refused(UNSUPPORTED, *call(torch.float8_e4m3fnuz)) and refused(UNSUPPORTED, *call(torch.float8_e5m2))
+
+
+def test_binding_refuses_other_numbers_of_dimensions():
+    """topk_ids [T, k, 2] and A [rows, K, 2] would be read as if their last axis were not there."""
+    bf, u8, i32 = torch.bfloat16, torch.uint8, torch.int32
+    z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt)
+    off = z(3, dt=i32)
+    g = dict(A=z(4, 32, dt=u8), A_sf=z(4, 1), B=z(2, 48, 32, dt=u8), B_sf=z(2, 1, 1), expert_offsets=off, R=4, epilogue=moe.MOE_EPI_NONE)
+    b = dict(logits=z(6, 4), topk_ids=z(6, 2, dt=i32), counts=z(1, 4, dt=i32), coef=z(1, 4), loss=z(1))
+    d = dict(logits=z(6, 4), coef=z(1, 4), grad_loss=z(1), dlogits=z(6, 4))
+    wg = dict(Y=z(2, 48, 128, dt=u8), Y_sf=z(2, 48), X=z(2, 32, 128, dt=u8), X_sf=z(2, 32), expert_offsets=off, R=4, D=z(2, 48, 32))
+    for f, kw in ((moe.make_gemm_fp8_args, g | dict(A=z(4, 32, 2, dt=u8))), (moe.make_gemm_fp8_args, g | dict(A=z(128, dt=u8))),
+                  (moe.make_gemm_fp8_args, g | dict(B=z(96, 32, dt=u8))), (moe.make_wgrad_fp8_args, wg | dict(D=z(2, 48 * 32))),
+                  (moe.moe_balance_loss, b | dict(topk_ids=z(6, 2, 2, dt=i32))), (moe.moe_balance_loss, b | dict(topk_ids=z(6, dt=i32))),
+                  (moe.moe_balance_loss, b | dict(logits=z(2, 3, 4))), (moe.moe_balance_loss_backward, d | dict(logits=z(24))),
+                  (moe.moe_balance_loss_backward, d | dict(d_topk_w=z(6))),
+                  (moe.moe_quantize_fp8, dict(x=z(2, 2, 32, dt=bf), q=z(4, 32, dt=u8), sf=z(4, 1))),
+                  (moe.moe_quantize_fp8_weights, dict(w=z(32, 48, dt=bf), q=z(32, 48, dt=u8), sf=z(1, 1))),
+                  (moe.moe_quantize_fp8_tokens, dict(x=z(128, dt=bf), expert_offsets=off, R=4, q=z(2, 32, 128, dt=u8), sf=z(2, 32)))):
+        with pytest.raises(moe.MoeError) as e:
+            f(**kw)
+        assert e.value.status == SHAPE, f.__name__
