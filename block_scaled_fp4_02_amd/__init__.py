@@ -30,6 +30,7 @@ MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE
 MOE_DTYPE_BF16, MOE_DTYPE_F32 = 0, 1
 MOE_GS_STATIC, MOE_GS_DYNAMIC = 0, 1
 MOE_EPI_NONE, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_NVFP4, MOE_EPI_SWIGLU_FP8 = 0, 1, 2, 3
+MOE_SUMS_WHOLE = 0x100   # with an FP8 product's epilogue
 MOE_LAYOUT_ROWMAJOR, MOE_LAYOUT_PACKED = 0, 1
 
 EXPORTED = [
@@ -339,8 +340,8 @@ def moe_quantize_fp8_tokens(x, expert_offsets, R, q, sf, rows=None, stream=None)
 def make_gemm_fp8_args(A, A_sf, B, B_sf, expert_offsets, R, epilogue, D=None, D_sf=None, A_rows=None) -> moe_gemm_fp8_args:
     """A [rows_A, K] / A_sf from moe_quantize_fp8, B [E, N, K] / B_sf from moe_quantize_fp8_weights;
     D bf16 [R, N] (NONE), or codes [R, N/2] with D_sf f32 [R, N/256] (SWIGLU_FP8).  The tensors must
-    outlive the arguments' use."""
-    fp8_act = epilogue == MOE_EPI_SWIGLU_FP8
+    outlive the arguments' use.  epilogue | MOE_SUMS_WHOLE: whole products and binary32 sums."""
+    fp8_act = epilogue & ~MOE_SUMS_WHOLE == MOE_EPI_SWIGLU_FP8
     _dense("make_gemm_fp8_args", ("A", A, _CODES), ("A_sf", A_sf, _F32), ("B", B, _CODES), ("B_sf", B_sf, _F32), ("expert_offsets", expert_offsets, _I32),
            ("D", D, _CODES if fp8_act else _BF16), ("D_sf", D_sf, _F32), ("A_rows", A_rows, _I32))
     _sized("make_gemm_fp8_args", A.dim() == 2 and B.dim() == 3, "A [rows_A, K] and B [E, N, K] are needed")
@@ -661,10 +662,11 @@ def quantize_fp8_tokens_alloc(x: torch.Tensor, expert_offsets, R, rows=None, str
 
 
 def grouped_gemm_fp8_alloc(A: FP8Tensor, B: FP8Tensor, expert_offsets, R, epilogue=MOE_EPI_NONE, A_rows=None, stream=None):
-    """D bf16 [R, N] (NONE) or the FP8Tensor act [R, N/2] (SWIGLU_FP8)."""
+    """D bf16 [R, N] (NONE) or the FP8Tensor act [R, N/2] (SWIGLU_FP8); epilogue | MOE_SUMS_WHOLE as in
+    make_gemm_fp8_args."""
     N, R, dev = B.q.shape[1], int(R), A.q.device
     with _allocating(stream):
-        if epilogue == MOE_EPI_SWIGLU_FP8:
+        if epilogue & ~MOE_SUMS_WHOLE == MOE_EPI_SWIGLU_FP8:
             out = FP8Tensor(torch.empty(R, N // 2, dtype=torch.uint8, device=dev),
                             torch.empty(R, N // 256, dtype=torch.float32, device=dev))
             D, D_sf = out.q, out.sf
@@ -698,9 +700,10 @@ def balance_loss_alloc(logits: torch.Tensor, topk_ids: torch.Tensor, seq_offsets
 class MoEFP8LayerPlan:
     """The layer of MoELayerPlan with FP8 experts: W1 [E, 2I, H] and W2 [E, H, I] as FP8Tensor of
     quantize_fp8_weights_alloc (I % 128 == 0).  Buffers and argument blocks are allocated once; the
-    gate/up product quantises its SwiGLU output itself."""
+    gate/up product quantises its SwiGLU output itself.  whole_sums: both products with MOE_SUMS_WHOLE,
+    so a token's output does not depend on the tokens beside it."""
 
-    def __init__(self, T: int, E: int, k: int, H: int, I: int, W1: FP8Tensor, W2: FP8Tensor, device="cuda"):
+    def __init__(self, T: int, E: int, k: int, H: int, I: int, W1: FP8Tensor, W2: FP8Tensor, device="cuda", whole_sums=False):
         self.T, self.E, self.k, self.H, self.I = T, E, k, H, I
         R = self.R = T * k
         dev = torch.device(device)
@@ -712,9 +715,10 @@ class MoEFP8LayerPlan:
         self.Y, self.out = z(R, H, dt=torch.bfloat16), z(T, H, dt=torch.bfloat16)
         _sized("MoEFP8LayerPlan", W1.q.shape == (E, 2 * I, H) and W2.q.shape == (E, H, I), "W1 [E, 2I, H] and W2 [E, H, I] are needed")
         self.W1, self.W2 = W1, W2
-        self.args1 = make_gemm_fp8_args(self.xq.q, self.xq.sf, W1.q, W1.sf, self.off, R, MOE_EPI_SWIGLU_FP8,
+        whole = MOE_SUMS_WHOLE if whole_sums else 0
+        self.args1 = make_gemm_fp8_args(self.xq.q, self.xq.sf, W1.q, W1.sf, self.off, R, MOE_EPI_SWIGLU_FP8 | whole,
                                         self.actq.q, self.actq.sf, self.row_src)
-        self.args2 = make_gemm_fp8_args(self.actq.q, self.actq.sf, W2.q, W2.sf, self.off, R, MOE_EPI_NONE, self.Y)
+        self.args2 = make_gemm_fp8_args(self.actq.q, self.actq.sf, W2.q, W2.sf, self.off, R, MOE_EPI_NONE | whole, self.Y)
         for a in (self.args1, self.args2):
             _check("moe_grouped_gemm_fp8_can_implement", moe_grouped_gemm_fp8_can_implement(a))
         self.ws_route = _ws(lib().moe_route_permute_workspace(T, E, k), dev)

@@ -29,13 +29,16 @@ moe_status check_product(int32_t E, int32_t N, int32_t K, int64_t R) {
   return MOE_OK;
 }
 
+int epilogue_of(const moe_gemm_fp8_args *a) { return a->epilogue & ~MOE_SUMS_WHOLE; }
+
 moe_status check_gemm_fp8(const moe_gemm_fp8_args *a, bool need_pointers) {
   if (a == nullptr) return MOE_ERR_NULL;
   const moe_status st = check_product(a->E, a->N, a->K, a->R);
   if (st != MOE_OK) return st;
   if (a->rows_A < 0 || (a->R > 0 && a->rows_A < 1)) return MOE_ERR_SHAPE;
-  if (a->epilogue != MOE_EPI_NONE && a->epilogue != MOE_EPI_SWIGLU_FP8) return MOE_ERR_UNSUPPORTED;
-  if (a->epilogue == MOE_EPI_SWIGLU_FP8 && a->N % (2 * kFp8Block) != 0) return MOE_ERR_UNSUPPORTED;
+  const int epilogue = epilogue_of(a);
+  if (epilogue != MOE_EPI_NONE && epilogue != MOE_EPI_SWIGLU_FP8) return MOE_ERR_UNSUPPORTED;
+  if (epilogue == MOE_EPI_SWIGLU_FP8 && a->N % (2 * kFp8Block) != 0) return MOE_ERR_UNSUPPORTED;
   // without a gather map row p of A is permuted row p; with one, all of A sits behind one descriptor
   if (a->A_rows == nullptr && a->rows_A < a->R) return MOE_ERR_SHAPE;
   if (a->A_rows != nullptr && a->rows_A > kMaxPackedBufBytes / a->K) return MOE_ERR_UNSUPPORTED;
@@ -44,7 +47,7 @@ moe_status check_gemm_fp8(const moe_gemm_fp8_args *a, bool need_pointers) {
   if (need_pointers) {
     if (!a->B || !a->B_sf || !a->expert_offsets) return MOE_ERR_NULL;
     if (a->R > 0 && (!a->A || !a->A_sf || !a->D)) return MOE_ERR_NULL;
-    if (a->epilogue == MOE_EPI_SWIGLU_FP8 && a->R > 0 && !a->D_sf) return MOE_ERR_NULL;
+    if (epilogue == MOE_EPI_SWIGLU_FP8 && a->R > 0 && !a->D_sf) return MOE_ERR_NULL;
   }
   return MOE_OK;
 }
@@ -128,7 +131,7 @@ moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args *args, hipStream_t strea
   p.R = static_cast<int>(args->R);
   p.D = args->D;
   p.D_sf = args->D_sf;
-  return launch_status(fp8::launch_gemm(p, args->epilogue == MOE_EPI_SWIGLU_FP8, stream));
+  return launch_status(fp8::launch_gemm(p, epilogue_of(args) == MOE_EPI_SWIGLU_FP8, (args->epilogue & MOE_SUMS_WHOLE) != 0, stream));
 }
 
 moe_status moe_grouped_wgrad_fp8_can_implement(const moe_wgrad_fp8_args *args) { return check_wgrad_fp8(args); }

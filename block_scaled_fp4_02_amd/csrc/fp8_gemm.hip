@@ -487,8 +487,8 @@ __device__ __forceinline__ int64_t row_of_a(const GemmParams &P, int p) {
   return a < 0 ? 0 : (a >= P.rows_A ? P.rows_A - 1 : a);
 }
 
-// One tile: up to BQ rows from `first` of group g, n tile `nt`.
-template <class T, Mode MODE>
+// One tile: up to BQ rows from `first` of group g, n tile `nt`.  WHOLE: fp16 matrix core.
+template <class T, Mode MODE, bool WHOLE>
 __device__ __forceinline__ void gemm_tile(const GemmParams &P, uint8_t *lds, const groups::Chunk &g, int first, int count, int nt) {
   const int half_n = P.N / 2;                       // SWIGLU: gate rows, then up rows
   const int n0 = nt * (MODE == kSwigluFp8 ? kFp8Block : T::BP);
@@ -542,20 +542,20 @@ __device__ __forceinline__ void gemm_tile(const GemmParams &P, uint8_t *lds, con
   src.s = uniform(src.s);
 
   float4v acc[T::TP][T::TQ];
-  constexpr bool kWhole = MODE == kSwigluFp8;   // fp16 matrix core
   // the weights of a group of one chunk are read by this workgroup alone (measured at 32 rows per
   // expert, 805 MB of weights: 130 us past the caches, 138 us through them; with two chunks, whose
   // second one finds them in L2, 35 us against 24 us for 77 MB)
   const bool once = g.total == 1 && P.stream_weights;
   if constexpr (T::kLarge) {
+    static_assert(!WHOLE, "the large tile has the FP8 form alone");
     if (once) contract_large<T, true>(src, lds, kb_n, count, acc);
     else contract_large<T, false>(src, lds, kb_n, count, acc);
   } else {
     // Q tiles behind the last row are left out
     auto run = [&](auto active) {
       constexpr int kActive = decltype(active)::value;
-      if (once) contract<T, true, kWhole, kActive>(src, lds, kb_n, acc);
-      else contract<T, false, kWhole, kActive>(src, lds, kb_n, acc);
+      if (once) contract<T, true, WHOLE, kActive>(src, lds, kb_n, acc);
+      else contract<T, false, WHOLE, kActive>(src, lds, kb_n, acc);
     };
     const int active = T::WQ == 1 ? (count + 15) / 16 : T::TQ;
     if (T::TQ >= 4 && active == 3) run(std::integral_constant<int, T::TQ >= 4 ? 3 : T::TQ>());
@@ -638,19 +638,19 @@ __device__ __forceinline__ void gemm_tile(const GemmParams &P, uint8_t *lds, con
   }
 }
 
-template <class T, Mode MODE, int TILES>
+template <class T, Mode MODE, bool WHOLE, int TILES>
 __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) {
   __shared__ __align__(1024) uint8_t lds[T::kLds];
   groups::Chunk g;
   int chunk, nt;
   if (!find_item(P, T::BQ, g, chunk, nt)) return;
   const int first = g.lo + chunk * T::BQ, count = min(T::BQ, g.hi - first);
-  gemm_tile<T, MODE>(P, lds, g, first, count, TILES * nt);
+  gemm_tile<T, MODE, WHOLE>(P, lds, g, first, count, TILES * nt);
 #pragma unroll 1
   for (int i = 1; i < TILES; i++) {
     if ((TILES * nt + i) * T::BP >= P.N) return;
     __syncthreads();   // the tile before is out of LDS
-    gemm_tile<T, MODE>(P, lds, g, first, count, TILES * nt + i);
+    gemm_tile<T, MODE, WHOLE>(P, lds, g, first, count, TILES * nt + i);
   }
 }
 
@@ -937,14 +937,14 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
 }
 
 // TILES: n tiles that a workgroup does one after the other.
-template <class T, Mode MODE, int TILES = 1>
+template <class T, Mode MODE, bool WHOLE, int TILES = 1>
 hipError_t run_gemm(GemmParams p, hipStream_t stream) {
   static_assert(MODE != kSwigluFp8 || TILES == 1, "an n tile is 128 columns of act");
   p.n_tiles = MODE == kSwigluFp8 ? p.N / 2 / kFp8Block : (p.N + TILES * T::BP - 1) / (TILES * T::BP);
   const int64_t items = groups::max_chunks(p.R, p.E, T::BQ) * p.n_tiles;
   const int64_t grid = (items + kXcds - 1) / kXcds * kXcds;
   if (grid > 0)
-    hipLaunchKernelGGL((gemm_kernel<T, MODE, TILES>), dim3(static_cast<uint32_t>(grid)), dim3(T::kThreadsT), 0, stream, p);
+    hipLaunchKernelGGL((gemm_kernel<T, MODE, WHOLE, TILES>), dim3(static_cast<uint32_t>(grid)), dim3(T::kThreadsT), 0, stream, p);
   return hipGetLastError();
 }
 
@@ -977,7 +977,7 @@ hipError_t run_wgrad(const WgradParams &p, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_gemm(GemmParams p, bool swiglu, hipStream_t stream) {
+hipError_t launch_gemm(GemmParams p, bool swiglu, bool whole, hipStream_t stream) {
   const int64_t hit = p.R < p.E ? p.R : p.E;   // at most so many experts have rows
   if (hit == 0) return hipSuccess;
   const int64_t mean = p.R / hit;
@@ -986,23 +986,28 @@ hipError_t launch_gemm(GemmParams p, bool swiglu, hipStream_t stream) {
   auto tiles = [&](int q, int c) { return groups::max_chunks(p.R, p.E, q) * ((p.N + c - 1) / c); };
   const bool large = mean > kLargeRows && p.K > 3 * kFp8Block && tiles(256, 256) >= kManyTiles;
   if (swiglu) {
-    if (large) return run_gemm<Large, kSwigluFp8>(p, stream);
-    if (tiles(64, 256) < kManyTiles) return run_gemm<Tile<32, 256, 1, 4, 3>, kSwigluFp8>(p, stream);
-    return run_gemm<Tile<64, 256, 1, 8, 3>, kSwigluFp8>(p, stream);
+    if (large && !whole) return run_gemm<Large, kSwigluFp8, false>(p, stream);
+    if (tiles(64, 256) < kManyTiles) return run_gemm<Tile<32, 256, 1, 4, 3>, kSwigluFp8, true>(p, stream);
+    return run_gemm<Tile<64, 256, 1, 8, 3>, kSwigluFp8, true>(p, stream);
   }
-  if (large) return run_gemm<Large, kNone>(p, stream);
+  const bool middle = mean > 2 * kLargeRows && tiles(128, 128) >= kManyTiles;
+  if (whole) {
+    if (middle) return run_gemm<Tile<128, 128, 2, 2, 2>, kNone, true>(p, stream);
+    return run_gemm<Tile<64, 128, 1, 4, 3>, kNone, true>(p, stream);
+  }
+  if (large) return run_gemm<Large, kNone, false>(p, stream);
   if (tiles(64, 128) < kManyTiles && p.K >= 4 * kFp8Block) {
     if (mean > 32) return run_split<Split<64, 32, 4, 3>>(p, stream);
     if (mean > 16) return run_split<Split<32, 32, 8, 2>>(p, stream);
     if (tiles(16, 32) >= kManyTiles) return run_split<Split<16, 32, 8, 3>>(p, stream);
     return run_split<Split<16, 16, 8, 3>>(p, stream);
   }
-  if (mean > 2 * kLargeRows && tiles(128, 128) >= kManyTiles) return run_gemm<Tile<128, 128, 2, 2, 2>, kNone>(p, stream);
+  if (middle) return run_gemm<Tile<128, 128, 2, 2, 2>, kNone, false>(p, stream);
   // two steps a tile: looking the item up takes as long (256 experts of 32 rows, N 6144, K 256: 119 us, one
   // tile a workgroup 136; with K 512 no difference)
-  if (p.K <= 2 * kFp8Block && tiles(64, 512) >= 4 * kManyTiles) return run_gemm<Tile<64, 128, 1, 4, 2>, kNone, 4>(p, stream);
-  if (p.K <= 4 * kFp8Block) return run_gemm<Tile<64, 128, 1, 4, 2>, kNone>(p, stream);
-  return run_gemm<Tile<64, 128, 1, 4, 3>, kNone>(p, stream);
+  if (p.K <= 2 * kFp8Block && tiles(64, 512) >= 4 * kManyTiles) return run_gemm<Tile<64, 128, 1, 4, 2>, kNone, false, 4>(p, stream);
+  if (p.K <= 4 * kFp8Block) return run_gemm<Tile<64, 128, 1, 4, 2>, kNone, false>(p, stream);
+  return run_gemm<Tile<64, 128, 1, 4, 3>, kNone, false>(p, stream);
 }
 
 hipError_t launch_wgrad(const WgradParams &p, bool bf16, hipStream_t stream) {

@@ -30,7 +30,7 @@ struct WgradParams {
   void *D;                  // [E, N, K]
 };
 
-hipError_t launch_gemm(GemmParams p, bool swiglu, hipStream_t stream);
+hipError_t launch_gemm(GemmParams p, bool swiglu, bool whole, hipStream_t stream);
 hipError_t launch_wgrad(const WgradParams &p, bool bf16, hipStream_t stream);
 
 }  // namespace fp8

@@ -320,3 +320,18 @@ def test_binding_refuses_other_numbers_of_dimensions():
         with pytest.raises(moe.MoeError) as e:
             f(**kw)
         assert e.value.status == SHAPE, f.__name__
+
+
+def test_whole_sums_are_asked_for_with_the_epilogue(tmp_path):
+    L = moe.lib()
+    whole = moe.MOE_SUMS_WHOLE
+    for epi, want in ((whole, OK), (whole | moe.MOE_EPI_SWIGLU_FP8, OK), (whole | 1, UNSUPPORTED), (whole | 2, UNSUPPORTED),
+                      (2 * whole, UNSUPPORTED), (whole >> 1, UNSUPPORTED), (-whole, UNSUPPORTED), (-1 - whole, UNSUPPORTED)):
+        a = gemm_args(epilogue=epi)
+        assert L.moe_grouped_gemm_fp8_can_implement(C.byref(a)) == want, epi
+        if want != OK:
+            assert L.moe_grouped_gemm_fp8(C.byref(a), None) == want
+    assert L.moe_grouped_gemm_fp8_can_implement(C.byref(gemm_args(epilogue=whole | 3, D_sf=None))) == NULL
+    assert L.moe_grouped_gemm_fp8_can_implement(C.byref(gemm_args(epilogue=whole | 3, N=384))) == UNSUPPORTED
+    with open(os.path.join(ROOT, "include", "moe_nvfp4.h")) as f:
+        assert f"MOE_SUMS_WHOLE = 0x{whole:x} " in f.read()

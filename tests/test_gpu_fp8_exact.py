@@ -9,7 +9,7 @@ import torch
 
 import block_scaled_fp4_02_amd as moe
 from tests import fp8_ref as ref
-from tests.fp8_ref import U32, dev
+from tests.fp8_ref import U16, U32, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -202,3 +202,76 @@ def test_codes_in_their_own_type():
     moe.moe_grouped_gemm_fp8(moe.make_gemm_fp8_args(a8.q, a8.sf, b8.q, b8.sf, o, R, moe.MOE_EPI_SWIGLU_FP8, act8.q, act8.sf))
     assert same(act8, act)
     assert torch.equal(moe.grouped_wgrad_fp8_alloc(t8, t8, o, R), moe.grouped_wgrad_fp8_alloc(t, t, o, R))
+
+
+# ---- whole sums asked for ---------------------------------------------------------------------
+
+WHOLE = {"64 rows": [(1, 1, 16, 16), (6, 9, 272, 2064), (90, 12, 528, 400), (40, 6, 2048, 2064)],
+         "128 rows": [(8, 220, 1648, 368), (64, 200, 1024, 1024), (30, 300, 1296, 400)]}
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("size", [s for sizes in WHOLE.values() for s in sizes])
+def test_whole_product(size, gather):
+    """Two products of 100352 that cancel in front of every sum take nothing from the others."""
+    E, mean, N, K = size
+    off, R, A, B, rows, a, b = _integers(E, mean, N, K, gather, True)
+    D = torch.full((R + 3, N), 7.5, dtype=torch.bfloat16, device="cuda")
+    moe.moe_grouped_gemm_fp8(moe.make_gemm_fp8_args(A.q, A.sf, B.q, B.sf, dev(off), R, moe.MOE_EPI_NONE | moe.MOE_SUMS_WHOLE, D, A_rows=rows))
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        assert torch.equal(D[lo:hi].double(), (a[lo:hi] @ b(e).T).bfloat16().double()), e
+    assert (D[R:] == 7.5).all()
+
+
+@pytest.mark.parametrize("size", [s for sizes in SWIGLU.values() for s in sizes])
+def test_whole_swiglu(size):
+    E, mean, N, K = size
+    off, R, A, B, rows, a, b = _integers(E, mean, N, K, True, True)
+    act = moe.grouped_gemm_fp8_alloc(A, B, dev(off), R, moe.MOE_EPI_SWIGLU_FP8 | moe.MOE_SUMS_WHOLE, rows)
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if hi > lo:
+            _check_act(moe.FP8Tensor(act.q[lo:hi], act.sf[lo:hi]), a[lo:hi] @ b(e).T, e)
+
+
+@pytest.mark.parametrize("E, mean, N, K", [(3, 20, 272, 2064), (8, 220, 1648, 368), (20, 400, 1040, 1040)])
+def test_whole_product_of_random_operands(E, mean, N, K):
+    """Within binary32 sums' bound and bf16's half step."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    off = np.concatenate([[0], np.cumsum(_sizes(E, mean))]).astype(np.int32)
+    R = int(off[-1])
+    A = moe.quantize_fp8_alloc(torch.randn(R, K, generator=g, device="cuda").bfloat16())
+    B = moe.quantize_fp8_weights_alloc(torch.randn(E, N, K, generator=g, device="cuda").bfloat16())
+    D = moe.grouped_gemm_fp8_alloc(A, B, dev(off), R, moe.MOE_EPI_NONE | moe.MOE_SUMS_WHOLE)
+    table = torch.from_numpy(ref.e4m3_values()).cuda()
+    up = lambda s, n, d: s.double().repeat_interleave(128, d).narrow(d, 0, n)
+    a = table[A.q.long()] * up(A.sf, K, 1)
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        w = table[B.q[e].long()] * up(up(B.sf[e], N, 0), K, 1)
+        y, mag = a[lo:hi] @ w.T, a[lo:hi].abs() @ w.abs().T
+        assert ((D[lo:hi].double() - y).abs() <= U16 * y.abs() + (1 + U16) * ref.sum_error(K) * mag).all(), e
+
+
+def test_whole_sums_do_not_depend_on_the_other_rows():
+    """A layer's output for its first tokens, alone and in a prompt, with a graph's replays between."""
+    E, k, H, I = 8, 2, 528, 256
+    g = torch.Generator(device="cuda").manual_seed(9)
+    randn = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    W1, W2 = (moe.quantize_fp8_weights_alloc((0.05 * randn(*s)).bfloat16()) for s in ((E, 2 * I, H), (E, H, I)))
+    logits, x = randn(3000, E), randn(3000, H).bfloat16()
+    run = lambda T: moe.MoEFP8LayerPlan(T, E, k, H, I, W1, W2, whole_sums=True).forward(logits[:T].contiguous(), x[:T].contiguous())
+    want = run(3000).view(torch.int16)
+    for T in (1, 7, 300):
+        assert torch.equal(run(T).view(torch.int16), want[:T]), T
+    plan = moe.MoEFP8LayerPlan(7, E, k, H, I, W1, W2, whole_sums=True)
+    l, y = logits[:7].clone(), x[:7].clone()
+    graph = plan.graph(l, y)
+    for first in (0, 40, 2000):
+        l.copy_(logits[first:first + 7])
+        y.copy_(x[first:first + 7])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(plan.out.view(torch.int16), want[first:first + 7]), first
+        run(300)
