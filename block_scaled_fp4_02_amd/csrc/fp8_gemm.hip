@@ -656,10 +656,10 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
 
 // ---- few items ------------------------------------------------------------------------------
 //
-// When 128-column tiles are fewer than the CUs (a single token: k experts' weights, each a few
-// hundred rows), the contraction is dealt to the eight waves of a workgroup: wave w takes the
-// scale blocks w, w + 8, ... of a tile of 32 columns (16 where tiles are very few: 7.9 us against 8.4
-// for the token below) and 16 rows, with a ring of its own and no barrier before the end, and the
+// Where there are few rows and columns (a single token: k experts' weights, each a few hundred
+// rows), the contraction is dealt to the eight waves of a workgroup: wave w takes the
+// scale blocks w, w + 8, ... of a tile of 32 columns (16 where even those are one round: 7.9 us against
+// 8.4 for the token below) and 16 rows, with a ring of its own and no barrier before the end, and the
 // eight partial tiles are added in order through LDS.  Bound by latency: the item lookup, about two
 // round trips to HBM and the sum.  One token, eight experts of 512 x 6144: 7.9 us (28 us in 64 x 128
 // tiles).
@@ -960,12 +960,24 @@ hipError_t run_split(GemmParams p, hipStream_t stream) {
 using Large = Tile<256, 256, 4, 2, 2>;
 constexpr int64_t kCacheBytes = 256 << 20;   // MI355X's memory-side cache
 // Fewer tiles leave CUs without one.  One group, N = K = 4096: of 1024 rows, 64 large tiles 55 us, 512
-// 64-row tiles 31; of 2048, 128 large tiles 59 us, 256 128-row tiles 46; of 64 rows, 32 64-row tiles
-// 23 us, the contraction split over waves 11.
+// 64-row tiles 31; of 2048, 128 large tiles 59 us, 256 128-row tiles 46.  N = K = 2048: of 4096 rows, 128
+// large tiles 34 us, 512 128-row tiles 27; of 6144, 192 and 768, 36 and 39.  N 8192, K 2048: of 1024
+// rows (128, 512) 34 and 27, of 2048 (256, 1024) 40 and 49.
 constexpr int kManyTiles = 192;
-// Rows per expert above which 64-row tiles read weights twice too often.  32 experts, N 4096, K 6144: of
-// 32 rows, 64-row tiles 136 us, large ones 140; of 50 rows 161 and 146; of 64 rows 215 and 149.
+// Rows per expert above which 64-row tiles read weights twice too often, in us of 64-row tiles and of
+// large ones, rows dealt to the experts at random.  32 experts, N 4096, K 6144: mean of 32 rows 136 and
+// 136; 44: 147 and 136; 64: 203 and 138.  64 experts, N = K = 2048: 44: 51 and 58; 64: 59 and 57; 80: 71
+// and 60.  32 experts, N 6144, K 2048: 50: 79 and 84; 56: 86 and 84; 64: 92 and 85.  128 experts, N 1024, K
+// 4096: 50: 124 and 133; 64: 124 and 134; 80: 155 and 136.  So the two meet between 32 and 70
+// rows: with 44 up to 18 % are lost (the last case just above it), with 64 up to 47 % would be (the first).
 constexpr int kLargeRows = 44;
+// The split tiles' rings take a CU's LDS, so a second round of workgroups costs as much as the first.
+// Groups of 8 rows, in us of 64-row tiles and of the split: N = K = 2048: 4 groups (256 split tiles) 9.4
+// and 7.0, 6 (384) 9.4 and 9.6, 8 (512) 9.6 and 10.8.  N 2048, K 6144: 4 groups 19.0 and 11.6, 6: 19.2 and
+// 17.4, 8: 19.6 and 21.0.  N 6144, K 1024: 1 group (192) 7.2 and 5.6, 4 (768) 7.3 and 14.1.  One group, N 2048, K
+// 2048: of 64 rows 12.5 and 7.2, of 256 (256 tiles) 12.5 and 8.1, of 384 (384) 12.6 and 13.1.  The 16-column
+// form against 32 columns, K 6144, N 512: 8 groups (256 tiles of 16 columns) 6.9 and 7.1, 10 (320) 10.8 and 7.4.
+constexpr int kCus = 256;
 
 template <class T, Mode MODE>
 hipError_t run_wgrad(const WgradParams &p, hipStream_t stream) {
@@ -992,19 +1004,29 @@ hipError_t launch_gemm(GemmParams p, bool swiglu, bool whole, hipStream_t stream
   }
   const bool middle = mean > 2 * kLargeRows && tiles(128, 128) >= kManyTiles;
   if (whole) {
+    // (32 experts, N 4096, K 2048, us in 128-row and in 64-row tiles: of 64 rows 80 and 72, of 96 83 and 99, of 512 320
+    // and 380; 16, N 2048, K 4096: of 96 rows 43 and 44, of 512 156 and 173)
     if (middle) return run_gemm<Tile<128, 128, 2, 2, 2>, kNone, true>(p, stream);
     return run_gemm<Tile<64, 128, 1, 4, 3>, kNone, true>(p, stream);
   }
   if (large) return run_gemm<Large, kNone, false>(p, stream);
-  if (tiles(64, 128) < kManyTiles && p.K >= 4 * kFp8Block) {
-    if (mean > 32) return run_split<Split<64, 32, 4, 3>>(p, stream);
-    if (mean > 16) return run_split<Split<32, 32, 8, 2>>(p, stream);
-    if (tiles(16, 32) >= kManyTiles) return run_split<Split<16, 32, 8, 3>>(p, stream);
-    return run_split<Split<16, 16, 8, 3>>(p, stream);
+  // q rows by c columns of groups of the mean size: at most one tile for each CU
+  auto one_round = [&](int q, int c) { return hit * ((mean + q - 1) / q) * ((p.N + c - 1) / c) <= kCus; };
+  if (p.K >= 4 * kFp8Block) {
+    if (mean > 32) {
+      if (one_round(64, 32)) return run_split<Split<64, 32, 4, 3>>(p, stream);
+    } else if (mean > 16) {
+      if (one_round(32, 32)) return run_split<Split<32, 32, 8, 2>>(p, stream);
+    } else if (one_round(16, 16)) {
+      return run_split<Split<16, 16, 8, 3>>(p, stream);
+    } else if (one_round(16, 32)) {
+      return run_split<Split<16, 32, 8, 3>>(p, stream);
+    }
   }
   if (middle) return run_gemm<Tile<128, 128, 2, 2, 2>, kNone, false>(p, stream);
   // two steps a tile: looking the item up takes as long (256 experts of 32 rows, N 6144, K 256: 119 us, one
-  // tile a workgroup 136; with K 512 no difference)
+  // tile a workgroup 136; with K 512 no difference; 32 of 64 rows, N 8192: K 128 18.0 and 19.6, K 256 22.5 and
+  // 25.7; 256 of 32, N 2048, K 256: 37.1 and 37.7, K 384: 58.3 and 55.9)
   if (p.K <= 2 * kFp8Block && tiles(64, 512) >= 4 * kManyTiles) return run_gemm<Tile<64, 128, 1, 4, 2>, kNone, false, 4>(p, stream);
   if (p.K <= 4 * kFp8Block) return run_gemm<Tile<64, 128, 1, 4, 2>, kNone, false>(p, stream);
   return run_gemm<Tile<64, 128, 1, 4, 3>, kNone, false>(p, stream);

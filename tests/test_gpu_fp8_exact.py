@@ -33,8 +33,12 @@ def kernel_of(R, E, N, K, swiglu=False):
         return "256 x 256" if large else "32 rows" if tiles(64, 256) < 192 else "64 rows"
     if large:
         return "256 x 256"
-    if tiles(64, 128) < 192 and K >= 512:
-        return "split 64" if mean > 32 else "split 32" if mean > 16 else "split 16" if tiles(16, 32) >= 192 else "split 16, 16 columns"
+    q = 64 if mean > 32 else 32 if mean > 16 else 16
+    one_round = lambda c: hit * -(-mean // q) * -(-N // c) <= 256
+    if K >= 512 and q == 16 and one_round(16):
+        return "split 16, 16 columns"
+    if K >= 512 and one_round(32):
+        return f"split {q}"
     if mean > 88 and tiles(128, 128) >= 192:
         return "128 x 128"
     if K <= 256 and tiles(64, 512) >= 768:
@@ -75,12 +79,12 @@ def _integers(E, mean, N, K, gather, wide):
 
 PRODUCTS = {
     "split 16, 16 columns": [(6, 9, 272, 2064), (1, 1, 16, 528)],
-    "split 16": [(8, 10, 784, 1040), (8, 16, 1040, 512)],
+    "split 16": [(8, 10, 784, 1040), (7, 16, 1040, 512)],
     "split 32": [(4, 26, 240, 1104), (9, 17, 528, 2064)],
     "split 64": [(3, 80, 400, 656), (2, 33, 1040, 1040)],
     "64 rows, four tiles": [(200, 12, 1616, 240), (256, 3, 2576, 16), (200, 70, 1024, 144)],
     "64 rows, two stages": [(90, 12, 528, 400), (5, 7, 48, 272)],
-    "64 rows": [(90, 20, 528, 1552), (40, 6, 2048, 2064)],      # the second one past the caches
+    "64 rows": [(90, 20, 528, 1552), (40, 6, 2048, 2064), (5, 48, 2064, 1040), (9, 1, 1040, 528)],      # the second one past the caches
     "128 x 128": [(8, 220, 1648, 368), (20, 130, 1040, 144)],
     "256 x 256": [(70, 70, 1040, 528), (64, 200, 1024, 1024), (72, 90, 2048, 1040), (30, 300, 1296, 400)],
 }
