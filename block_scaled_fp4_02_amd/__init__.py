@@ -726,6 +726,7 @@ class MoEFP8LayerPlan:
     def forward(self, logits, x, stream=None):
         _dense("MoEFP8LayerPlan.forward", ("logits", logits, _F32), ("x", x, _REAL), ("out", self.out, _BF16))
         _sized("MoEFP8LayerPlan.forward", logits.shape == (self.T, self.E) and x.shape == (self.T, self.H), "logits [T, E] and x [T, H] are needed")
+        _current("MoEFP8LayerPlan.forward", self.out.get_device(), stream)
         main = stream if stream is not None else torch.cuda.current_stream()
         moe_route_permute(logits, self.k, self.ids, self.w, self.off, self.row_src, self.tsr, self.ws_route, main)
         moe_quantize_fp8(x, self.xq.q, self.xq.sf, main)

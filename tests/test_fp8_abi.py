@@ -335,3 +335,13 @@ def test_whole_sums_are_asked_for_with_the_epilogue(tmp_path):
     assert L.moe_grouped_gemm_fp8_can_implement(C.byref(gemm_args(epilogue=whole | 3, N=384))) == UNSUPPORTED
     with open(os.path.join(ROOT, "include", "moe_nvfp4.h")) as f:
         assert f"MOE_SUMS_WHOLE = 0x{whole:x} " in f.read()
+
+
+def test_layer_refuses_tensors_of_another_device_before_its_first_launch():
+    """The routing call checks no device, so the plan has to before it."""
+    plan = object.__new__(moe.MoEFP8LayerPlan)
+    plan.T, plan.E, plan.k, plan.H, plan.I = 4, 2, 1, 256, 128
+    plan.out = torch.zeros(4, 256, dtype=torch.bfloat16)
+    with pytest.raises(moe.MoeError) as e:
+        plan.forward(torch.zeros(4, 2), torch.zeros(4, 256, dtype=torch.bfloat16))
+    assert e.value.status == UNSUPPORTED

@@ -279,3 +279,29 @@ def test_whole_sums_do_not_depend_on_the_other_rows():
         torch.cuda.synchronize()
         assert torch.equal(plan.out.view(torch.int16), want[first:first + 7]), first
         run(300)
+
+
+def test_layer_refuses_a_stream_of_another_device_before_its_first_launch():
+    class Elsewhere:
+        device_index, cuda_stream = 1, 0
+    E, k, H, I = 4, 2, 256, 128
+    g = torch.Generator(device="cuda").manual_seed(2)
+    W1, W2 = (moe.quantize_fp8_weights_alloc(torch.randn(*s, generator=g, device="cuda")) for s in ((E, 2 * I, H), (E, H, I)))
+    plan = moe.MoEFP8LayerPlan(5, E, k, H, I, W1, W2)
+    for t in (plan.ids, plan.off):
+        t.fill_(-5)
+    logits, x = torch.randn(5, E, generator=g, device="cuda"), torch.randn(5, H, generator=g, device="cuda")
+    with pytest.raises(moe.MoeError):
+        plan.forward(logits, x, Elsewhere())
+    torch.cuda.synchronize()
+    assert (plan.ids == -5).all() and (plan.off == -5).all()
+    assert not (plan.forward(logits, x, torch.cuda.current_stream()) != plan.forward(logits, x)).any()
+
+
+def test_layer_of_no_tokens():
+    z = lambda *s: moe.quantize_fp8_weights_alloc(torch.zeros(*s, device="cuda"))
+    for whole in (False, True):
+        plan = moe.MoEFP8LayerPlan(0, 4, 2, 256, 128, z(4, 256, 256), z(4, 256, 128), whole_sums=whole)
+        out = plan.forward(torch.empty(0, 4, device="cuda"), torch.empty(0, 256, device="cuda"))
+        torch.cuda.synchronize()
+        assert out.shape == (0, 256) and (plan.off == 0).all()
