@@ -17,7 +17,8 @@
 // and sums are whole, takes them: in wgrad_kernel, whose D may be binary32, and in the SwiGLU
 // epilogue's smaller tiles, whose act is rounded again to E4M3 (a code next to a border falls the
 // other way for the least difference: 1.3 to 1.6 times the error of the down projection's result,
-// against 4 % of a decode batch's time; the large tile, at half its rate with fp16, keeps FP8).
+// against 4 % of a decode batch's time; the large tile keeps FP8, a prompt's gate/up product taking 467 us
+// with it and 1027 with fp16).  MOE_SUMS_WHOLE takes the fp16 matrix core for every call.
 //
 // Both products have the same inner form.  The "row" operand P (weight rows; columns k of x)
 // gives the MFMA's rows, of which a lane holds 4 consecutive ones, so results are contiguous
@@ -315,9 +316,9 @@ __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps
 // step.  The last group of a row that has no whole number of groups starts at its fourth scale
 // from the end (a large tile has at least four steps).
 //
-// Measured, one group of 8192 rows, N = K = 8192 (1.1 TFLOP): 480 us, 2.3 PFLOP/s (128 x 128 tiles
-// 680 us).  What bounds it: the matrix cores are busy for half of the cycles at a clock that this
-// load holds near 2.0 GHz (the same launch on zeros takes 420 us; a loop of these MFMAs and fmas
+// Measured, one group of 8192 rows, N = K = 8192 (1.1 TFLOP): 472 us, 2.3 PFLOP/s (128 x 128 tiles
+// 680 us).  What bounds it: the matrix cores are busy for 56 % of the cycles at a clock that this
+// load holds at 1.9 GHz (the same launch on zeros takes 420 us; a loop of these MFMAs and fmas
 // alone runs at 3.5 PFLOP/s on random data, 4.5 on constants); writing D costs 25 us, the copies
 // from L2 some 30.
 constexpr int kLag = 4;   // an MFMA's result is read that many MFMAs later (3: the same within 1 %; 2: 3 % slower)
@@ -778,8 +779,9 @@ __global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams
 // ---- the weight gradient -----------------------------------------------------------------------
 //
 // A tile of D has a few steps (one per 128 tokens of its expert).  Measured, 16 experts of 512 rows, N
-// 4096, K 6144, binary32 D (412 GFLOP, 1.6 GB written): 600 us; 64 rows each: 300 us, 5.4 TB/s
-// written.  Per step and wave 64 MFMAs (1024 cycles) stand against 128 conversions and 128
+// 4096, K 6144, binary32 D (412 GFLOP, 1.6 GB written): 565 us (rows dealt at random, a
+// fifth, nearly empty block for some experts: 587), matrix cores busy for 34 % of the cycles; 64 rows
+// each: 300 us, 5.4 TB/s written.  Per step and wave 64 MFMAs (1024 cycles) stand against 128 conversions and 128
 // scalings (1024), which the MFMAs hide in part only.  One pipeline through several tiles, the
 // next one's first stage copied during the last step: 620 to 710 us.
 struct GradTile {
