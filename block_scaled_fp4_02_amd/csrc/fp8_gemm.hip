@@ -998,10 +998,15 @@ hipError_t launch_gemm(GemmParams p, bool swiglu, bool whole, hipStream_t stream
   p.stream_weights = static_cast<int64_t>(p.E) * p.N * p.K > kCacheBytes / 2;
   // tiles of q rows by c columns that there can be
   auto tiles = [&](int q, int c) { return groups::max_chunks(p.R, p.E, q) * ((p.N + c - 1) / c); };
+  // q rows by c columns of groups of the mean size: at most one tile for each CU
+  auto one_round = [&](int q, int c) { return hit * ((mean + q - 1) / q) * ((p.N + c - 1) / c) <= kCus; };
   const bool large = mean > kLargeRows && p.K > 3 * kFp8Block && tiles(256, 256) >= kManyTiles;
   if (swiglu) {
     if (large && !whole) return run_gemm<Large, kSwigluFp8, false>(p, stream);
-    if (tiles(64, 256) < kManyTiles) return run_gemm<Tile<32, 256, 1, 4, 3>, kSwigluFp8, true>(p, stream);
+    // fewer rows a tile while that makes no second round, in us of 32-row and of 64-row tiles: 8 experts, N
+    // 4096, K 6144, of 64 rows (256 tiles) 49 and 69, of 100 (512) 87 and 66; 32, N 1024, K 2048, of 64 rows (256)
+    // 20 and 25, of 100 (512) 35 and 26; 48, of 48 rows (384) 35 and 23; up to 32 rows no difference
+    if (one_round(32, 256)) return run_gemm<Tile<32, 256, 1, 4, 3>, kSwigluFp8, true>(p, stream);
     return run_gemm<Tile<64, 256, 1, 8, 3>, kSwigluFp8, true>(p, stream);
   }
   const bool middle = mean > 2 * kLargeRows && tiles(128, 128) >= kManyTiles;
@@ -1012,8 +1017,6 @@ hipError_t launch_gemm(GemmParams p, bool swiglu, bool whole, hipStream_t stream
     return run_gemm<Tile<64, 128, 1, 4, 3>, kNone, true>(p, stream);
   }
   if (large) return run_gemm<Large, kNone, false>(p, stream);
-  // q rows by c columns of groups of the mean size: at most one tile for each CU
-  auto one_round = [&](int q, int c) { return hit * ((mean + q - 1) / q) * ((p.N + c - 1) / c) <= kCus; };
   if (p.K >= 4 * kFp8Block) {
     if (mean > 32) {
       if (one_round(64, 32)) return run_split<Split<64, 32, 4, 3>>(p, stream);

@@ -323,8 +323,9 @@ moe_status moe_quantize_fp8_tokens(const void *x, int x_dtype, int64_t rows_x, c
  * each cut off at 2^-13 of the largest one's power of two, and those sums in binary32; the blocks
  * are summed in binary32, each times the binary32 product of its two scales.  (Where products of one
  * group of 8 cancel, what the small ones add may be lost: by more than the rounding of D to bf16,
- * though by less than the E4M3 rounding of the large ones.)  SWIGLU_FP8 with up to about 44 rows per
- * expert sums whole products.
+ * though by less than the E4M3 rounding of the large ones.)  SWIGLU_FP8 sums whole
+ * products outside the largest calls (up to 44 rows per expert with rows, K <= 384, or fewer than 192
+ * tiles of 256 x 256).
  * With MOE_SUMS_WHOLE in `epilogue` every product of either epilogue enters its sum whole and every
  * sum is binary32 (the fp16 matrix core on the exactly converted codes: 1.7 to 2.2 times the time of
  * large calls, a few per cent where reading the weights bounds them), in one order whatever the other

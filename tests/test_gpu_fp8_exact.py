@@ -29,15 +29,15 @@ def kernel_of(R, E, N, K, swiglu=False):
     mean = R // hit
     tiles = lambda q, c: (R // q + hit) * -(-N // c)
     large = mean > 44 and K > 384 and tiles(256, 256) >= 192
-    if swiglu:
-        return "256 x 256" if large else "32 rows" if tiles(64, 256) < 192 else "64 rows"
+    one_round = lambda q, c: hit * -(-mean // q) * -(-N // c) <= 256
     if large:
         return "256 x 256"
+    if swiglu:
+        return "32 rows" if one_round(32, 256) else "64 rows"
     q = 64 if mean > 32 else 32 if mean > 16 else 16
-    one_round = lambda c: hit * -(-mean // q) * -(-N // c) <= 256
-    if K >= 512 and q == 16 and one_round(16):
+    if K >= 512 and q == 16 and one_round(16, 16):
         return "split 16, 16 columns"
-    if K >= 512 and one_round(32):
+    if K >= 512 and one_round(q, 32):
         return f"split {q}"
     if mean > 88 and tiles(128, 128) >= 192:
         return "128 x 128"
@@ -121,8 +121,8 @@ def _check_act(act, y, what):
 
 
 SWIGLU = {
-    "32 rows": [(8, 5, 512, 1040), (3, 20, 256, 144), (1, 1, 256, 16)],
-    "64 rows": [(90, 20, 512, 528), (40, 6, 2048, 2064)],
+    "32 rows": [(8, 5, 512, 1040), (3, 70, 256, 144), (1, 1, 256, 16)],
+    "64 rows": [(150, 20, 512, 528), (9, 100, 2048, 144), (40, 6, 2048, 2064)],
     "256 x 256": [(70, 70, 1024, 528), (64, 200, 1024, 1024), (72, 90, 2048, 1040)],
 }
 
