@@ -12,7 +12,10 @@ an NVFP4 weight tensor into the packed layout once; :class:`MoELayerPlan` pre-al
 MoE layer's buffers and sequences its six calls.  The FP8 operators (:func:`moe_quantize_fp8` and its
 kin, :func:`moe_grouped_gemm_fp8`, :func:`moe_grouped_wgrad_fp8`, :class:`MoEFP8LayerPlan`) and the
 router's balance loss (:func:`moe_balance_loss`) check their tensors (dtype, strides, sizes,
-device) before they pass the pointers on.
+device) before they pass the pointers on, and so do the gated experts in bf16 with their backward pass
+(:func:`gated_ffn_alloc`, :func:`gated_ffn_backward_alloc`, :func:`moe_grouped_gemm_bf16`,
+:func:`moe_grouped_wgrad_bf16`), the clipping of gradients (:func:`clip_grad_norm`) and the products of
+single tokens with NVFP4 weights (:func:`moe_gemv_nvfp4`, :class:`MoETokenPlan`).
 """
 from __future__ import annotations
 
@@ -30,8 +33,9 @@ MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE
 MOE_DTYPE_BF16, MOE_DTYPE_F32 = 0, 1
 MOE_GS_STATIC, MOE_GS_DYNAMIC = 0, 1
 MOE_EPI_NONE, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_NVFP4, MOE_EPI_SWIGLU_FP8 = 0, 1, 2, 3
+MOE_EPI_SWIGLU_BACKWARD, MOE_EPI_FINALIZE = 4, 5
 MOE_SUMS_WHOLE = 0x100   # with an FP8 product's epilogue
-MOE_LAYOUT_ROWMAJOR, MOE_LAYOUT_PACKED = 0, 1
+MOE_LAYOUT_ROWMAJOR, MOE_LAYOUT_PACKED, MOE_LAYOUT_TRANSPOSED = 0, 1, 2
 
 EXPORTED = [
     "moe_status_string", "moe_last_hip_error",
@@ -45,6 +49,10 @@ EXPORTED = [
     "moe_grouped_gemm_fp8_can_implement", "moe_grouped_gemm_fp8",
     "moe_grouped_wgrad_fp8_can_implement", "moe_grouped_wgrad_fp8",
     "moe_balance_loss_workspace", "moe_balance_loss", "moe_balance_loss_backward",
+    "moe_grouped_gemm_bf16_can_implement", "moe_grouped_gemm_bf16",
+    "moe_grouped_wgrad_bf16_can_implement", "moe_grouped_wgrad_bf16",
+    "moe_grad_norm_workspace", "moe_grad_norm", "moe_grad_clip",
+    "moe_gemv_nvfp4_can_implement", "moe_gemv_nvfp4",
 ]
 
 
@@ -86,6 +94,36 @@ class moe_wgrad_fp8_args(C.Structure):
     ]
 
 
+class moe_gemm_bf16_args(C.Structure):
+    _fields_ = [
+        ("A", C.c_void_p), ("A_rows", C.c_void_p), ("rows_A", C.c_int64),
+        ("B", C.c_void_p), ("expert_offsets", C.c_void_p),
+        ("E", C.c_int32), ("N", C.c_int32), ("K", C.c_int32), ("epilogue", C.c_int32), ("B_layout", C.c_int32),
+        ("R", C.c_int64), ("D", C.c_void_p), ("Z", C.c_void_p),
+    ]
+
+
+class moe_wgrad_bf16_args(C.Structure):
+    _fields_ = [
+        ("Y", C.c_void_p), ("X", C.c_void_p), ("X_rows", C.c_void_p), ("rows_X", C.c_int64),
+        ("expert_offsets", C.c_void_p), ("E", C.c_int32), ("N", C.c_int32), ("K", C.c_int32),
+        ("D_dtype", C.c_int32), ("R", C.c_int64), ("D", C.c_void_p),
+    ]
+
+
+class moe_tensor(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32)]
+
+
+class moe_gemv_args(C.Structure):
+    _fields_ = [
+        ("x", C.c_void_p), ("rows_x", C.c_int64), ("B", C.c_void_p), ("B_sf", C.c_void_p), ("B_gs", C.c_void_p),
+        ("ids", C.c_void_p), ("topk_w", C.c_void_p),
+        ("T", C.c_int32), ("k", C.c_int32), ("E", C.c_int32), ("N", C.c_int32), ("K", C.c_int32),
+        ("epilogue", C.c_int32), ("B_layout", C.c_int32), ("D", C.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -100,6 +138,8 @@ def lib():
         P, i32, i64, sz = C.c_void_p, C.c_int, C.c_int64, C.c_size_t
         args_p = C.POINTER(moe_gemm_args)
         fp8_p, wgrad_p = C.POINTER(moe_gemm_fp8_args), C.POINTER(moe_wgrad_fp8_args)
+        bf16_p, bf16_wgrad_p = C.POINTER(moe_gemm_bf16_args), C.POINTER(moe_wgrad_bf16_args)
+        gemv_p = C.POINTER(moe_gemv_args)
         sig = {
             "moe_status_string": (C.c_char_p, [i32]),
             "moe_last_hip_error": (i32, []),
@@ -126,6 +166,15 @@ def lib():
             "moe_balance_loss_workspace": (sz, [i32, i32, i32, i32]),
             "moe_balance_loss": (i32, [P, P, i32, i32, i32, P, i32, P, P, P, P, P, sz, P]),
             "moe_balance_loss_backward": (i32, [P, i32, i32, P, i32, P, P, P, P, P, P, i32, P, P]),
+            "moe_grouped_gemm_bf16_can_implement": (i32, [bf16_p]),
+            "moe_grouped_gemm_bf16": (i32, [bf16_p, P]),
+            "moe_grouped_wgrad_bf16_can_implement": (i32, [bf16_wgrad_p]),
+            "moe_grouped_wgrad_bf16": (i32, [bf16_wgrad_p, P]),
+            "moe_grad_norm_workspace": (sz, [P, i32]),
+            "moe_grad_norm": (i32, [P, i32, P, P, sz, P]),
+            "moe_grad_clip": (i32, [P, i32, P, C.c_float, P]),
+            "moe_gemv_nvfp4_can_implement": (i32, [gemv_p]),
+            "moe_gemv_nvfp4": (i32, [gemv_p, P]),
         }
         for name, (res, argt) in sig.items():
             fn = getattr(L, name)
@@ -440,6 +489,149 @@ def moe_balance_loss_backward(logits, coef, grad_loss, dlogits, seq_offsets=None
         _at(d_topk_w), k, _at(dlogits), _stream(stream)))
 
 
+def make_gemm_bf16_args(A, B, expert_offsets, R, epilogue, D=None, Z=None, A_rows=None, B_layout=MOE_LAYOUT_ROWMAJOR) -> moe_gemm_bf16_args:
+    """A [rows_A, K] and B [E, N, K] (MOE_LAYOUT_TRANSPOSED: [E, K, N]) bf16; D [R, N] (NONE), [R, N/2] with
+    the pre-activations Z [R, N] or None (SWIGLU), [R, 2N] of Z [R, 2N] (SWIGLU_BACKWARD), all bf16.  The
+    tensors must outlive the arguments' use."""
+    fn = "make_gemm_bf16_args"
+    _dense(fn, ("A", A, _BF16), ("B", B, _BF16), ("expert_offsets", expert_offsets, _I32), ("D", D, _BF16), ("Z", Z, _BF16), ("A_rows", A_rows, _I32))
+    _sized(fn, A.dim() == 2 and B.dim() == 3, "A [rows_A, K] and B [E, N, K] or [E, K, N] are needed")
+    E, N, K = B.shape
+    if B_layout == MOE_LAYOUT_TRANSPOSED:
+        N, K = K, N
+    rows_A, R = A.shape[0], int(R)
+    cols_D, cols_Z = {MOE_EPI_SWIGLU: (N // 2, N), MOE_EPI_SWIGLU_BACKWARD: (2 * N, 2 * N)}.get(epilogue, (N, 0))
+    _sized(fn, A.shape[1] == K and expert_offsets.numel() == E + 1 and (A_rows is None or A_rows.numel() >= R)
+           and (D is None or D.numel() >= R * cols_D) and (Z is None or Z.numel() >= R * cols_Z), "operand sizes do not agree")
+    _current(fn, A.get_device())
+    args = moe_gemm_bf16_args(A.data_ptr(), _at(A_rows), rows_A, B.data_ptr(), expert_offsets.data_ptr(), E, N, K, epilogue, B_layout, R, _at(D), _at(Z))
+    args.device = A.get_device()
+    return args
+
+
+def moe_grouped_gemm_bf16_can_implement(args: moe_gemm_bf16_args) -> int:
+    return lib().moe_grouped_gemm_bf16_can_implement(C.byref(args))
+
+
+def moe_grouped_gemm_bf16(args: moe_gemm_bf16_args, stream=None):
+    if (at := getattr(args, "device", None)) is not None:   # (a caller may fill the structure without make_gemm_bf16_args)
+        _current("moe_grouped_gemm_bf16", at, stream)
+    _check("moe_grouped_gemm_bf16", lib().moe_grouped_gemm_bf16(C.byref(args), _stream(stream)))
+
+
+def make_wgrad_bf16_args(Y, X, expert_offsets, R, D, X_rows=None) -> moe_wgrad_bf16_args:
+    """Y [R, N] (permuted rows) and X [rows_X, K] bf16, D [E, N, K] f32 or bf16."""
+    fn = "make_wgrad_bf16_args"
+    _dense(fn, ("Y", Y, _BF16), ("X", X, _BF16), ("expert_offsets", expert_offsets, _I32), ("D", D, _REAL), ("X_rows", X_rows, _I32))
+    _sized(fn, D.dim() == 3 and Y.dim() == 2 and X.dim() == 2, "Y [R, N], X [rows_X, K] and D [E, N, K] are needed")
+    (E, N, K), R = D.shape, int(R)
+    _sized(fn, expert_offsets.numel() == E + 1 and Y.shape[0] >= R and Y.shape[1] == N and X.shape[1] == K
+           and (X_rows is None or X_rows.numel() >= R), "operand sizes do not agree")
+    _current(fn, D.get_device())
+    args = moe_wgrad_bf16_args(Y.data_ptr(), X.data_ptr(), _at(X_rows), X.shape[0], expert_offsets.data_ptr(), E, N, K, _DTYPES[D.dtype], R, D.data_ptr())
+    args.device = D.get_device()
+    return args
+
+
+def moe_grouped_wgrad_bf16_can_implement(args: moe_wgrad_bf16_args) -> int:
+    return lib().moe_grouped_wgrad_bf16_can_implement(C.byref(args))
+
+
+def moe_grouped_wgrad_bf16(args: moe_wgrad_bf16_args, stream=None):
+    if (at := getattr(args, "device", None)) is not None:   # (a caller may fill the structure without make_wgrad_bf16_args)
+        _current("moe_grouped_wgrad_bf16", at, stream)
+    _check("moe_grouped_wgrad_bf16", lib().moe_grouped_wgrad_bf16(C.byref(args), _stream(stream)))
+
+
+class GradList:
+    """The tensors of a gradient norm and its clipping, checked and laid out for the library once: `tensors`
+    f32 or bf16, dense, on one device; `out` (of the same sizes and types) receives the clipped values, None:
+    `tensors` themselves.  It holds the tensors, and may serve any number of calls."""
+
+    def __init__(self, tensors, out=None):
+        fn = "GradList"
+        self.tensors, self.out = list(tensors), None if out is None else list(out)
+        n = len(self.tensors)
+        _sized(fn, self.out is None or len(self.out) == n, "as many outputs as tensors are needed")
+        self.device = self.tensors[0].get_device() if n else None
+        self.items = (moe_tensor * max(n, 1))()
+        self.count = n
+        for i, t in enumerate(self.tensors):
+            o = t if self.out is None else self.out[i]
+            if t.dtype not in _DTYPES or o.dtype != t.dtype or not (t.is_contiguous() and o.is_contiguous()) \
+                    or t.get_device() != self.device or o.get_device() != self.device:
+                raise MoeError(fn, MOE_ERR_UNSUPPORTED, f"tensor {i}: dense f32 or bf16 tensors on one device are needed, outputs of the same type, "
+                               f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device} and {o.dtype} on {o.device}")
+            if o.numel() != t.numel():
+                raise MoeError(fn, MOE_ERR_SHAPE, f"tensor {i}: {t.numel()} elements, its output has {o.numel()}")
+            self.items[i] = (t.data_ptr(), None if o is t else o.data_ptr(), t.numel(), _DTYPES[t.dtype])
+
+
+def _grad_list(tensors, out=None) -> GradList:
+    if isinstance(tensors, GradList):
+        _sized("GradList", out is None, "a GradList has its outputs")
+        return tensors
+    return GradList(tensors, out)
+
+
+def moe_grad_norm_workspace(tensors) -> int:
+    g = _grad_list(tensors)
+    return lib().moe_grad_norm_workspace(g.items, g.count)
+
+
+def moe_grad_norm(tensors, norm, ws=None, stream=None):
+    """norm [1] f32 = the 2-norm of all elements of `tensors` (a list, or a GradList)."""
+    g = _grad_list(tensors)
+    _dense("moe_grad_norm", ("norm", norm, _F32), ("ws", ws, _U8))
+    _sized("moe_grad_norm", norm.numel() >= 1 and g.device in (None, norm.get_device()), "norm [1] on the tensors' device is needed")
+    _current("moe_grad_norm", norm.get_device(), stream)
+    if ws is None:
+        with _allocating(stream):
+            ws = _ws(lib().moe_grad_norm_workspace(g.items, g.count), norm.device)
+    _check("moe_grad_norm", lib().moe_grad_norm(g.items, g.count, _at(norm), _at(ws), ws.numel(), _stream(stream)))
+
+
+def moe_grad_clip(tensors, norm, max_norm, out=None, stream=None):
+    """out (None: `tensors`, or what the GradList has) = tensors * min(1, max_norm / (norm + 1e-6))."""
+    g = _grad_list(tensors, out)
+    _dense("moe_grad_clip", ("norm", norm, _F32))
+    _sized("moe_grad_clip", norm.numel() >= 1 and g.device in (None, norm.get_device()), "norm [1] on the tensors' device is needed")
+    _current("moe_grad_clip", norm.get_device(), stream)
+    _check("moe_grad_clip", lib().moe_grad_clip(g.items, g.count, _at(norm), float(max_norm), _stream(stream)))
+
+
+def make_gemv_args(x, B, ids=None, topk_w=None, epilogue=MOE_EPI_NONE, D=None) -> moe_gemv_args:
+    """x [T, K] bf16 (or [T*k, K], a row for each slot), B an NVFP4Tensor [E, N, K] or PackedWeights, ids
+    [T, k] i32 or None (one expert), topk_w [T, k] f32 (FINALIZE); D bf16 [T*k, N] (NONE), [T*k, N/2]
+    (SWIGLU), [T, N] (FINALIZE).  The tensors must outlive the arguments' use."""
+    fn = "make_gemv_args"
+    packed = isinstance(B, PackedWeights)
+    codes, sf = (B.data, None) if packed else (B.q, B.sf)
+    _dense(fn, ("x", x, _BF16), ("B", codes, _U8), ("B_sf", sf, _U8), ("B_gs", B.gs, _F32), ("ids", ids, _I32), ("topk_w", topk_w, _F32), ("D", D, _BF16))
+    _sized(fn, x.dim() == 2 and codes.dim() == (2 if packed else 3) and (ids is None or ids.dim() == 2), "x [rows, K], B [E, N, K] and ids [T, k] are needed")
+    E, (N, K) = codes.shape[0], (B.N, B.K) if packed else (codes.shape[1], 2 * codes.shape[2])
+    T, k = (x.shape[0], 1) if ids is None else ids.shape
+    cols, rows = (N // 2, T * k) if epilogue == MOE_EPI_SWIGLU else (N, T if epilogue == MOE_EPI_FINALIZE else T * k)
+    _sized(fn, x.shape[1] == K and x.shape[0] in (T, T * k) and B.gs.numel() == E
+           and (codes.numel() == E * N * K * 9 // 16 if packed else sf.numel() == E * N * K // 16)
+           and (topk_w is None or topk_w.numel() == T * k) and (D is None or D.numel() >= rows * cols), "operand sizes do not agree")
+    _current(fn, x.get_device())
+    args = moe_gemv_args(x.data_ptr(), x.shape[0], codes.data_ptr(), _at(sf), B.gs.data_ptr(), _at(ids), _at(topk_w), T, k, E, N, K, epilogue,
+                         MOE_LAYOUT_PACKED if packed else MOE_LAYOUT_ROWMAJOR, _at(D))
+    args.device = x.get_device()
+    return args
+
+
+def moe_gemv_nvfp4_can_implement(args: moe_gemv_args) -> int:
+    return lib().moe_gemv_nvfp4_can_implement(C.byref(args))
+
+
+def moe_gemv_nvfp4(args: moe_gemv_args, stream=None):
+    if (at := getattr(args, "device", None)) is not None:   # (a caller may fill the structure without make_gemv_args)
+        _current("moe_gemv_nvfp4", at, stream)
+    _check("moe_gemv_nvfp4", lib().moe_gemv_nvfp4(C.byref(args), _stream(stream)))
+
+
 # ---- allocating helpers ------------------------------------------------------------
 
 @dataclass
@@ -733,6 +925,110 @@ class MoEFP8LayerPlan:
         moe_grouped_gemm_fp8(self.args1, main)
         moe_grouped_gemm_fp8(self.args2, main)
         moe_finalize(self.Y, self.w, self.tsr, self.out, main)
+        return self.out
+
+    def graph(self, logits, x) -> "torch.cuda.CUDAGraph":
+        """As MoELayerPlan.graph: one forward pass over these input buffers, captured."""
+        self.forward(logits, x)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            self.forward(logits, x)
+        torch.cuda.synchronize()
+        return g
+
+
+def grouped_gemm_bf16_alloc(A: torch.Tensor, B: torch.Tensor, expert_offsets, R, A_rows=None, transposed=False, stream=None) -> torch.Tensor:
+    """D bf16 [R, N] of A [rows_A, K] and B [E, N, K]; `transposed`: B [E, K, N]."""
+    with _allocating(stream):
+        D = torch.empty(int(R), B.shape[2 if transposed else 1], dtype=torch.bfloat16, device=A.device)
+    moe_grouped_gemm_bf16(make_gemm_bf16_args(A, B, expert_offsets, R, MOE_EPI_NONE, D, A_rows=A_rows,
+                                              B_layout=MOE_LAYOUT_TRANSPOSED if transposed else MOE_LAYOUT_ROWMAJOR), stream)
+    return D
+
+
+def gated_ffn_alloc(x: torch.Tensor, W1: torch.Tensor, expert_offsets, R, A_rows=None, save=True, stream=None):
+    """(act [R, I], Z [R, 2I]) of x [rows, K] and W1 [E, 2I, K] (gate rows, then up rows): act = silu(gate) up,
+    and with `save` the pre-activations that gated_ffn_backward_alloc reads (else None)."""
+    N, R = W1.shape[1], int(R)
+    with _allocating(stream):
+        act = torch.empty(R, N // 2, dtype=torch.bfloat16, device=x.device)
+        Z = torch.empty(R, N, dtype=torch.bfloat16, device=x.device) if save else None
+    moe_grouped_gemm_bf16(make_gemm_bf16_args(x, W1, expert_offsets, R, MOE_EPI_SWIGLU, act, Z, A_rows), stream)
+    return act, Z
+
+
+def gated_ffn_backward_alloc(dY: torch.Tensor, W2: torch.Tensor, Z: torch.Tensor, expert_offsets, R, stream=None) -> torch.Tensor:
+    """dZ [R, 2I]: the gradient of the pre-activations Z, from that of the down projection's output dY [R, H]
+    and its weights W2 [E, H, I], in one product.  The rows' gradient is grouped_gemm_bf16_alloc(dZ, W1, ...,
+    transposed=True), the weights' grouped_wgrad_bf16_alloc(dZ, x, ...)."""
+    with _allocating(stream):
+        dZ = torch.empty(int(R), 2 * W2.shape[2], dtype=torch.bfloat16, device=dY.device)
+    moe_grouped_gemm_bf16(make_gemm_bf16_args(dY, W2, expert_offsets, R, MOE_EPI_SWIGLU_BACKWARD, dZ, Z, B_layout=MOE_LAYOUT_TRANSPOSED), stream)
+    return dZ
+
+
+def grouped_wgrad_bf16_alloc(dY: torch.Tensor, X: torch.Tensor, expert_offsets, R, X_rows=None, dtype=torch.float32, stream=None) -> torch.Tensor:
+    """dW [E, N, K] of the permuted rows dY [R, N] and X [rows, K]."""
+    with _allocating(stream):
+        D = torch.empty(expert_offsets.numel() - 1, dY.shape[1], X.shape[1], dtype=dtype, device=dY.device)
+    moe_grouped_wgrad_bf16(make_wgrad_bf16_args(dY, X, expert_offsets, R, D, X_rows), stream)
+    return D
+
+
+def clip_grad_norm(tensors, max_norm, out=None, stream=None) -> torch.Tensor:
+    """Clips `tensors` (a list, or a GradList) by their global norm, in place or into `out`, and returns the
+    norm before it, [1] f32 on the device."""
+    g = _grad_list(tensors, out)
+    device = torch.device("cuda", g.device if g.count else torch.cuda.current_device())
+    with _allocating(stream):
+        norm = torch.empty(1, dtype=torch.float32, device=device)
+    moe_grad_norm(g, norm, stream=stream)
+    moe_grad_clip(g, norm, max_norm, stream=stream)
+    return norm
+
+
+def gemv_nvfp4_alloc(x: torch.Tensor, B, ids=None, topk_w=None, epilogue=MOE_EPI_NONE, stream=None) -> torch.Tensor:
+    """D of make_gemv_args, allocated."""
+    N = B.N if isinstance(B, PackedWeights) else B.q.shape[1]
+    T, k = (x.shape[0], 1) if ids is None else ids.shape
+    with _allocating(stream):
+        D = torch.empty(T if epilogue == MOE_EPI_FINALIZE else T * k, N // 2 if epilogue == MOE_EPI_SWIGLU else N, dtype=torch.bfloat16, device=x.device)
+    moe_gemv_nvfp4(make_gemv_args(x, B, ids, topk_w, epilogue, D), stream)
+    return D
+
+
+class MoETokenPlan:
+    """The layer of MoELayerPlan for one or a few tokens: the same weights (NVFP4Tensor or PackedWeights), the
+    tokens and activations left in bf16, and three calls: routing, gate/up products with SwiGLU, down products
+    with the weighted sum.  Buffers are allocated once."""
+
+    def __init__(self, T: int, E: int, k: int, H: int, I: int, W1, W2, device="cuda"):
+        self.T, self.E, self.k, self.H, self.I = T, E, k, H, I
+        dev = torch.device(device)
+        z = lambda *s, dt: torch.empty(*s, dtype=dt, device=dev)
+        self.ids, self.w = z(T, k, dt=torch.int32), z(T, k, dt=torch.float32)
+        self.off, self.row_src, self.tsr = z(E + 1, dt=torch.int32), z(T * k, dt=torch.int32), z(T * k, dt=torch.int32)
+        self.x, self.act, self.out = z(T, H, dt=torch.bfloat16), z(T * k, I, dt=torch.bfloat16), z(T, H, dt=torch.bfloat16)
+        self.W1, self.W2 = W1, W2
+        self.args1 = make_gemv_args(self.x, W1, self.ids, None, MOE_EPI_SWIGLU, self.act)
+        self.args2 = make_gemv_args(self.act, W2, self.ids, self.w, MOE_EPI_FINALIZE, self.out)
+        _sized("MoETokenPlan", (self.args1.E, self.args1.N, self.args1.K) == (E, 2 * I, H)
+               and (self.args2.E, self.args2.N, self.args2.K) == (E, H, I), "W1 [E, 2I, H] and W2 [E, H, I] are needed")
+        for a in (self.args1, self.args2):
+            _check("moe_gemv_nvfp4_can_implement", moe_gemv_nvfp4_can_implement(a))
+        self.ws_route = _ws(lib().moe_route_permute_workspace(T, E, k), dev)
+
+    def forward(self, logits, x, stream=None):
+        fn = "MoETokenPlan.forward"
+        _dense(fn, ("logits", logits, _F32), ("x", x, _BF16), ("out", self.out, _BF16))
+        _sized(fn, logits.shape == (self.T, self.E) and x.shape == (self.T, self.H), "logits [T, E] and x [T, H] are needed")
+        _current(fn, self.out.get_device(), stream)
+        main = stream if stream is not None else torch.cuda.current_stream()
+        moe_route_permute(logits, self.k, self.ids, self.w, self.off, self.row_src, self.tsr, self.ws_route, main)
+        self.args1.x = x.data_ptr()
+        moe_gemv_nvfp4(self.args1, main)
+        moe_gemv_nvfp4(self.args2, main)
         return self.out
 
     def graph(self, logits, x) -> "torch.cuda.CUDAGraph":

@@ -18,7 +18,7 @@ BUILD_DIR = os.path.join(ROOT, "_build", "moe_nvfp4")
 LIB_PATH = os.path.join(PKG, "libmoe_nvfp4.so")
 SOURCES = ["route_permute.hip", "quantize.hip", "grouped_gemm.hip", "gemm_lds.hip", "gemm_ksplit.hip",
            "gemm_rowmajor.hip", "finalize.hip", "moe_api.hip", "fp8_quantize.hip", "fp8_gemm.hip",
-           "balance_loss.hip", "fp8_api.hip"]
+           "balance_loss.hip", "fp8_api.hip", "bf16_gemm.hip", "grad_clip.hip", "gemv_nvfp4.hip", "experts_api.hip"]
 # the benchmark's measurement kernels (streaming read, MFMA throughput), a library of their own
 # (not the MoE ABI)
 PROBE_SOURCES = ["stream_probe.hip", "mfma_probe.hip"]

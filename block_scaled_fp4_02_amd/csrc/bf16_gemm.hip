@@ -1,0 +1,859 @@
+// Grouped bf16 matrix products of an expert layer's training: the forward product and the input
+// gradient with their epilogues (gemm_kernel, split_kernel), and the weight gradient (wgrad_kernel).
+//
+//   y[p, n]     = sum_k a[r, k] b[e, n, k]      or, b transposed, sum_k a[r, k] b[e, k, n]
+//   gated:        g = y[p, i], u = y[p, I + i]; act = silu(g) u, with g and u kept on request
+//   backward:     y = d act; dg = y u s (1 + g (1 - s)), du = y g s, s = sigmoid(g), of the kept g, u
+//   dW[e, n, k] = sum_p dy[p, n] x[r, k]        over the rows p of group e
+//
+// The bf16 matrix core's products are whole and its sums binary32; one 16x16x32 MFMA takes 8
+// consecutive elements of the contraction from each of four lane groups.  The "row" operand P
+// (weight rows n; columns k of dW) gives the MFMA's rows, of which a lane holds 4 consecutive ones, so
+// results are contiguous along P; the "column" operand Q (tokens; rows n of dW) gives its columns.
+//
+// A stage holds 64 elements of the contraction of both operands, in panels of 128 rows or columns
+// (16 KB), copied from memory straight into LDS (16 bytes per lane, no registers).  An operand whose
+// rows run along the contraction keeps 128 bytes of a row together in 8 pieces; row r has piece c at
+// place c ^ ((r >> 1) & 7), so the 16 rows that 16 lanes read together fall on all 64 banks once.  An
+// operand whose rows run across it (b transposed, both operands of dW) keeps 256 bytes of each of 64
+// rows, in 8 pairs of pieces of 16 columns, and is read through the transposing LDS load: 16 lanes
+// read four rows of a pair and each gets one column's four elements.  Row k has pair c at place c ^
+// (k & 3 | (k >> 3 & 1) << 2): the eight rows that 32 lanes read together fall on all banks once.
+// The copies are range-checked and what lies outside an operand arrives as zeros, in both
+// operands, so nothing outside (a NaN, an infinity) meets a zero.
+#include "bf16_gemm.hpp"
+#include "groups.hpp"
+#include "lds_tiles.hpp"
+
+#include <type_traits>
+
+#pragma clang fp contract(off)
+
+namespace moe {
+namespace bf16 {
+namespace {
+
+using namespace lds;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short short4v __attribute__((ext_vector_type(4)));
+typedef short short8v __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) short4v lds_short4;
+
+constexpr int kStep = 64;            // elements of the contraction in a stage
+constexpr int kPanelCols = 128;      // rows or columns of an operand in a panel
+constexpr int kPanel = kPanelCols * kStep * 2;   // bytes
+constexpr int kRowBytes = kStep * 2; // of a row along the contraction
+constexpr int kAcross = kPanelCols * 2;          // bytes of a row across the contraction
+
+// ---- one tile -----------------------------------------------------------------------------
+
+// PT, QT: the operand's rows run across the contraction.
+template <int BQ_, int BP_, int WQ_, int WP_, int STAGES_, bool PT_, bool QT_ = false>
+struct Tile {
+  static constexpr int BQ = BQ_, BP = BP_, WQ = WQ_, WP = WP_, STAGES = STAGES_;
+  static constexpr bool PT = PT_, QT = QT_;
+  static constexpr int kWaves = WQ * WP, kThreadsT = kWaves * kWave;
+  static constexpr int kHalves = BP / kPanelCols;            // panels of P
+  static constexpr int kPerHalf = kPanelCols / WP / 16;      // a wave's 16-row tiles in each panel
+  static constexpr int TP = kHalves * kPerHalf, TQ = BQ / WQ / 16;
+  static constexpr int kCopiesP = BP / 8 / kWaves;           // copies of 1 KB per wave and stage
+  static constexpr int kCopiesQ = (BQ / 8 + kWaves - 1) / kWaves;
+  static constexpr int kCopies = kCopiesP + kCopiesQ;
+  static constexpr int kBytesP = BP * kRowBytes, kBytesQ = kCopiesQ * kWaves * 1024;
+  static constexpr int kStage = kBytesP + kBytesQ;
+  static constexpr bool kLarge = BQ == 256 && BP == 256;     // contract_large
+  static constexpr int kLds = STAGES * kStage;
+  static_assert(BP % kPanelCols == 0 && BP / 8 % kWaves == 0 && BQ % (16 * WQ) == 0 && kPerHalf >= 1, "tile split");
+  static_assert(!QT || BQ % kPanelCols == 0, "whole panels");
+  static_assert(STAGES >= 2 && kCopies * (STAGES - 2) < 64, "copies under way fit the counter");
+};
+
+// Copy number j of a wave's stage of P among all copies of the stage: in the large tile a wave copies
+// as many of either panel.
+template <class T>
+__device__ __forceinline__ int copy_p(int wave, int j) {
+  constexpr int kHalf = T::kCopiesP / 2;
+  return T::kLarge ? j / kHalf * 16 + wave * kHalf + j % kHalf : wave * T::kCopiesP + j;
+}
+
+// What copy number c moves in this lane.  Along: 16-byte piece `piece` of row `row` of the operand.
+// Across: row `k` of the stage, columns from `col`.
+__device__ __forceinline__ void place_along(int c, int &row, int &piece) {
+  const int lane = threadIdx.x & 63;
+  row = c * 8 + lane / 8;
+  piece = (lane & 7) ^ ((row >> 1) & 7);
+}
+__device__ __forceinline__ int swizzle_across(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
+__device__ __forceinline__ void place_across(int c, int &k, int &col) {
+  const int lane = threadIdx.x & 63;
+  k = c % 16 * 4 + lane / 16;
+  const int pair = ((lane & 15) >> 1) ^ swizzle_across(k);
+  col = c / 16 * kPanelCols + pair * 16 + (lane & 1) * 8;
+}
+
+// Where one lane's copies of a stage come from: byte offsets of its pieces in the two buffers (kOob:
+// nothing) and what the buffers advance per stage.  `last`: elements of the contraction in the last stage.
+template <class T>
+struct Source {
+  Buf p, q;
+  uint32_t vp[T::kCopiesP], vq[T::kCopiesQ];
+  uint32_t step_p, step_q;
+  int last;
+};
+
+// This lane's offset in copy c: nothing if the contraction ends before its piece.
+template <bool ACROSS>
+__device__ __forceinline__ uint32_t in_range(uint32_t voff, int c, bool is_last, int last) {
+  int a, b;
+  if (ACROSS) place_across(c, a, b);
+  else place_along(c, b, a), a *= 8;
+  return is_last && a >= last ? kOob : voff;
+}
+
+template <class T, bool ONCE, int FROM, int TO>
+__device__ __forceinline__ void issue_p(const Source<T> &src, uint32_t lds, int wave, bool is_last) {
+#pragma unroll
+  for (int j = FROM; j < TO; j++) {
+    const int c = copy_p<T>(wave, j);
+    copy16<ONCE>(src.p, lds + c * 1024, in_range<T::PT>(src.vp[j], c, is_last, src.last));
+  }
+}
+template <class T>
+__device__ __forceinline__ void issue_q(const Source<T> &src, uint32_t lds, int wave, bool is_last) {
+#pragma unroll
+  for (int j = 0; j < T::kCopiesQ; j++) {
+    const int c = wave * T::kCopiesQ + j;
+    copy16(src.q, lds + T::kBytesP + c * 1024, in_range<T::QT>(src.vq[j], c, is_last, src.last));
+  }
+}
+
+// The copies of stage `kb` into the buffer at `lds`; beyond the last stage they move nothing.
+template <class T, bool ONCE>
+__device__ __forceinline__ void issue(Source<T> &src, uint32_t lds, int wave, int kb, int steps) {
+  const bool is_last = kb == steps - 1 && src.last < kStep;
+  if (kb >= steps) src.p.bytes = src.q.bytes = 0;
+  issue_p<T, ONCE, 0, T::kCopiesP>(src, lds, wave, is_last);
+  issue_q<T>(src, lds, wave, is_last);
+  src.p.base += src.step_p;
+  src.q.base += src.step_q;
+}
+
+// Elements [32 h + 8 g, + 8) of the stage, for lane group g, of row `row` of an operand along it ...
+__device__ __forceinline__ bf16x8 along(const uint8_t *rows, int row, int h, int g) {
+  return *reinterpret_cast<const bf16x8 *>(rows + row * kRowBytes + ((4 * h + g) ^ ((row >> 1) & 7)) * 16);
+}
+// ... or of column r of the 16 from `tile` * 16 of an operand across it.
+__device__ __forceinline__ bf16x8 across(const uint8_t *operand, int tile, int h, int g, int r) {
+  const int k = 32 * h + 8 * g + (r >> 2);   // and k + 4, whose swizzle is the same
+  const uint8_t *at = operand + tile / 8 * kPanel + k * kAcross + ((tile % 8) ^ ((r >> 2) | (g & 1) << 2)) * 32 + (r & 3) * 8;
+  const short4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)at);
+  const short4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(at + 4 * kAcross));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// The wave's 16-row tile i of panel `half` of P, and its column tile j of Q.
+template <class T>
+__device__ __forceinline__ bf16x8 fragment_p(const uint8_t *P, int wp, int half, int i, int h, int g, int r) {
+  const int tile = half * (kPanelCols / 16) + wp * T::kPerHalf + i;
+  if constexpr (T::PT) return across(P, tile, h, g, r);
+  else return along(P, tile * 16 + r, h, g);
+}
+template <class T>
+__device__ __forceinline__ bf16x8 fragment_q(const uint8_t *Q, int wq, int j, int h, int g, int r) {
+  const int tile = wq * T::TQ + j;
+  if constexpr (T::QT) return across(Q, tile, h, g, r);
+  else return along(Q, tile * 16 + r, h, g);
+}
+
+template <class T>
+__device__ __forceinline__ void clear(float4v (&acc)[T::TP][T::TQ]) {
+#pragma unroll
+  for (int i = 0; i < T::TP; i++)
+#pragma unroll
+    for (int j = 0; j < T::TQ; j++) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
+}
+
+// The whole contraction of one tile; ACTIVE of the wave's TQ column tiles are in use.
+template <class T, bool ONCE, int ACTIVE>
+__device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps, float4v (&acc)[T::TP][T::TQ]) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x & 63, g = lane / 16, r = lane % 16;
+  const int wp = wave % T::WP, wq = wave / T::WP;
+  const uint32_t lds0 = lds_address(lds);
+  clear<T>(acc);
+#pragma unroll
+  for (int s = 0; s < T::STAGES - 1; s++) issue<T, ONCE>(src, lds0 + s * T::kStage, wave, s, steps);
+  int slot = 0;
+  for (int kb = 0; kb < steps; kb++) {
+    arrive<T::kCopies *(T::STAGES - 2)>();
+    const int next = slot == 0 ? T::STAGES - 1 : slot - 1;
+    issue<T, ONCE>(src, lds0 + next * T::kStage, wave, kb + T::STAGES - 1, steps);
+    const uint8_t *P = lds + slot * T::kStage, *Q = P + T::kBytesP;
+    bf16x8 q[2][ACTIVE];
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+      for (int j = 0; j < ACTIVE; j++) q[h][j] = fragment_q<T>(Q, wq, j, h, g, r);
+#pragma unroll
+    for (int i = 0; i < T::TP; i++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const bf16x8 p = fragment_p<T>(P, wp, i / T::kPerHalf, i % T::kPerHalf, h, g, r);
+#pragma unroll
+        for (int j = 0; j < ACTIVE; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, q[h][j], acc[i][j], 0, 0, 0);
+      }
+    slot = slot == T::STAGES - 1 ? 0 : slot + 1;
+  }
+  arrive<0>();   // the copies past the end (zeros) are in before the buffers serve anything else
+}
+
+// ---- the large tile -------------------------------------------------------------------------
+//
+// 256 x 256 results in eight waves, two on each SIMD, each 128 P rows (64 of either panel) by 64 Q
+// rows.  A step has four phases per wave: read panel 0 of P and all of Q from LDS into registers, 32
+// MFMAs, read panel 1 of P, 32 MFMAs.  Two workgroup barriers a step, after an MFMA phase of waves
+// 0-3 and a reading phase of waves 4-7, keep the two halves of the workgroup one phase apart, so on
+// every SIMD one wave's matrix instructions run while the other reads.  A stage has two parts, X (Q,
+// panel 0 of P) and Y (panel 1 of P), whose buffers are free again at the next barrier after they were
+// read: part X of step b + 2 is copied in the reading phase of panel 1 of step b, part Y of step b + 1
+// in that of panel 0, about six phases before they are read.
+
+template <class T>
+__device__ __forceinline__ void mfma_half(const bf16x8 (&p)[2][T::kPerHalf], const bf16x8 (&q)[2][T::TQ], float4v (*acc)[T::TQ]) {
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int h = 0; h < 2; h++)
+#pragma unroll
+    for (int i = 0; i < T::kPerHalf; i++)
+#pragma unroll
+      for (int j = 0; j < T::TQ; j++)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p[h][i], q[h][j], acc[i][j], 0, 0, 0);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Copies that may be under way at a barrier: the two parts issued after the one it waits for.
+template <class T>
+constexpr int kLaterCopies = T::kCopiesQ + T::kCopiesP;
+
+// BEHIND: waves 4-7, whose barriers follow their reading phases.  issue_x and issue_y issue the parts
+// of a step.
+template <class T, bool BEHIND, class X, class Y>
+__device__ __forceinline__ void large_loop(X issue_x, Y issue_y, const uint8_t *lds, int steps, int wave, float4v (&acc)[T::TP][T::TQ]) {
+  constexpr int kLater = kLaterCopies<T>;
+  const int lane = threadIdx.x & 63, g = lane / 16, r = lane % 16;
+  const int wp = wave % T::WP, wq = wave / T::WP;
+  for (int kb = 0; kb < steps; kb++) {
+    const uint8_t *P = lds + (kb & 1) * T::kStage, *Q = P + T::kBytesP;
+    bf16x8 p[2][T::kPerHalf], q[2][T::TQ];
+    issue_y(kb + 1);
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+#pragma unroll
+      for (int j = 0; j < T::TQ; j++) q[h][j] = fragment_q<T>(Q, wq, j, h, g, r);
+#pragma unroll
+      for (int i = 0; i < T::kPerHalf; i++) p[h][i] = fragment_p<T>(P, wp, 0, i, h, g, r);
+    }
+    if (BEHIND) arrive<kLater>();    // part Y of this step is there
+    mfma_half<T>(p, q, acc);
+    if (!BEHIND) arrive<kLater>();
+    issue_x(kb + 2);
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+      for (int i = 0; i < T::kPerHalf; i++) p[h][i] = fragment_p<T>(P, wp, 1, i, h, g, r);
+    if (BEHIND) arrive<kLater>();    // part X of the next step is there
+    mfma_half<T>(p, q, acc + T::kPerHalf);
+    if (!BEHIND) arrive<kLater>();
+  }
+}
+
+// `cols`: rows of Q in use; a wave whose 64 are all behind them only copies.
+template <class T, class X, class Y>
+__device__ __forceinline__ void contract_large(X issue_x, Y issue_y, const uint8_t *lds, int steps, int cols, float4v (&acc)[T::TP][T::TQ]) {
+  static_assert(T::kWaves == 8 && T::WP == 2 && T::kHalves == 2 && T::STAGES == 2, "the schedule above");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  constexpr int kLater = kLaterCopies<T>;
+  clear<T>(acc);
+  issue_x(0);
+  issue_y(0);
+  issue_x(1);
+  arrive<kLater>();                  // part X of step 0 is there
+  if (wave / T::WP * T::TQ * 16 >= cols) {
+    for (int kb = 0; kb < steps; kb++) {
+      issue_y(kb + 1);
+      arrive<kLater>();
+      issue_x(kb + 2);
+      arrive<kLater>();
+    }
+  } else if (wave >= T::kWaves / 2) {
+    large_loop<T, true>(issue_x, issue_y, lds, steps, wave, acc);
+  } else {
+    large_loop<T, false>(issue_x, issue_y, lds, steps, wave, acc);
+  }
+  arrive<0>();
+}
+
+// ---- results --------------------------------------------------------------------------------
+
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
+}
+
+// Each wave turns 16 rows of its results at a time around in LDS (or a few times 16, to have a piece
+// for every lane), NT tiles of P wide, and hands whole 16-byte pieces of them to store(row of the
+// wave's Q rows, column of its NT * 16, piece).
+template <class T, int NT, class V, class S>
+__device__ __forceinline__ void turn(uint8_t *lds, V value, S store) {
+  constexpr int kRow = NT * 32, kStride = kRow + 16;   // bytes
+  constexpr int kTurn = kRow < kWave ? kWave / kRow : 1;
+  constexpr int kPieces = kTurn * kRow / kWave;
+  static_assert(T::TQ % kTurn == 0 && kPieces * kWave == kTurn * kRow && T::kWaves * kTurn * 16 * kStride <= T::kLds, "staging");
+  const int lane = threadIdx.x & 63, lg = lane / 16, r = lane % 16;
+  uint8_t *mine = lds + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * kTurn * 16 * kStride;
+#pragma unroll
+  for (int j0 = 0; j0 < T::TQ; j0 += kTurn) {
+#pragma unroll
+    for (int j = 0; j < kTurn; j++)
+#pragma unroll
+      for (int ti = 0; ti < NT; ti++) *reinterpret_cast<uint2 *>(mine + (j * 16 + r) * kStride + ti * 32 + lg * 8) = bf16x4(value(ti, j0 + j));
+    wave_order();
+#pragma unroll
+    for (int c = 0; c < kPieces; c++) {
+      const int at = c * kWave + lane, row = at / (kRow / 16), col = at % (kRow / 16) * 8;
+      store(j0 * 16 + row, col, *reinterpret_cast<const uint4 *>(mine + row * kStride + col * 2));
+    }
+    wave_order();
+  }
+}
+
+// The same with binary32 values, handed over as 8 at a time.
+template <class T, int NT, class S>
+__device__ __forceinline__ void turn_f32(uint8_t *lds, const float4v (&acc)[NT][T::TQ], S store) {
+  constexpr int kRow = NT * 64, kStride = kRow + 16, kPieces = kRow / 128;   // bytes
+  static_assert(kPieces >= 1 && kPieces * 128 == kRow && T::kWaves * 16 * kStride <= T::kLds, "staging");
+  const int lane = threadIdx.x & 63, lg = lane / 16, r = lane % 16;
+  uint8_t *mine = lds + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * 16 * kStride;
+#pragma unroll
+  for (int j = 0; j < T::TQ; j++) {
+#pragma unroll
+    for (int ti = 0; ti < NT; ti++) *reinterpret_cast<float4v *>(mine + r * kStride + ti * 64 + lg * 16) = acc[ti][j];
+    wave_order();
+#pragma unroll
+    for (int c = 0; c < kPieces; c++) {
+      const int at = c * kWave + lane, row = at / (kRow / 32), col = at % (kRow / 32) * 8;
+      const float4v *v = reinterpret_cast<const float4v *>(mine + row * kStride + col * 4);
+      store(j * 16 + row, col, v[0], v[1]);
+    }
+    wave_order();
+  }
+}
+
+__device__ __forceinline__ float element(const uint4 &v, int i) {
+  const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+  return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+}
+
+// ---- the product ----------------------------------------------------------------------------
+
+// The item of this workgroup: group g, its chunk of `size` rows and n tile.
+__device__ __forceinline__ bool find_item(const GemmParams &P, int size, groups::Chunk &g, int &chunk, int &nt) {
+  int64_t w = 0;
+  int i;
+  auto index = [&](int total) {
+    return item_of(blockIdx.x, static_cast<int64_t>(total) * P.n_tiles, w) ? static_cast<int>(w / P.n_tiles) : -1;
+  };
+  if (!groups::find_chunk_of_all(P.offsets, P.E, P.R, size, index, i, g)) return false;
+  place_in_band(static_cast<int>(w - static_cast<int64_t>(i - g.index) * P.n_tiles), g.total, P.n_tiles, chunk, nt);
+  return true;
+}
+
+// Row number v of an operand of `rows` rows, kept inside it.
+__device__ __forceinline__ int64_t clamped(int64_t v, int64_t rows) { return v < 0 ? 0 : (v >= rows ? rows - 1 : v); }
+
+template <class T, Epilogue MODE>
+__global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) {
+  static_assert(MODE != kGated || (T::kHalves == 2 && !T::PT), "gate and up panels");
+  __shared__ __align__(1024) uint8_t lds[T::kLds];
+  groups::Chunk g;
+  int chunk, nt;
+  if (!find_item(P, T::BQ, g, chunk, nt)) return;
+  const int first = g.lo + chunk * T::BQ, count = min(T::BQ, g.hi - first);
+  const int width = MODE == kGated ? P.N / 2 : P.N;   // columns of act, or of y
+  const int n0 = nt * (MODE == kGated ? kPanelCols : T::BP);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+
+  Source<T> src;
+  const int steps = (P.K + kStep - 1) / kStep;
+  src.last = P.K - (steps - 1) * kStep;
+  src.p.base = reinterpret_cast<uint64_t>(P.B) + static_cast<uint64_t>(g.group) * P.N * P.K * 2;
+  src.p.bytes = static_cast<uint32_t>(P.N) * P.K * 2;
+  src.step_p = T::PT ? static_cast<uint32_t>(P.N) * kStep * 2 : kRowBytes;
+#pragma unroll
+  for (int j = 0; j < T::kCopiesP; j++) {
+    const int c = copy_p<T>(wave, j);
+    if (T::PT) {
+      int k, col;
+      place_across(c, k, col);
+      src.vp[j] = n0 + col < P.N ? (static_cast<uint32_t>(k) * P.N + n0 + col) * 2 : kOob;
+    } else {
+      int row, piece;
+      place_along(c, row, piece);
+      const int i = n0 + (MODE == kGated ? row % kPanelCols : row);
+      const int n = MODE == kGated ? i + row / kPanelCols * width : i;
+      src.vp[j] = i < width ? static_cast<uint32_t>(n) * P.K * 2 + piece * 16 : kOob;
+    }
+  }
+  // token rows: gathered from all of A, or the group's own
+  const bool gather = P.A_rows != nullptr;
+  src.q.base = reinterpret_cast<uint64_t>(P.A) + (gather ? 0 : static_cast<uint64_t>(first) * P.K * 2);
+  src.q.bytes = static_cast<uint32_t>((gather ? P.rows_A : count) * P.K * 2);
+  src.step_q = kRowBytes;
+#pragma unroll
+  for (int j = 0; j < T::kCopiesQ; j++) {
+    int row, piece;
+    place_along(wave * T::kCopiesQ + j, row, piece);
+    src.vq[j] = kOob;
+    if (row < count) {
+      const int64_t a = gather ? clamped(P.A_rows[first + row], P.rows_A) : row;
+      src.vq[j] = static_cast<uint32_t>(a) * P.K * 2 + piece * 16;
+    }
+  }
+
+  float4v acc[T::TP][T::TQ];
+  // the weights of a group of one chunk are read by this workgroup alone
+  const bool once = g.total == 1 && P.stream_weights;
+  if constexpr (T::kLarge) {
+    const uint32_t lds0 = lds_address(lds);
+    auto large = [&](auto streamed) {
+      constexpr bool kOnce = decltype(streamed)::value;
+      contract_large<T>(
+          [&](int kb) {
+            if (kb >= steps) src.p.bytes = src.q.bytes = 0;
+            const uint32_t at = lds0 + (kb & 1) * T::kStage;
+            const bool is_last = kb == steps - 1 && src.last < kStep;
+            issue_q<T>(src, at, wave, is_last);
+            issue_p<T, kOnce, 0, T::kCopiesP / 2>(src, at, wave, is_last);
+            src.q.base += src.step_q;
+          },
+          [&](int kb) {
+            if (kb >= steps) src.p.bytes = 0;
+            issue_p<T, kOnce, T::kCopiesP / 2, T::kCopiesP>(src, lds0 + (kb & 1) * T::kStage, wave, kb == steps - 1 && src.last < kStep);
+            src.p.base += src.step_p;
+          },
+          lds, steps, count, acc);
+    };
+    if (once) large(std::true_type());
+    else large(std::false_type());
+  } else {
+    // Q tiles behind the last row are left out
+    auto run = [&](auto active) {
+      constexpr int kActive = decltype(active)::value;
+      if (once) contract<T, true, kActive>(src, lds, steps, acc);
+      else contract<T, false, kActive>(src, lds, steps, acc);
+    };
+    const int active = T::WQ == 1 ? (count + 15) / 16 : T::TQ;
+    if (T::TQ >= 4 && active == 3) run(std::integral_constant<int, T::TQ >= 4 ? 3 : T::TQ>());
+    else if (T::TQ >= 4 && active == 2) run(std::integral_constant<int, T::TQ >= 4 ? 2 : T::TQ>());
+    else if (T::TQ >= 2 && active == 1) run(std::integral_constant<int, T::TQ >= 2 ? 1 : T::TQ>());
+    else run(std::integral_constant<int, T::TQ>());
+  }
+
+  const int wp = wave % T::WP, wq = wave / T::WP;
+  constexpr int kCols = kPanelCols / T::WP;           // a wave's columns of a panel
+  const int t0 = wq * T::TQ * 16;                     // its first row of the tile
+  if (MODE == kPlain) {
+    turn<T, T::TP>(lds, [&](int ti, int j) { return acc[ti][j]; },
+                   [&](int row, int col, const uint4 &v) {
+                     const int n = n0 + col / kCols * kPanelCols + wp * kCols + col % kCols;
+                     if (t0 + row < count && n < P.N) store16<T::kLarge>(P.D + static_cast<int64_t>(first + t0 + row) * P.N + n, v);
+                   });
+  } else if (MODE == kGated) {
+    const int i0 = n0 + wp * kCols;
+    if (P.Z != nullptr) {
+#pragma unroll
+      for (int half = 0; half < T::kHalves; half++)
+        turn<T, T::kPerHalf>(lds, [&](int ti, int j) { return acc[half * T::kPerHalf + ti][j]; },
+                             [&](int row, int col, const uint4 &v) {
+                               if (t0 + row < count && i0 + col < width)
+                                 store16<T::kLarge>(P.Z + static_cast<int64_t>(first + t0 + row) * P.N + half * width + i0 + col, v);
+                             });
+    }
+    turn<T, T::kPerHalf>(lds,
+                         [&](int ti, int j) {
+                           float4v act;
+#pragma unroll
+                           for (int c = 0; c < 4; c++) {
+                             const float gate = acc[ti][j][c], up = acc[(T::kHalves - 1) * T::kPerHalf + ti][j][c];
+                             act[c] = gate * sigmoid(gate) * up;
+                           }
+                           return act;
+                         },
+                         [&](int row, int col, const uint4 &v) {
+                           if (t0 + row < count && i0 + col < width)
+                             store16<T::kLarge>(P.D + static_cast<int64_t>(first + t0 + row) * width + i0 + col, v);
+                         });
+  } else {
+    turn_f32<T, T::TP>(lds, acc, [&](int row, int col, const float4v &lo, const float4v &hi) {
+      const int n = n0 + col / kCols * kPanelCols + wp * kCols + col % kCols;
+      if (t0 + row >= count || n >= P.N) return;
+      const int64_t at = static_cast<int64_t>(first + t0 + row) * 2 * P.N + n;
+      const uint4 gate = *reinterpret_cast<const uint4 *>(P.Z + at), up = *reinterpret_cast<const uint4 *>(P.Z + at + P.N);
+      float4v dg[2], du[2];
+#pragma unroll
+      for (int c = 0; c < 8; c++) {
+        const float y = c < 4 ? lo[c & 3] : hi[c & 3], gv = element(gate, c), uv = element(up, c), s = sigmoid(gv);
+        dg[c / 4][c & 3] = y * uv * (s * (1.0f + gv * (1.0f - s)));
+        du[c / 4][c & 3] = y * (gv * s);
+      }
+      const uint2 a = bf16x4(dg[0]), b = bf16x4(dg[1]), c = bf16x4(du[0]), d = bf16x4(du[1]);
+      store16<T::kLarge>(P.D + at, make_uint4(a.x, a.y, b.x, b.y));
+      store16<T::kLarge>(P.D + at + P.N, make_uint4(c.x, c.y, d.x, d.y));
+    });
+  }
+}
+
+// ---- few items ------------------------------------------------------------------------------
+//
+// Where there are few rows and columns (a single token: k experts' weights, each a few hundred rows),
+// the contraction is dealt to the eight waves of a workgroup: wave w takes the steps w, w + 8, ... of a
+// tile of P rows of the weights and 16 rows of A, with a ring of its own and no barrier before the end,
+// and the eight partial tiles are added in order through LDS.  Gated: a 16-row tile of the weights
+// holds 8 gate rows and the 8 up rows that belong to them, which end in lane groups two apart.
+template <int P_, int WAVES_, int STAGES_>
+struct Split {
+  static constexpr int Q = 16, P = P_, WAVES = WAVES_, STAGES = STAGES_;
+  static constexpr int TP = P / 16;
+  static constexpr int kCopiesP = P / 8, kCopies = kCopiesP + Q / 8;
+  static constexpr int kStage = (P + Q) * kRowBytes;
+  static constexpr int kLds = WAVES * STAGES * kStage;
+  static_assert(TP * kWave * 16 <= STAGES * kStage, "a wave's partial tiles fit");
+};
+
+template <class T, Epilogue MODE>
+__global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams P) {
+  static_assert(MODE != kGatedBackward, "weights along the contraction");
+  __shared__ __align__(1024) uint8_t lds[T::kLds];
+  groups::Chunk g;
+  int chunk, nt;
+  if (!find_item(P, T::Q, g, chunk, nt)) return;
+  const int first = g.lo + chunk * T::Q, count = min(T::Q, g.hi - first);
+  constexpr int kTile = MODE == kGated ? 8 : 16;      // columns of the result in a 16-row tile
+  const int width = MODE == kGated ? P.N / 2 : P.N, n0 = nt * T::TP * kTile;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x & 63, lg = lane / 16, r = lane % 16;
+  const int steps = (P.K + kStep - 1) / kStep, last = P.K - (steps - 1) * kStep;
+  const bool gather = P.A_rows != nullptr;
+  const Buf bp = {reinterpret_cast<uint64_t>(P.B) + static_cast<uint64_t>(g.group) * P.N * P.K * 2, static_cast<uint32_t>(P.N) * P.K * 2};
+  const Buf bq = {reinterpret_cast<uint64_t>(P.A) + (gather ? 0 : static_cast<uint64_t>(first) * P.K * 2),
+                  static_cast<uint32_t>((gather ? P.rows_A : count) * P.K * 2)};
+  uint32_t vp[T::kCopiesP], vq[T::Q / 8];
+#pragma unroll
+  for (int j = 0; j < T::kCopiesP; j++) {
+    int row, piece;
+    place_along(j, row, piece);
+    const int i = n0 + row / 16 * kTile + row % kTile;
+    const int n = MODE == kGated ? i + row % 16 / 8 * width : i;
+    vp[j] = i < width ? static_cast<uint32_t>(n) * P.K * 2 + piece * 16 : kOob;
+  }
+#pragma unroll
+  for (int j = 0; j < T::Q / 8; j++) {
+    int row, piece;
+    place_along(j, row, piece);
+    vq[j] = kOob;
+    if (row < count) {
+      const int64_t a = gather ? clamped(P.A_rows[first + row], P.rows_A) : row;
+      vq[j] = static_cast<uint32_t>(a) * P.K * 2 + piece * 16;
+    }
+  }
+  uint8_t *ring = lds + wave * T::STAGES * T::kStage;
+  const uint32_t ring0 = lds_address(ring);
+  // the wave's i-th step into buffer `slot`
+  auto issue_step = [&](int i, int slot) {
+    const int kb = wave + T::WAVES * i;
+    const uint32_t at = ring0 + slot * T::kStage;
+    const bool past = kb >= steps, is_last = kb == steps - 1;
+#pragma unroll
+    for (int j = 0; j < T::kCopiesP; j++) {
+      const uint32_t v = in_range<false>(vp[j], j, is_last, last);
+      copy16<true>(bp, at + j * 1024, past || v == kOob ? kOob : v + kb * kRowBytes);
+    }
+#pragma unroll
+    for (int j = 0; j < T::Q / 8; j++) {
+      const uint32_t v = in_range<false>(vq[j], j, is_last, last);
+      copy16(bq, at + T::P * kRowBytes + j * 1024, past || v == kOob ? kOob : v + kb * kRowBytes);
+    }
+  };
+  float4v acc[T::TP] = {};
+#pragma unroll
+  for (int i = 0; i < T::STAGES; i++) issue_step(i, i);
+  int slot = 0;
+  for (int i = 0; wave + T::WAVES * i < steps; i++) {
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(T::kCopies * (T::STAGES - 1)) : "memory");
+    const uint8_t *S = ring + slot * T::kStage;
+    bf16x8 q[2], p[2][T::TP];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      q[h] = along(S + T::P * kRowBytes, r, h, lg);
+#pragma unroll
+      for (int t = 0; t < T::TP; t++) p[h][t] = along(S, t * 16 + r, h, lg);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // the buffer is read before it is filled again
+    issue_step(i + T::STAGES, slot);
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+      for (int t = 0; t < T::TP; t++) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p[h][t], q[h], acc[t], 0, 0, 0);
+    slot = slot == T::STAGES - 1 ? 0 : slot + 1;
+  }
+  arrive<0>();
+  float4v *part = reinterpret_cast<float4v *>(lds);   // [wave][tile][lane]
+#pragma unroll
+  for (int t = 0; t < T::TP; t++) part[(wave * T::TP + t) * kWave + lane] = acc[t];
+  __syncthreads();
+  for (int t = wave; t < T::TP; t += T::WAVES) {
+    float4v sum = part[t * kWave + lane];
+#pragma unroll
+    for (int w = 1; w < T::WAVES; w++) sum += part[(w * T::TP + t) * kWave + lane];
+    const int64_t p = first + r;
+    if (MODE == kPlain) {
+      const int n = n0 + t * 16 + 4 * lg;
+      if (r < count && n < P.N) *reinterpret_cast<uint2 *>(P.D + p * P.N + n) = bf16x4(sum);
+    } else {
+      float4v other, act;
+#pragma unroll
+      for (int c = 0; c < 4; c++) other[c] = __shfl_xor(sum[c], 32, kWave);
+      const int i = n0 + t * 8 + 4 * (lg & 1);
+#pragma unroll
+      for (int c = 0; c < 4; c++) act[c] = sum[c] * sigmoid(sum[c]) * other[c];   // of gate lanes
+      if (r >= count || i >= width) continue;
+      if (P.Z != nullptr) *reinterpret_cast<uint2 *>(P.Z + p * P.N + lg / 2 * width + i) = bf16x4(sum);
+      if (lg < 2) *reinterpret_cast<uint2 *>(P.D + p * width + i) = bf16x4(act);
+    }
+  }
+}
+
+// ---- the weight gradient -----------------------------------------------------------------------
+
+typedef const __attribute__((address_space(4))) int32_t *const_rows;   // read through scalar loads
+
+// One tile of D: Q is Y's columns n, P is X's columns k, the contraction the tokens of group e.
+template <class T, bool BF16>
+__global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P) {
+  static_assert(T::PT && T::QT && T::STAGES == 2, "the schedule below");
+  __shared__ __align__(1024) uint8_t lds[T::kLds];
+  const int n_tiles = (P.N + T::BQ - 1) / T::BQ, k_tiles = (P.K + T::BP - 1) / T::BP, per = n_tiles * k_tiles;
+  int64_t w;
+  if (!item_of(blockIdx.x, static_cast<int64_t>(P.E) * per, w)) return;
+  const int e = static_cast<int>(w / per);
+  int nt, kt;
+  place_in_band(static_cast<int>(w - static_cast<int64_t>(e) * per), n_tiles, k_tiles, nt, kt);
+  const int n0 = nt * T::BQ, k0 = kt * T::BP;
+  int lo = __builtin_amdgcn_readfirstlane(P.offsets[e]), hi = __builtin_amdgcn_readfirstlane(P.offsets[e + 1]);
+  groups::clamp_pair(lo, hi, P.R);
+  const int rows = hi - lo, steps = (rows + kStep - 1) / kStep;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & 63;
+  const bool gather = P.X_rows != nullptr;
+  const_rows index = (const_rows)(uintptr_t)P.X_rows;
+
+  Source<T> src;
+  src.last = rows - (steps - 1) * kStep;
+  // columns are checked by the offsets below, rows by `last`, so the ranges may be wide
+  src.q.base = reinterpret_cast<uint64_t>(P.Y) + static_cast<uint64_t>(lo) * P.N * 2;
+  src.p.base = reinterpret_cast<uint64_t>(P.X) + (gather ? 0 : static_cast<uint64_t>(lo) * P.K * 2);
+  src.q.bytes = src.p.bytes = kOob;
+  src.step_q = static_cast<uint32_t>(P.N) * kStep * 2;
+  src.step_p = gather ? 0 : static_cast<uint32_t>(P.K) * kStep * 2;
+#pragma unroll
+  for (int j = 0; j < T::kCopiesQ; j++) {
+    int k, col;
+    place_across(wave * T::kCopiesQ + j, k, col);
+    src.vq[j] = n0 + col < P.N ? (static_cast<uint32_t>(k) * P.N + n0 + col) * 2 : kOob;
+  }
+#pragma unroll
+  for (int j = 0; j < T::kCopiesP; j++) {
+    int k, col;
+    place_across(copy_p<T>(wave, j), k, col);
+    src.vp[j] = k0 + col < P.K ? (static_cast<uint32_t>(gather ? 0 : k) * P.K + k0 + col) * 2 : kOob;
+  }
+  const uint32_t lds0 = lds_address(lds);
+  // copies FROM to TO of X's stage kb; its gathered row numbers come through the scalar cache, so
+  // that no vector load stands between the copies
+  auto issue_x_rows = [&](auto from, auto to, int kb) {
+    constexpr int kFrom = decltype(from)::value, kTo = decltype(to)::value;
+    const uint32_t at = lds0 + (kb & 1) * T::kStage;
+    const bool is_last = kb == steps - 1 && src.last < kStep;
+    if (!gather) {
+      issue_p<T, false, kFrom, kTo>(src, at, wave, is_last);
+      return;
+    }
+#pragma unroll
+    for (int j = kFrom; j < kTo; j++) {
+      const int c = copy_p<T>(wave, j), row0 = lo + kb * kStep + c % 16 * 4;
+      uint32_t row = 0;
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const int v = index[min(row0 + q, P.R - 1)];
+        if (lane / 16 == q) row = static_cast<uint32_t>(clamped(v, P.rows_X));
+      }
+      const uint32_t v = in_range<true>(src.vp[j], c, is_last, src.last);
+      copy16(src.p, at + c * 1024, v == kOob ? kOob : v + row * static_cast<uint32_t>(P.K) * 2);
+    }
+  };
+  float4v acc[T::TP][T::TQ];
+  using std::integral_constant;
+  if constexpr (T::kLarge) {
+    contract_large<T>(
+        [&](int kb) {
+          if (kb >= steps) src.p.bytes = src.q.bytes = 0;
+          issue_q<T>(src, lds0 + (kb & 1) * T::kStage, wave, kb == steps - 1 && src.last < kStep);
+          issue_x_rows(integral_constant<int, 0>(), integral_constant<int, T::kCopiesP / 2>(), kb);
+          src.q.base += src.step_q;
+        },
+        [&](int kb) {
+          if (kb >= steps) src.p.bytes = 0;
+          issue_x_rows(integral_constant<int, T::kCopiesP / 2>(), integral_constant<int, T::kCopiesP>(), kb);
+          src.p.base += src.step_p;
+        },
+        lds, steps, P.N - n0, acc);
+  } else {
+    const int g = lane / 16, r = lane % 16, wp = wave % T::WP, wq = wave / T::WP;
+    auto issue_stage = [&](int kb) {
+      if (kb >= steps) src.p.bytes = src.q.bytes = 0;
+      issue_q<T>(src, lds0 + (kb & 1) * T::kStage, wave, kb == steps - 1 && src.last < kStep);
+      issue_x_rows(integral_constant<int, 0>(), integral_constant<int, T::kCopiesP>(), kb);
+      src.q.base += src.step_q;
+      src.p.base += src.step_p;
+    };
+    clear<T>(acc);
+    issue_stage(0);
+    for (int kb = 0; kb < steps; kb++) {
+      arrive<0>();
+      issue_stage(kb + 1);
+      const uint8_t *Ps = lds + (kb & 1) * T::kStage, *Qs = Ps + T::kBytesP;
+      bf16x8 q[2][T::TQ];
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int j = 0; j < T::TQ; j++) q[h][j] = fragment_q<T>(Qs, wq, j, h, g, r);
+#pragma unroll
+      for (int i = 0; i < T::TP; i++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const bf16x8 p = fragment_p<T>(Ps, wp, i / T::kPerHalf, i % T::kPerHalf, h, g, r);
+#pragma unroll
+          for (int j = 0; j < T::TQ; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, q[h][j], acc[i][j], 0, 0, 0);
+        }
+    }
+    arrive<0>();
+  }
+  const int wp = wave % T::WP, wq = wave / T::WP, t0 = n0 + wq * T::TQ * 16;
+  constexpr int kCols = kPanelCols / T::WP;
+  auto column = [&](int col) { return k0 + col / kCols * kPanelCols + wp * kCols + col % kCols; };
+  if (BF16) {
+    uint16_t *D = static_cast<uint16_t *>(P.D);
+    turn<T, T::TP>(lds, [&](int ti, int j) { return acc[ti][j]; },
+                   [&](int row, int col, const uint4 &v) {
+                     const int n = t0 + row, k = column(col);
+                     if (n < P.N && k < P.K) store16<true>(D + (static_cast<int64_t>(e) * P.N + n) * P.K + k, v);
+                   });
+  } else {
+    float *D = static_cast<float *>(P.D);
+    turn_f32<T, T::TP>(lds, acc, [&](int row, int col, const float4v &a, const float4v &b) {
+      const int n = t0 + row, k = column(col);
+      if (n >= P.N || k >= P.K) return;
+      float *at = D + (static_cast<int64_t>(e) * P.N + n) * P.K + k;
+      store16<true>(at, __builtin_bit_cast(uint4, a));
+      store16<true>(at + 4, __builtin_bit_cast(uint4, b));
+    });
+  }
+}
+
+// ---- launches -----------------------------------------------------------------------------------
+
+template <class T, Epilogue MODE>
+hipError_t run_gemm(GemmParams p, hipStream_t stream) {
+  p.n_tiles = MODE == kGated ? (p.N / 2 + kPanelCols - 1) / kPanelCols : (p.N + T::BP - 1) / T::BP;
+  const int64_t items = groups::max_chunks(p.R, p.E, T::BQ) * p.n_tiles;
+  const int64_t grid = (items + kXcds - 1) / kXcds * kXcds;
+  if (grid > 0) hipLaunchKernelGGL((gemm_kernel<T, MODE>), dim3(static_cast<uint32_t>(grid)), dim3(T::kThreadsT), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <class T, Epilogue MODE>
+hipError_t run_split(GemmParams p, hipStream_t stream) {
+  constexpr int kCols = MODE == kGated ? T::P / 2 : T::P;
+  const int width = MODE == kGated ? p.N / 2 : p.N;
+  p.n_tiles = (width + kCols - 1) / kCols;
+  const int64_t items = groups::max_chunks(p.R, p.E, T::Q) * p.n_tiles;
+  const int64_t grid = (items + kXcds - 1) / kXcds * kXcds;
+  hipLaunchKernelGGL((split_kernel<T, MODE>), dim3(static_cast<uint32_t>(grid)), dim3(T::WAVES * kWave), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <class T, bool BF16>
+hipError_t run_wgrad(const WgradParams &p, hipStream_t stream) {
+  const int64_t items = static_cast<int64_t>(p.E) * ((p.N + T::BQ - 1) / T::BQ) * ((p.K + T::BP - 1) / T::BP);
+  const int64_t grid = (items + kXcds - 1) / kXcds * kXcds;
+  hipLaunchKernelGGL((wgrad_kernel<T, BF16>), dim3(static_cast<uint32_t>(grid)), dim3(T::kThreadsT), 0, stream, p);
+  return hipGetLastError();
+}
+
+constexpr int64_t kCacheBytes = 256 << 20;   // MI355X's memory-side cache
+constexpr int kManyTiles = 192, kLargeRows = 44, kCus = 256;
+
+template <bool PT>
+using Large = Tile<256, 256, 4, 2, 2, PT>;
+
+}  // namespace
+
+hipError_t launch_gemm(GemmParams p, Epilogue epilogue, bool transposed, hipStream_t stream) {
+  const int64_t hit = p.R < p.E ? p.R : p.E;   // at most so many experts have rows
+  if (hit == 0) return hipSuccess;
+  const int64_t mean = p.R / hit;
+  p.stream_weights = static_cast<int64_t>(p.E) * p.N * p.K * 2 > kCacheBytes / 2;
+  auto tiles = [&](int q, int c) { return groups::max_chunks(p.R, p.E, q) * ((p.N + c - 1) / c); };
+  // q rows by c columns of groups of the mean size: at most one tile for each CU
+  auto one_round = [&](int q, int c) { return hit * ((mean + q - 1) / q) * ((p.N + c - 1) / c) <= kCus; };
+  const bool large = mean > kLargeRows && tiles(256, 256) >= kManyTiles;
+  const bool middle = mean > 2 * kLargeRows && tiles(128, 128) >= kManyTiles;
+  if (epilogue == kGated) {
+    if (large) return run_gemm<Large<false>, kGated>(p, stream);
+    if (mean <= 16 && p.K >= 4 * kStep) {
+      if (one_round(16, 16)) return run_split<Split<16, 8, 3>, kGated>(p, stream);
+      if (one_round(16, 32)) return run_split<Split<32, 8, 3>, kGated>(p, stream);
+    }
+    if (one_round(32, 256)) return run_gemm<Tile<32, 256, 1, 4, 3, false>, kGated>(p, stream);
+    return run_gemm<Tile<64, 256, 1, 8, 3, false>, kGated>(p, stream);
+  }
+  if (epilogue == kGatedBackward) {
+    if (large) return run_gemm<Large<true>, kGatedBackward>(p, stream);
+    if (middle) return run_gemm<Tile<128, 128, 2, 2, 2, true>, kGatedBackward>(p, stream);
+    return run_gemm<Tile<64, 128, 1, 4, 3, true>, kGatedBackward>(p, stream);
+  }
+  if (transposed) {
+    if (large) return run_gemm<Large<true>, kPlain>(p, stream);
+    if (middle) return run_gemm<Tile<128, 128, 2, 2, 2, true>, kPlain>(p, stream);
+    return run_gemm<Tile<64, 128, 1, 4, 3, true>, kPlain>(p, stream);
+  }
+  if (large) return run_gemm<Large<false>, kPlain>(p, stream);
+  if (mean <= 16 && p.K >= 4 * kStep) {
+    if (one_round(16, 16)) return run_split<Split<16, 8, 3>, kPlain>(p, stream);
+    if (one_round(16, 32)) return run_split<Split<32, 8, 3>, kPlain>(p, stream);
+  }
+  if (middle) return run_gemm<Tile<128, 128, 2, 2, 2, false>, kPlain>(p, stream);
+  return run_gemm<Tile<64, 128, 1, 4, 3, false>, kPlain>(p, stream);
+}
+
+hipError_t launch_wgrad(const WgradParams &p, bool bf16, hipStream_t stream) {
+  const int64_t large = static_cast<int64_t>(p.E) * ((p.N + 255) / 256) * ((p.K + 255) / 256);
+  if (large >= kManyTiles) {
+    using T = Tile<256, 256, 4, 2, 2, true, true>;
+    return bf16 ? run_wgrad<T, true>(p, stream) : run_wgrad<T, false>(p, stream);
+  }
+  using T = Tile<128, 128, 2, 2, 2, true, true>;
+  return bf16 ? run_wgrad<T, true>(p, stream) : run_wgrad<T, false>(p, stream);
+}
+
+}  // namespace bf16
+}  // namespace moe

@@ -1,0 +1,206 @@
+// The global norm of many gradient tensors and their clipping:
+//
+//   norm = sqrt(sum over all elements of x^2),   out = x min(1, max_norm / (norm + 1e-6))
+//
+// Both are one read of the tensors (the second also a write), so HBM bounds them, and launches where
+// the tensors are small.  The tensors' addresses travel in the kernel's arguments, up to kTable of them
+// in a launch, so nothing is copied to the device and a captured launch holds what it needs.  A
+// workgroup takes one chunk of kChunk elements of one tensor.  Squares are taken and summed in 64 bits:
+// gfx950's vector units do that as fast as in 32, and no gradient is too large or too small for it.
+#include "grad_clip.hpp"
+
+#pragma clang fp contract(off)
+
+namespace moe {
+namespace grad {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 256;
+constexpr int kTable = 96;
+constexpr int kChunkBits = 14;
+constexpr int64_t kChunk = int64_t(1) << kChunkBits;
+
+enum { kBf16 = 1, kWide = 2 };   // kWide: 16 bytes at a time
+
+// (Whole words only: the table lies in the kernel's arguments and is read with scalar loads, which
+// drop the low bits of an address's base and of its offset, so neither may be built from byte indexes.)
+struct Entry {
+  const void *src;
+  void *dst;
+  int64_t n;
+  int32_t first;               // chunks of the tensors before it
+  int32_t flags;
+};
+struct Table {
+  Entry e[kTable];
+  int32_t count, chunks;
+};
+
+int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
+
+// The tensor of chunk b, and its elements [lo, hi).
+__device__ __forceinline__ Entry find(const Table &t, int b, int64_t &lo, int64_t &hi) {
+  int i = 0;
+#pragma unroll
+  for (int step = 64; step > 0; step >>= 1)
+    if (i + step < t.count && t.e[i + step].first <= b) i += step;
+  const Entry e = t.e[i];
+  lo = static_cast<int64_t>(b - e.first) << kChunkBits;
+  hi = lo + kChunk < e.n ? lo + kChunk : e.n;
+  return e;
+}
+
+__device__ __forceinline__ double square(uint32_t bits) {
+  const double v = __uint_as_float(bits);
+  return v * v;
+}
+template <bool BF16>
+__device__ __forceinline__ float element(const void *p, int64_t i) {
+  return BF16 ? bf16_to_f32(static_cast<const uint16_t *>(p)[i]) : static_cast<const float *>(p)[i];
+}
+
+// The sum of v over the workgroup, in thread 0.
+template <int THREADS>
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double part[THREADS / kWave];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x / kWave] = v;
+  __syncthreads();
+  double s = 0.0;
+#pragma unroll
+  for (int w = 0; w < THREADS / kWave; w++) s += part[w];
+  return s;
+}
+
+template <bool BF16>
+__device__ __forceinline__ double sum_of_squares(const Entry &e, int64_t lo, int64_t hi) {
+  constexpr int kPer = BF16 ? 3 : 2;   // log2 of the elements in 16 bytes
+  double sum = 0.0;
+  if (e.flags & kWide) {
+    const u32x4 *p = static_cast<const u32x4 *>(e.src);
+    const int64_t to = hi >> kPer;
+#pragma unroll 4
+    for (int64_t a = (lo >> kPer) + threadIdx.x; a < to; a += kThreads) {
+      const u32x4 v = p[a];
+#pragma unroll
+      for (int c = 0; c < 4; c++) sum += BF16 ? square(v[c] << 16) + square(v[c] & 0xffff0000u) : square(v[c]);
+    }
+    lo = to << kPer;
+  }
+  for (int64_t a = lo + threadIdx.x; a < hi; a += kThreads) {
+    const double v = element<BF16>(e.src, a);
+    sum += v * v;
+  }
+  return sum;
+}
+
+__global__ __launch_bounds__(kThreads) void norm_kernel(const Table t, double *partial) {
+  int64_t lo, hi;
+  const Entry e = find(t, blockIdx.x, lo, hi);
+  const double sum = block_sum<kThreads>(e.flags & kBf16 ? sum_of_squares<true>(e, lo, hi) : sum_of_squares<false>(e, lo, hi));
+  if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+}
+
+constexpr int kSumThreads = 1024;
+__global__ __launch_bounds__(kSumThreads) void sum_kernel(const double *partial, int64_t n, float *norm) {
+  double sum = 0.0;
+  for (int64_t a = threadIdx.x; a < n; a += kSumThreads) sum += partial[a];
+  sum = block_sum<kSumThreads>(sum);
+  if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(sum));
+}
+
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t v, float s) {
+  return f32_to_bf16(__uint_as_float(v << 16) * s) | (static_cast<uint32_t>(f32_to_bf16(__uint_as_float(v & 0xffff0000u) * s)) << 16);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void scale(const Entry &e, int64_t lo, int64_t hi, float s) {
+  constexpr int kPer = BF16 ? 3 : 2;
+  if (e.flags & kWide) {
+    const u32x4 *p = static_cast<const u32x4 *>(e.src);
+    u32x4 *q = static_cast<u32x4 *>(e.dst);
+    const int64_t to = hi >> kPer;
+#pragma unroll 4
+    for (int64_t a = (lo >> kPer) + threadIdx.x; a < to; a += kThreads) {
+      u32x4 v = p[a];
+#pragma unroll
+      for (int c = 0; c < 4; c++) v[c] = BF16 ? scaled_pair(v[c], s) : __float_as_uint(__uint_as_float(v[c]) * s);
+      q[a] = v;
+    }
+    lo = to << kPer;
+  }
+  for (int64_t a = lo + threadIdx.x; a < hi; a += kThreads) {
+    const float v = element<BF16>(e.src, a) * s;
+    if (BF16) static_cast<uint16_t *>(e.dst)[a] = f32_to_bf16(v);
+    else static_cast<float *>(e.dst)[a] = v;
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void clip_kernel(const Table t, const float *norm, float max_norm) {
+  int64_t lo, hi;
+  const Entry e = find(t, blockIdx.x, lo, hi);
+  float s = max_norm / (*norm + 1e-6f);
+  if (s >= 1.0f || max_norm == INFINITY) s = 1.0f;   // (otherwise a NaN norm stays one)
+  if (s == 1.0f && e.src == e.dst) return;           // x * 1 = x
+  if (e.flags & kBf16) scale<true>(e, lo, hi, s);
+  else scale<false>(e, lo, hi, s);
+}
+
+// Calls launch(table) for the non-empty tensors, kTable at a time.
+template <class F>
+hipError_t for_tables(const moe_tensor *tensors, int count, bool write, F launch) {
+  Table t = {};
+  for (int i = 0; i <= count; i++) {
+    if (i < count && tensors[i].n > 0) {
+      const moe_tensor &x = tensors[i];
+      Entry &e = t.e[t.count++];
+      e.src = x.src;
+      e.dst = x.dst ? x.dst : x.src;
+      e.n = x.n;
+      e.first = t.chunks;
+      const uintptr_t at = reinterpret_cast<uintptr_t>(e.src) | (write ? reinterpret_cast<uintptr_t>(e.dst) : 0);
+      e.flags = (x.dtype == MOE_DTYPE_BF16 ? kBf16 : 0) | (at % 16 == 0 ? kWide : 0);
+      t.chunks += static_cast<int32_t>(chunks_of(x.n));
+    }
+    if (t.count > 0 && (t.count == kTable || i == count)) {
+      const hipError_t e = launch(t);
+      if (e != hipSuccess) return e;
+      t.count = t.chunks = 0;
+    }
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t norm_ws_bytes(const moe_tensor *tensors, int count) {
+  int64_t chunks = 0;
+  for (int i = 0; i < count; i++) chunks += chunks_of(tensors[i].n);
+  return static_cast<size_t>(chunks < 2 ? 2 : chunks) * sizeof(double);
+}
+
+hipError_t launch_norm(const moe_tensor *tensors, int count, float *norm, void *ws, hipStream_t stream) {
+  double *partial = static_cast<double *>(ws);
+  int64_t done = 0;
+  const hipError_t e = for_tables(tensors, count, false, [&](const Table &t) {
+    hipLaunchKernelGGL(norm_kernel, dim3(t.chunks), dim3(kThreads), 0, stream, t, partial + done);
+    done += t.chunks;
+    return hipGetLastError();
+  });
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(sum_kernel, dim3(1), dim3(kSumThreads), 0, stream, partial, done, norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_clip(const moe_tensor *tensors, int count, const float *norm, float max_norm, hipStream_t stream) {
+  return for_tables(tensors, count, true, [&](const Table &t) {
+    hipLaunchKernelGGL(clip_kernel, dim3(t.chunks), dim3(kThreads), 0, stream, t, norm, max_norm);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace grad
+}  // namespace moe

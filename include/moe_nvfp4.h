@@ -14,7 +14,8 @@
  *   6. moe_finalize        router-weighted gather-reduce of each token's k rows
  *                          into the bf16 output.
  * The same layer with FP8 experts, their training step and the router's balance
- * term are sections 5 to 8.
+ * term are sections 5 to 8; experts in bf16 with their backward pass, the clipping of
+ * gradients and the layer for single tokens are sections 9 to 11.
  *
  * Sources (web pages cited by title and section):
  *  - Operands are FP4 E2M1 with one FP8 scale per 16 elements along the
@@ -427,6 +428,142 @@ moe_status moe_balance_loss_backward(const float *logits, int T, int E, const in
                                      const uint8_t *token_mask, const float *coef, const float *grad_loss,
                                      const int32_t *topk_ids, const float *topk_w, const float *d_topk_w,
                                      int k, float *dlogits, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 9. Gated experts in bf16, with their backward pass.
+ *
+ * Defined by: this library (the pages serve experts that were trained and then quantised; this is
+ * the block of sections 3 and 6 as it is trained).  For expert e and permuted row p in
+ * [expert_offsets[e], expert_offsets[e+1]):
+ *   y[p, n] = sum_k a[r, k] b[e, n, k]   with B_layout MOE_LAYOUT_ROWMAJOR,   B [E, N, K]
+ *   y[p, n] = sum_k a[r, k] b[e, k, n]   with B_layout MOE_LAYOUT_TRANSPOSED, B [E, K, N]
+ * with r = A_rows ? A_rows[p] : p; products are exact and sums binary32 (a bf16 denormal counts as its value).
+ * Epilogues:
+ *   MOE_EPI_NONE    D bf16 [R, N]: D[p, n] = bf16(y[p, n]).
+ *   MOE_EPI_SWIGLU  row-major B, N = 2I; columns [0, I) are gate g, [I, 2I) are up u:
+ *                   D bf16 [R, I]: D[p, i] = bf16(silu(g) u) of the unrounded sums (hardware exp2
+ *                   and reciprocal: a few ulp of binary32); with Z != NULL also Z bf16 [R, 2I] =
+ *                   bf16(y), which the backward pass reads.
+ *   MOE_EPI_SWIGLU_BACKWARD  transposed B (the down projection W2 [E, K = H, N = I], A the gradient
+ *                   of its output): y is the gradient of the activations; with g, u of Z bf16
+ *                   [R, 2N] and s = 1 / (1 + exp(-g)), D bf16 [R, 2N] receives
+ *                   D[p, i] = bf16(y u s (1 + g (1 - s))),  D[p, N + i] = bf16(y g s).
+ * Rows p >= expert_offsets[E] of D and Z are not written.  The gradient with respect to the block's
+ * rows is the product MOE_EPI_NONE of that D with W1 [E, 2I, H] transposed (moe_finalize with unit
+ * weights sums a token's rows).
+ * Supported: N % 8 == 0 (SWIGLU: N % 16 == 0), K % 8 == 0, N, K <= 2^20, N * K <= 2^30 - 2048,
+ * 1 <= E <= 1024, R <= 2^30, (R / 32 + E) * ceil(N / 128) < 2^24 - 8; with A_rows: rows_A * K <=
+ * 2^30 - 2048; MOE_ERR_UNSUPPORTED otherwise.  Without A_rows, rows_A >= R.  No workspace.
+ *
+ * Weight gradient: D[e, n, k] = sum over the rows p of group e of Y[p, n] X[r, k], r = X_rows ?
+ * X_rows[p] : p, products exact, sums binary32; Y bf16 [R, N], X bf16 [rows_X, K], D [E, N, K] in
+ * D_dtype (MOE_DTYPE_F32, or MOE_DTYPE_BF16: rounded once), zeros for an expert without rows.
+ * Limits: N, K, E and R as above, with X_rows rows_X * K <= 2^30 - 2048, E * ceil(N / 128) *
+ * ceil(K / 128) < 2^24 - 8.
+ * ------------------------------------------------------------------------- */
+enum { MOE_EPI_SWIGLU_BACKWARD = 4, MOE_LAYOUT_TRANSPOSED = 2 };
+
+typedef struct moe_gemm_bf16_args {
+  const uint16_t *A;              /* [rows_A, K] */
+  const int32_t *A_rows;          /* [R] gather map, or NULL for the identity */
+  int64_t rows_A;                 /* rows of A */
+  const uint16_t *B;              /* [E, N, K] or, transposed, [E, K, N] */
+  const int32_t *expert_offsets;  /* [E+1] */
+  int32_t E, N, K;
+  int32_t epilogue;
+  int32_t B_layout;               /* MOE_LAYOUT_ROWMAJOR or MOE_LAYOUT_TRANSPOSED */
+  int64_t R;
+  uint16_t *D;                    /* [R, N] (NONE), [R, N/2] (SWIGLU), [R, 2N] (SWIGLU_BACKWARD) */
+  uint16_t *Z;                    /* SWIGLU: out [R, N] or NULL; SWIGLU_BACKWARD: in [R, 2N] */
+} moe_gemm_bf16_args;
+
+moe_status moe_grouped_gemm_bf16_can_implement(const moe_gemm_bf16_args *args);
+moe_status moe_grouped_gemm_bf16(const moe_gemm_bf16_args *args, hipStream_t stream);
+
+typedef struct moe_wgrad_bf16_args {
+  const uint16_t *Y;              /* [R, N] */
+  const uint16_t *X;              /* [rows_X, K] */
+  const int32_t *X_rows;          /* [R] gather map, or NULL for the identity */
+  int64_t rows_X;
+  const int32_t *expert_offsets;  /* [E+1] */
+  int32_t E, N, K;
+  int32_t D_dtype;
+  int64_t R;
+  void *D;                        /* [E, N, K] */
+} moe_wgrad_bf16_args;
+
+moe_status moe_grouped_wgrad_bf16_can_implement(const moe_wgrad_bf16_args *args);
+moe_status moe_grouped_wgrad_bf16(const moe_wgrad_bf16_args *args, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 10. The global norm of gradients and their clipping.
+ *
+ * Defined by: this library.  `tensors` is a HOST array of `count` entries; they are read before the
+ * call returns, and the kernels get the addresses in their arguments.
+ *   moe_grad_norm  *norm = sqrt(sum of x^2 over the n elements of every src), squares and sums in
+ *                  binary64, rounded once to binary32 (0 for no elements; NaN or infinity where an
+ *                  element is one).
+ *   moe_grad_clip  dst = x s with s = min(1, max_norm / (*norm + 1e-6)), in binary32, rounded once to
+ *                  the tensor's type; dst NULL: in place.  A NaN norm makes s NaN, an infinite one 0;
+ *                  in place with s = 1 nothing is written.  A dst other than NULL and src may not
+ *                  overlap any src.
+ * dtype: MOE_DTYPE_BF16 or MOE_DTYPE_F32, of src and dst.  A tensor need be aligned to its elements
+ * only; where src and dst lie on 16 bytes it is read and written 16 bytes at a time.  Several processes' shares
+ * of one model: sum the squares of their norms, and clip by the root of it.
+ * Limits: 0 <= count <= 2^20, at most 2^37 elements in all, max_norm >= 0 (not NaN; infinity clips
+ * nothing).  ws: moe_grad_norm_workspace(tensors, count) bytes, 16-byte aligned (contents on entry
+ * irrelevant; calls that may overlap need one each).
+ * ------------------------------------------------------------------------- */
+typedef struct moe_tensor {
+  void *src;
+  void *dst;                      /* moe_grad_clip; NULL: src */
+  int64_t n;
+  int32_t dtype;
+} moe_tensor;
+
+size_t moe_grad_norm_workspace(const moe_tensor *tensors, int count);
+moe_status moe_grad_norm(const moe_tensor *tensors, int count, float *norm, void *ws, size_t ws_bytes,
+                         hipStream_t stream);
+moe_status moe_grad_clip(const moe_tensor *tensors, int count, const float *norm, float max_norm,
+                         hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 11. One or a few tokens with NVFP4 weights, activations in bf16.
+ *
+ * Defined by: this library; the weights are section 3's (row-major, or packed by section 3b), so a
+ * server holds them once for its batches and its single tokens.  For token t and slot j with expert
+ * e = ids[t, j] (ids NULL: k = 1, e = 0, a dense projection):
+ *   y[t, j, n] = B_gs[e] * sum_kb sB[e, n, kb] sum_{i<16} x[r, 16kb+i] b[e, n, 16kb+i]
+ * with r = t where rows_x == T, and r = t*k + j where rows_x == T*k; products are exact and sums
+ * binary32 (a bf16 denormal counts as zero or as its value).  No permutation and no quantisation of the tokens come before it.
+ * Epilogues:
+ *   MOE_EPI_NONE      D bf16 [T*k, N]: bf16(y[t, j, n]).
+ *   MOE_EPI_SWIGLU    N = 2I, gate columns first: D bf16 [T*k, I]: bf16(silu(g) u), unrounded sums
+ *                     (hardware exp2 and reciprocal).
+ *   MOE_EPI_FINALIZE  D bf16 [T, N]: bf16(sum_j topk_w[t, j] y[t, j, n]) in binary32; topk_w NULL: 1.
+ * An id outside [0, E) is a dropped slot: its row of D is zeros, and it adds nothing to a sum.  A token
+ * may name an expert twice.  Tokens that share an expert share the read of its weights, 16 tokens at a time.
+ * Supported: 0 <= T <= 4096, 1 <= k <= 32, 1 <= E <= 65536, N % 16 == 0 (SWIGLU: N % 32 == 0), K % 32
+ * == 0 (packed: K % 256 == 0), N, K <= 2^20; MOE_ERR_SHAPE or MOE_ERR_UNSUPPORTED otherwise.  No workspace.
+ * ------------------------------------------------------------------------- */
+enum { MOE_EPI_FINALIZE = 5 };
+
+typedef struct moe_gemv_args {
+  const uint16_t *x;              /* [rows_x, K] */
+  int64_t rows_x;                 /* T or T*k */
+  const uint8_t *B;               /* [E, N, K/2], or packed */
+  const uint8_t *B_sf;            /* [E, N, K/16] (packed: ignored) */
+  const float *B_gs;              /* [E] */
+  const int32_t *ids;             /* [T, k] or NULL */
+  const float *topk_w;            /* FINALIZE: [T, k] or NULL */
+  int32_t T, k, E, N, K;
+  int32_t epilogue;
+  int32_t B_layout;               /* moe_layout */
+  uint16_t *D;
+} moe_gemv_args;
+
+moe_status moe_gemv_nvfp4_can_implement(const moe_gemv_args *args);
+moe_status moe_gemv_nvfp4(const moe_gemv_args *args, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,210 @@
+"""Products of one or a few tokens with NVFP4 weights on the GPU against 64 bits: exact where the sums
+are, within the bounds of binary32 sums where they are not, over numbers of tokens, slots, experts
+(named twice, shared, dropped), sizes and both layouts; and the layer plan that is made of them."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import block_scaled_fp4_02_amd as moe
+from tests import experts_ref as ref
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    moe.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _exact_weights(g, E, N, K):
+    """Every code, scales 1 or 2: sums of products with small whole numbers are exact in binary32."""
+    q = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda").to(torch.uint8)
+    sf = (0x38 + 8 * torch.randint(0, 2, (E, N, K // 16), generator=g, device="cuda")).to(torch.uint8)
+    return moe.NVFP4Tensor(q, sf, 2.0 ** -torch.arange(1, E + 1, device="cuda").remainder(3).float())
+
+
+def _any_weights(g, E, N, K):
+    q = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda").to(torch.uint8)
+    sf = torch.randint(0, 0x7f, (E, N, K // 16), generator=g, device="cuda").to(torch.uint8)   # every finite scale
+    return moe.NVFP4Tensor(q, sf, 0.01 * torch.rand(E, generator=g, device="cuda") + 1e-3)
+
+
+def _ids(g, T, k, E, how):
+    if how == "any":        # the same expert twice for a token, and dropped slots
+        return torch.randint(-1, E + 1, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    return torch.randn(T, E, generator=g, device="cuda").topk(k, dim=1).indices.to(torch.int32)
+
+
+def _layouts(W):
+    yield W
+    if W.q.shape[2] * 2 % 256 == 0:
+        yield moe.pack_weights(W)
+
+
+# T, k, E, N, K
+CASES = {"one token": (1, 8, 16, 64, 512), "one slot": (1, 1, 1, 16, 32), "few experts": (4, 2, 3, 48, 256), "five": (5, 3, 7, 96, 288),
+         "eight": (8, 8, 8, 32, 1024), "nine": (9, 4, 40, 80, 96), "sixteen": (16, 8, 24, 32, 768), "seventeen": (17, 2, 5, 64, 2080),
+         "many": (130, 6, 11, 32, 256), "32 slots": (3, 32, 40, 32, 64), "wide": (2, 2, 4, 4112, 160), "long": (1, 2, 4, 32, 20512)}
+
+
+@pytest.mark.parametrize("how", ["distinct", "any"])
+@pytest.mark.parametrize("name", CASES)
+def test_exact_products(name, how):
+    T, k, E, N, K = CASES[name]
+    g = _gen(len(name))
+    W, ids = _exact_weights(g, E, N, K), _ids(g, T, k, E, how)
+    wv = ref.nvfp4_values(W.q, W.sf, W.gs)
+    for rows in {T, T * k}:
+        x = torch.randint(-3, 4, (rows, K), generator=g, device="cuda").to(BF16)
+        want, _ = ref.gemv(x, wv, ids)
+        for B in _layouts(W):
+            D = torch.full((T * k + 2, N), -77.0, dtype=BF16, device="cuda")
+            moe.moe_gemv_nvfp4(moe.make_gemv_args(x, B, ids, D=D))
+            assert torch.equal(D[:T * k].double(), ref.bf16(want)) and (D[T * k:] == -77.0).all()
+
+
+@pytest.mark.parametrize("how", ["distinct", "any"])
+@pytest.mark.parametrize("name", [n for n in CASES if CASES[n][3] % 32 == 0])
+def test_gated(name, how):
+    T, k, E, N, K = CASES[name]
+    g = _gen(2 * len(name))
+    W, ids = _any_weights(g, E, N, K), _ids(g, T, k, E, how)
+    x = (0.3 * torch.randn(T, K, generator=g, device="cuda")).to(BF16)
+    W.gs /= 40 * K ** 0.5       # pre-activations of a few units
+    y, mag = ref.gemv(x, ref.nvfp4_values(W.q, W.sf, W.gs), ids)
+    e = ref.sum_error(K + K // 16 + 2) * mag
+    gate, up = y.chunk(2, 1)
+    eg, eu = e.chunk(2, 1)
+    bound = 1.1 * eg * (up.abs() + eu) + (torch.nn.functional.silu(gate).abs() + 1.1 * eg) * eu + 1.01 * ref.swiglu_error(y)
+    for B in _layouts(W):
+        act = moe.gemv_nvfp4_alloc(x, B, ids, epilogue=moe.MOE_EPI_SWIGLU)
+        assert ref.close(act, ref.swiglu(y), bound)
+        assert not act[(ids.flatten() < 0) | (ids.flatten() >= E)].any()
+
+
+@pytest.mark.parametrize("weighted", [True, False], ids=["weighted", "plain sum"])
+@pytest.mark.parametrize("how", ["distinct", "any"])
+@pytest.mark.parametrize("name", CASES)
+def test_weighted_sums(name, how, weighted):
+    T, k, E, N, K = CASES[name]
+    g = _gen(3 * len(name))
+    W, ids = _any_weights(g, E, N, K), _ids(g, T, k, E, how)
+    x = torch.randn(T * k, K, generator=g, device="cuda").to(BF16)
+    tw = torch.rand(T, k, generator=g, device="cuda") if weighted else None
+    y, mag = ref.gemv(x, ref.nvfp4_values(W.q, W.sf, W.gs), ids)
+    w = (tw if weighted else torch.ones(T, k, device="cuda")).double()[..., None]
+    want, mag = (y.view(T, k, N) * w).sum(1), (mag.view(T, k, N) * w).sum(1)
+    for B in _layouts(W):
+        out = moe.gemv_nvfp4_alloc(x, B, ids, tw, moe.MOE_EPI_FINALIZE)
+        assert ref.close(out, want, ref.sum_error(K + K // 16 + k + 4) * mag)
+
+
+@pytest.mark.parametrize("T", [0, 1, 3, 7, 16, 40])
+def test_dense(T):
+    g = _gen(T)
+    W = _any_weights(g, 1, 208, 1056)
+    x = torch.randn(T, 1056, generator=g, device="cuda").to(BF16)
+    y, mag = ref.gemv(x, ref.nvfp4_values(W.q, W.sf, W.gs), torch.zeros(T, 1, dtype=torch.int32, device="cuda"))
+    for epilogue in (moe.MOE_EPI_NONE, moe.MOE_EPI_FINALIZE):
+        out = moe.gemv_nvfp4_alloc(x, W, epilogue=epilogue)
+        assert out.shape == (T, 208) and ref.close(out, y, ref.sum_error(1056 + 70) * mag)
+
+
+def test_all_slots_dropped():
+    g = _gen(9)
+    W, x = _any_weights(g, 4, 64, 256), torch.randn(6, 256, generator=g, device="cuda").to(BF16)
+    ids = torch.full((6, 1), -1, dtype=torch.int32, device="cuda")
+    for epilogue in (moe.MOE_EPI_NONE, moe.MOE_EPI_SWIGLU, moe.MOE_EPI_FINALIZE):
+        assert not moe.gemv_nvfp4_alloc(x, W, ids, epilogue=epilogue).any()
+
+
+def test_a_tokens_nan_stays_in_it():
+    g = _gen(10)
+    W, x = _exact_weights(g, 3, 32, 256), torch.randint(-3, 4, (5, 256), generator=g, device="cuda").to(BF16)
+    ids = torch.zeros(5, 2, dtype=torch.int32, device="cuda")
+    ids[:, 1] = 2
+    want = [moe.gemv_nvfp4_alloc(x.repeat_interleave(2, 0), W, ids, epilogue=e) for e in (moe.MOE_EPI_NONE, moe.MOE_EPI_FINALIZE)]
+    x[3] = float("nan")
+    got = [moe.gemv_nvfp4_alloc(x.repeat_interleave(2, 0), W, ids, epilogue=e) for e in (moe.MOE_EPI_NONE, moe.MOE_EPI_FINALIZE)]
+    for a, b, rows in zip(got, want, (slice(6, 8), slice(3, 4))):
+        assert a[rows].isnan().all()
+        a[rows] = b[rows]
+        assert torch.equal(a, b)
+
+
+def test_repeats_and_layouts_give_the_same_bits():
+    """Partial sums are taken in one order and joined in order, whichever layout holds the weights."""
+    g = _gen(12)
+    W, x = _any_weights(g, 6, 64, 2048), torch.randn(4, 2048, generator=g, device="cuda").to(BF16)
+    ids = _ids(g, 4, 3, 6, "distinct")
+    a = moe.gemv_nvfp4_alloc(x, W, ids)
+    for _ in range(3):
+        assert torch.equal(a, moe.gemv_nvfp4_alloc(x, W, ids))
+    assert torch.equal(a, moe.gemv_nvfp4_alloc(x, moe.pack_weights(W), ids))
+
+
+def _layer(g, E, H, I):
+    mk = lambda *s: moe.quantize_experts(0.05 * torch.randn(*s, generator=g, device="cuda"))  # noqa: E731
+    return mk(E, 2 * I, H), mk(E, H, I)
+
+
+@pytest.mark.parametrize("T, E, k, H, I", [(1, 16, 4, 512, 256), (3, 8, 2, 256, 512), (16, 12, 6, 768, 256)])
+def test_layer_plan(T, E, k, H, I):
+    """Routing, gate/up and down products together, eager, on another stream, and replayed on new inputs."""
+    g = _gen(T + E)
+    W1, W2 = _layer(g, E, H, I)
+    v1, v2 = (ref.nvfp4_values(W.q, W.sf, W.gs) for W in (W1, W2))
+    logits, x = torch.randn(T, E, generator=g, device="cuda"), torch.randn(T, H, generator=g, device="cuda").to(BF16)
+    plans = [moe.MoETokenPlan(T, E, k, H, I, W1, W2), moe.MoETokenPlan(T, E, k, H, I, moe.pack_weights(W1), moe.pack_weights(W2))]
+    graphs = [p.graph(logits, x) for p in plans]
+    s = torch.cuda.Stream()
+    for i in range(3):
+        logits.copy_(torch.randn(T, E, generator=g, device="cuda"))
+        x.copy_(torch.randn(T, H, generator=g, device="cuda"))
+        out = plans[0].forward(logits, x).clone()
+        ids, w, act = plans[0].ids.clone(), plans[0].w.clone(), plans[0].act.clone()
+        assert torch.equal(ids.sort(1).values, logits.topk(k, 1).indices.sort(1).values.to(torch.int32))
+        y, mag = ref.gemv(x, v1, ids)
+        e = ref.sum_error(H + H // 16 + 2) * mag
+        gate, up = y.chunk(2, 1)
+        eg, eu = e.chunk(2, 1)
+        assert ref.close(act, ref.swiglu(y), 1.1 * eg * (up.abs() + eu) + (torch.nn.functional.silu(gate).abs() + 1.1 * eg) * eu + 1.01 * ref.swiglu_error(y))
+        y, mag = ref.gemv(act, v2, ids)
+        ww = w.double()[..., None]
+        assert ref.close(out, (y.view(T, k, H) * ww).sum(1), ref.sum_error(I + I // 16 + k + 4) * (mag.view(T, k, H) * ww).sum(1))
+        s.wait_stream(torch.cuda.current_stream())
+        plans[1].forward(logits, x, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(plans[1].out, out)
+        for p, graph in zip(plans, graphs):
+            p.out.fill_(-77.0)
+            p.act.fill_(-77.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(p.out, out) and torch.equal(p.act, act)
+
+
+def test_offsets_past_32_bits():
+    """Codes beyond 2^32 bytes and scales beyond 2^29: the last expert."""
+    g = _gen(13)
+    E, N, K = 20, 16384, 32768    # 5.4 GB of codes
+    W = moe.NVFP4Tensor(torch.zeros(E, N, K // 2, dtype=torch.uint8, device="cuda"), torch.zeros(E, N, K // 16, dtype=torch.uint8, device="cuda"),
+                        torch.ones(E, device="cuda"))
+    W.q[-1] = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda").to(torch.uint8)
+    W.sf[-1] = 0x38
+    x = torch.randint(-1, 2, (2, K), generator=g, device="cuda").to(BF16)
+    ids = torch.tensor([[E - 1], [0]], dtype=torch.int32, device="cuda")
+    want = x[0].double() @ ref.nvfp4_values(W.q[-1:], W.sf[-1:], W.gs[-1:])[0].T
+    for B in _layouts(W):
+        D = moe.gemv_nvfp4_alloc(x, B, ids)
+        assert torch.equal(D[0].double(), ref.bf16(want)) and not D[1].any()
