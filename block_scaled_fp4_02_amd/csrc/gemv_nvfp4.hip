@@ -47,6 +47,7 @@ constexpr int kPackBlock = 2304;   // bytes of one (16-row tile, step) block of 
 constexpr int kMaxSlots = 32;
 constexpr int NT = 2;              // tiles of 16 weight rows that a wave takes together
 constexpr int kCodes = kStep / 2;  // bytes of a row's codes in a step
+constexpr int kCus = 256, kLdsBytes = 160 << 10;
 
 // Row-major weights, K a multiple of 64, or of 32 (rows of scales then start at even bytes); packed.
 enum Layout { kRows64, kRows32, kPacked };
@@ -57,13 +58,13 @@ struct Shape {
   static constexpr int TB = TB_, WAVES = WAVES_, STAGES = STAGES_;
   static constexpr Layout L = L_;
   static constexpr bool SINGLE = SINGLE_;
-  static constexpr int kTokens = TB * 4, kPairs = SINGLE ? 1 : kTokens * kMaxSlots;
+  static constexpr int kTokens = TB * 4, kPairs = SINGLE ? kMaxSlots : kTokens * kMaxSlots;
   static constexpr int kScaleCopies = L == kRows32 ? 2 * NT : NT;   // of 256 bytes
   static constexpr int kXCopies = SINGLE ? 1 : kTokens / 2;         // of 1 KB: two tokens
   static constexpr int kCopies = NT * 2 + kScaleCopies + kXCopies;
   static constexpr int kScales = NT * 2048, kX = kScales + kScaleCopies * 256, kStage = kX + kXCopies * 1024;
   static constexpr int kRing = WAVES * STAGES * kStage;
-  static_assert(WAVES * NT * kTokens * 16 * 4 <= kRing, "partial sums");
+  static_assert(kMaxSlots <= 127, "slots in 8 bits");
 };
 
 // One step's weights of a tile in this lane: 64 codes of its row and their four scales.
@@ -188,114 +189,124 @@ __device__ __forceinline__ void consume(const uint8_t *stage, int K, int step, f
   asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // the stage is read before it is filled again
 }
 
-// The groups of a workgroup's tokens, in LDS: ids of their pairs and the first pair of each group.
-template <int PAIRS>
+// The groups of a workgroup's tokens, in LDS: ids of their pairs, what a pair's product is multiplied by,
+// and for each group its expert and every token's slot in it.
+template <int PAIRS, int TOKENS>
 struct Groups {
   int id[PAIRS];
+  float coef[PAIRS];
   uint64_t lead[(PAIRS + kWave - 1) / kWave];
-  uint16_t first[PAIRS];
+  int expert[PAIRS];
+  int8_t slot[PAIRS][TOKENS];   // -1: none
   int count;
 };
 
 // Slots of token t before slot `end` that chose e.
-template <int PAIRS>
-__device__ __forceinline__ int chosen(const Groups<PAIRS> &g, int k, int t, int e, int end) {
+template <class G>
+__device__ __forceinline__ int chosen(const G &g, int k, int t, int e, int end) {
   int n = 0;
   for (int j = 0; j < end; j++) n += g.id[t * k + j] == e ? 1 : 0;
   return n;
 }
 
-template <int PAIRS>
-__device__ __forceinline__ void build_groups(const Params &P, int t0, int tokens, Groups<PAIRS> &g) {
-  const int pairs = tokens * P.k;
-  for (int p = threadIdx.x; p < pairs; p += blockDim.x) {
-    const int id = P.ids ? P.ids[static_cast<int64_t>(t0) * P.k + p] : 0;
-    g.id[p] = id >= 0 && id < P.E ? id : -1;
+// A pair's group is led by the first token that chose its expert as often (`nth` times before).
+template <int PAIRS, int TOKENS>
+__device__ __forceinline__ void build_groups(const Params &P, int t0, int tokens, bool weighted, Groups<PAIRS, TOKENS> &g) {
+  const int pairs = tokens * P.k, threads = blockDim.x;
+  for (int p = threadIdx.x; p < pairs; p += threads) {
+    const int64_t at = static_cast<int64_t>(t0) * P.k + p;
+    const int id = P.ids ? P.ids[at] : 0;
+    const bool in = id >= 0 && id < P.E;
+    g.id[p] = in ? id : -1;
+    if (in) g.coef[p] = P.B_gs[id] * (weighted && P.topk_w ? P.topk_w[at] : 1.0f);
+    for (int t = 0; t < TOKENS; t++) g.slot[p][t] = -1;
   }
   __syncthreads();
-  const int rounds = (pairs + blockDim.x - 1) / blockDim.x;
-  for (int i = 0; i < rounds; i++) {
-    const int p = i * blockDim.x + threadIdx.x;
-    bool lead = false;
-    if (p < pairs && g.id[p] >= 0) {
-      const int t = p / P.k, e = g.id[p], nth = chosen(g, P.k, t, e, p - t * P.k);
-      lead = true;
-      for (int u = 0; u < t && lead; u++) lead = chosen(g, P.k, u, e, P.k) <= nth;
+  const int rounds = (pairs + threads - 1) / threads;
+  // the pair that leads pair p's group; -1 for a dropped slot
+  auto leader = [&](int p) {
+    const int e = g.id[p], t = p / P.k;
+    if (e < 0) return -1;
+    const int nth = chosen(g, P.k, t, e, p - t * P.k);
+    for (int u = 0; u < t; u++) {
+      int n = 0;
+      for (int j = 0; j < P.k; j++)
+        if (g.id[u * P.k + j] == e && n++ == nth) return u * P.k + j;
     }
-    const uint64_t mask = __ballot(lead);
+    return p;
+  };
+  for (int i = 0; i < rounds; i++) {
+    const int p = i * threads + threadIdx.x;
+    const uint64_t mask = __ballot(p < pairs && leader(p) == p);
     if ((threadIdx.x & 63) == 0 && p < pairs) g.lead[p / kWave] = mask;
   }
   __syncthreads();
-  int total = 0;
-  for (int w = 0; w * kWave < pairs; w++) {
-    const uint64_t mask = g.lead[w];
-    const int p = w * kWave + threadIdx.x;
-    if (threadIdx.x < kWave && (mask >> threadIdx.x & 1)) g.first[total + __popcll(mask & ((uint64_t(1) << threadIdx.x) - 1))] = static_cast<uint16_t>(p);
-    total += __popcll(mask);
+  for (int p = threadIdx.x; p < pairs; p += threads) {
+    const int q = leader(p);
+    if (q < 0) continue;
+    int group = __popcll(g.lead[q / kWave] & ((uint64_t(1) << (q % kWave)) - 1));
+    for (int w = 0; w < q / kWave; w++) group += __popcll(g.lead[w]);
+    g.expert[group] = g.id[p];
+    g.slot[group][p / P.k] = static_cast<int8_t>(p % P.k);
   }
-  if (threadIdx.x == 0) g.count = total;
+  if (threadIdx.x == 0) {
+    int total = 0;
+    for (int w = 0; w * kWave < pairs; w++) total += __popcll(g.lead[w]);
+    g.count = total;
+  }
   __syncthreads();
 }
 
-// The slot of token t in group number i, or -1.
-template <int PAIRS>
-__device__ __forceinline__ int slot_in(const Groups<PAIRS> &g, int k, int i, int t, int tokens) {
-  if (t >= tokens) return -1;
-  const int p = g.first[i], u = p / k, e = g.id[p], nth = chosen(g, k, u, e, p - u * k);
-  int n = 0;
-  for (int j = 0; j < k; j++) {
-    if (g.id[t * k + j] != e) continue;
-    if (n == nth) return j;
-    n++;
-  }
-  return -1;
-}
-
-// KS (PLAIN, GATED): waves that share a pair of tiles and deal its steps among themselves.
+// An item is a pair of tiles of one group (MODE kWeighted: a group; the workgroup has one pair).  A
+// workgroup takes a run of items, whose steps are dealt to its waves in equal runs, so the copies of one
+// item follow those of another without a pause; an item that several waves had parts of is summed by
+// all of them at the end, in the order of its steps.
 template <class S, Epilogue MODE>
-__global__ __launch_bounds__(S::WAVES *kWave) void gemv_kernel(const Params P, int KS) {
-  __shared__ __align__(1024) uint8_t ring[S::kRing];
-  __shared__ Groups<S::kPairs> groups;
-  constexpr int TB = S::TB;
+__global__ __launch_bounds__(S::WAVES *kWave) void gemv_kernel(const Params P) {
+  constexpr int TB = S::TB, kHeld = S::SINGLE ? 1 : S::kTokens;
   constexpr bool SINGLE = S::SINGLE;
+  __shared__ __align__(1024) uint8_t ring[S::kRing];
+  __shared__ float part[S::WAVES][2][NT][kHeld][16];   // of a wave's first item, of its last one
+  __shared__ Groups<S::kPairs, kHeld> groups;
   const int t0 = SINGLE ? 0 : blockIdx.z * S::kTokens, tokens = SINGLE ? 1 : min(S::kTokens, P.T - t0);
-  if (!SINGLE) build_groups(P, t0, tokens, groups);
+  if (!SINGLE) build_groups(P, t0, tokens, MODE == kWeighted, groups);
   const int count = SINGLE ? P.k : __builtin_amdgcn_readfirstlane(groups.count);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & 63, r = lane % 16;
   const int width = MODE == kGated ? P.N / 2 : P.N;
   constexpr int kCols = MODE == kGated ? 16 : 32;   // columns of the result in a pair of tiles
   const int pairs = (width + kCols - 1) / kCols, steps = (P.K + kStep - 1) / kStep;
-  // this wave's pair of tiles, and which of its steps (MODE == kWeighted: all waves have one pair)
-  const int pair = MODE == kWeighted ? blockIdx.x : blockIdx.x * (S::WAVES / KS) + wave / KS;
-  const int n0 = pair * kCols;
-  const bool idle = pair >= pairs;
 
-  // expert of group i; -1: a dropped slot of the only token
-  auto expert = [&](int i) {
-    if (!SINGLE) return __builtin_amdgcn_readfirstlane(groups.id[groups.first[i]]);
-    const int id = P.ids ? P.ids[i] : 0;
-    return __builtin_amdgcn_readfirstlane(id >= 0 && id < P.E ? id : -1);
-  };
-  auto slot = [&](int i, int t) { return SINGLE ? (t == 0 ? i : -1) : slot_in(groups, P.k, i, t, tokens); };
+  // SINGLE: slot j's expert is in lane j (-1: dropped); every wave writes the same factors
+  int my_id = -1;
+  if (SINGLE && lane < P.k) {
+    const int id = P.ids ? P.ids[lane] : 0;
+    const bool in = id >= 0 && id < P.E;
+    if (in) my_id = id;
+    groups.coef[lane] = in ? P.B_gs[id] * (MODE == kWeighted && P.topk_w ? P.topk_w[lane] : 1.0f) : 0.f;
+  }
+  if (SINGLE) wave_order();
+  auto expert = [&](int i) { return SINGLE ? __builtin_amdgcn_readlane(my_id, i) : __builtin_amdgcn_readfirstlane(groups.expert[i]); };
+  auto slot = [&](int i, int t) { return SINGLE ? (t == 0 ? i : -1) : static_cast<int>(groups.slot[i][t]); };
+  // of token t, whose slot in group i is j
+  auto coef = [&](int i, int t, int j) { return groups.coef[SINGLE ? i : t * P.k + j]; };
 
-  Source<S> src = {};   // (no bytes: what has no source copies zeros)
+  Source<S> src = {};
   // the workgroup's rows of x (at most 16 * 32 * 2^20 * 2 bytes)
   const int per = P.per_pair ? P.k : 1;
   src.x = uniform(Buf{reinterpret_cast<uint64_t>(P.x + static_cast<int64_t>(t0) * per * P.K), static_cast<uint32_t>(tokens * per) * P.K * 2});
-  auto set_source = [&](int i) {
-    const int e = expert(i);
+  auto set_source = [&](int i, int pair) {
+    const int e = expert(i), n0 = pair * kCols;
 #pragma unroll
     for (int t = 0; t < NT; t++) {
       // a second tile past the end is the first again, and not stored
       int base = n0 + (MODE == kGated ? t * width : t * 16);
       if (MODE != kGated && base >= P.N) base = n0;
       const int64_t n = static_cast<int64_t>(e) * P.N + base;
-      const bool none = e < 0 || idle;
       if (S::L == kPacked) {
-        src.code[t] = src.scale[t] = uniform(Buf{reinterpret_cast<uint64_t>(P.B + n / 16 * steps * kPackBlock), none ? 0u : steps * kPackBlock});
+        src.code[t] = src.scale[t] = uniform(Buf{reinterpret_cast<uint64_t>(P.B + n / 16 * steps * kPackBlock), e < 0 ? 0u : steps * kPackBlock});
       } else {
-        src.code[t] = uniform(Buf{reinterpret_cast<uint64_t>(P.B + n * (P.K / 2)), none ? 0u : 8u * P.K});
-        src.scale[t] = uniform(Buf{reinterpret_cast<uint64_t>(P.B_sf + n * (P.K / 16)), none ? 0u : static_cast<uint32_t>(P.K)});
+        src.code[t] = uniform(Buf{reinterpret_cast<uint64_t>(P.B + n * (P.K / 2)), e < 0 ? 0u : 8u * P.K});
+        src.scale[t] = uniform(Buf{reinterpret_cast<uint64_t>(P.B_sf + n * (P.K / 16)), e < 0 ? 0u : static_cast<uint32_t>(P.K)});
       }
     }
 #pragma unroll
@@ -314,24 +325,25 @@ __global__ __launch_bounds__(S::WAVES *kWave) void gemv_kernel(const Params P, i
 #pragma unroll
       for (int tb = 0; tb < TB; tb++) acc[t][tb] = float4v{0.f, 0.f, 0.f, 0.f};
   };
-  // Steps `first`, first + by, ... of group i, `todo` of them (across the groups' ends where by == 1).
-  // The copies run STAGES - 1 steps ahead; done(i) is called behind a group's last step, or this wave's.
-  auto stream = [&](int i, int first, int by, int todo, auto done) {
-    int ci = i, cs = first, left = todo;   // the copies' place
-    if (todo > 0) set_source(ci);
-    auto next_copies = [&](int slot) {
-      if (left > 0 && cs >= steps) {
-        cs -= steps;
-        set_source(++ci);
+  // Steps [begin, end) of all items' steps; the copies run STAGES - 1 steps ahead.  done(q, from, to) is
+  // called with the sums of item q's steps [from, to) in acc, and clears them.
+  auto stream = [&](int begin, int end, auto source_of, auto done) {
+    int cq = begin / steps, cs = begin - cq * steps, left = end - begin;   // the copies' place
+    if (left > 0) source_of(cq);
+    auto next_copies = [&](int at) {
+      if (left > 0 && cs == steps) {
+        cs = 0;
+        source_of(++cq);
       }
-      issue<S>(src, P.K, mine0 + slot * S::kStage, cs, left <= 0);
-      cs += by;
+      issue<S>(src, P.K, mine0 + at * S::kStage, cs, left <= 0);
+      cs++;
       left--;
     };
 #pragma unroll
     for (int u = 0; u < S::STAGES; u++) next_copies(u);
-    int s = first, at = 0;
-    for (int n = 0; n < todo; n++) {
+    int q = begin / steps, s = begin - q * steps, from = s, at = 0;
+    clear();
+    for (int n = end - begin; n > 0; n--) {
       asm volatile("s_waitcnt vmcnt(%0)" : : "n"(S::kCopies * (S::STAGES - 1)) : "memory");
       Weights w[NT];
       Elements x[TB];
@@ -340,121 +352,136 @@ __global__ __launch_bounds__(S::WAVES *kWave) void gemv_kernel(const Params P, i
 #pragma unroll
       for (int t = 0; t < NT; t++) multiply<TB>(w[t], x, acc[t]);
       at = at == S::STAGES - 1 ? 0 : at + 1;
-      s += by;
-      if (n == todo - 1 || s >= steps) {
-        done(i);
-        s -= steps;
-        i++;
+      s++;
+      if (n == 1 || s == steps) {
+        done(q, from, s);
+        clear();
+        q++;
+        s = from = 0;
       }
     }
   };
-  // sums over lane groups, put beside the other waves'
-  float(*part)[NT][S::kTokens][16] = reinterpret_cast<float(*)[NT][S::kTokens][16]>(ring);
-  auto join = [&](const float4v (&v)[NT][TB]) {
-    arrive<0>();   // no copy is under way into the ring, which the partial sums reuse
-#pragma unroll
-    for (int t = 0; t < NT; t++)
-#pragma unroll
-      for (int tb = 0; tb < TB; tb++)
-#pragma unroll
-        for (int c = 0; c < 4; c++) {
-          float u = v[t][tb][c];
-          u += __shfl_xor(u, 16, kWave);
-          u += __shfl_xor(u, 32, kWave);
-          if (lane < 16) part[wave][t][tb * 4 + c][r] = u;
-        }
-    __syncthreads();
-  };
-  auto sum = [&](int from, int waves, int t, int token, int col) {
-    float v = part[from][t][token][col];
-    for (int w = 1; w < waves; w++) v += part[from + w][t][token][col];
-    return v;
+  // v summed over the lane groups
+  auto over_groups = [&](float v) {
+    v += __shfl_xor(v, 16, kWave);
+    return v + __shfl_xor(v, 32, kWave);
   };
 
   if (MODE == kWeighted) {
+    const int n0 = blockIdx.x * kCols;
     float4v out[NT][TB];
 #pragma unroll
     for (int t = 0; t < NT; t++)
 #pragma unroll
       for (int tb = 0; tb < TB; tb++) out[t][tb] = float4v{0.f, 0.f, 0.f, 0.f};
-    // the steps of all groups, in order, dealt to the waves in equal parts
     const int total = count * steps, share = (total + S::WAVES - 1) / S::WAVES;
     const int begin = min(total, wave * share), end = min(total, begin + share);
-    clear();
-    stream(begin / steps, begin % steps, 1, end - begin, [&](int i) {
-      const int e = expert(i);
-      if (e >= 0) {
-        const float gs = P.B_gs[e];
+    stream(begin, end, [&](int i) { set_source(i, blockIdx.x); },
+           [&](int i, int, int) {
 #pragma unroll
-        for (int tb = 0; tb < TB; tb++)
+             for (int tb = 0; tb < TB; tb++)
 #pragma unroll
-          for (int c = 0; c < 4; c++) {
-            const int t = tb * 4 + c, j = slot(i, t);
-            if (j < 0) continue;
-            const float w = (P.topk_w ? P.topk_w[static_cast<int64_t>(t0 + t) * P.k + j] : 1.0f) * gs;
+               for (int c = 0; c < 4; c++) {
+                 const int t = tb * 4 + c, j = t < kHeld ? slot(i, t) : -1;
+                 if (j < 0 || expert(i) < 0) continue;
+                 const float f = coef(i, t, j);
 #pragma unroll
-            for (int n = 0; n < NT; n++) out[n][tb][c] = fmaf(acc[n][tb][c], w, out[n][tb][c]);
-          }
+                 for (int n = 0; n < NT; n++) out[n][tb][c] = fmaf(acc[n][tb][c], f, out[n][tb][c]);
+               }
+           });
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int t = 0; t < kHeld; t++) {
+        const float v = over_groups(out[n][t / 4][t % 4]);
+        if (lane < 16) part[wave][0][n][t][r] = v;
       }
-      clear();
-    });
-    join(out);
+    arrive<0>();
     for (int i = threadIdx.x; i < NT * tokens * 16; i += S::WAVES * kWave) {
       const int col = i % 16, t = i / 16 % NT, token = i / 16 / NT;
-      if (n0 + t * 16 < P.N) P.D[static_cast<int64_t>(t0 + token) * P.N + n0 + t * 16 + col] = f32_to_bf16(sum(0, S::WAVES, t, token, col));
+      float v = part[0][0][t][token][col];
+#pragma unroll
+      for (int w = 1; w < S::WAVES; w++) v += part[w][0][t][token][col];
+      if (n0 + t * 16 < P.N) P.D[static_cast<int64_t>(t0 + token) * P.N + n0 + t * 16 + col] = f32_to_bf16(v);
     }
     return;
   }
 
-  constexpr int kOut = MODE == kGated ? 1 : NT;   // tiles of results
-  const int lead = wave / KS * KS, rank = (wave - lead) * kWave + lane;   // the waves of this pair, the thread among theirs
-  if (!SINGLE && blockIdx.y == 0 && !idle) {      // dropped slots: zeros
-    const int cols = min(kCols, width - n0);
-    for (int i = rank; i < tokens * P.k * cols; i += KS * kWave) {
-      const int p = i / cols;
-      if (groups.id[p] < 0) P.D[(static_cast<int64_t>(t0) * P.k + p) * width + n0 + i % cols] = 0;
-    }
+  if (!SINGLE) {   // dropped slots: zeros
+    for (int p = 0; p < tokens * P.k; p++)
+      if (groups.id[p] < 0)
+        for (int c = blockIdx.x * blockDim.x + threadIdx.x; c < width; c += gridDim.x * blockDim.x)
+          P.D[(static_cast<int64_t>(t0) * P.k + p) * width + c] = 0;
   }
-  for (int i = blockIdx.y; i < count; i += gridDim.y) {
-    const int e = expert(i), from = wave - lead;
-    clear();
-    stream(i, from, KS, idle || e < 0 || from >= steps ? 0 : (steps - from + KS - 1) / KS, [](int) {});
-    join(acc);
-    const float gs = e < 0 ? 0.f : P.B_gs[e];
-    for (int o = idle ? INT_MAX : rank; o < kOut * tokens * 16; o += KS * kWave) {
-      const int col = o % 16, t = o / 16 % kOut, token = o / 16 / kOut;
-      const int j = slot(i, token);
-      if (j < 0 || n0 + t * 16 >= width) continue;
-      float v = sum(lead, KS, t, token, col) * gs;
-      if (MODE == kGated) {
-        const float up = sum(lead, KS, 1, token, col) * gs;
-        v = v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f)) * up;
-      }
-      P.D[(static_cast<int64_t>(t0 + token) * P.k + j) * width + n0 + t * 16 + col] = e < 0 ? 0 : f32_to_bf16(v);
+  const int items = count * pairs, run = (items + gridDim.x - 1) / gridDim.x;
+  const int first = min(items, static_cast<int>(blockIdx.x) * run), total = min(items - first, run) * steps;
+  const int share = (total + S::WAVES - 1) / S::WAVES;
+  const int begin = first * steps + min(total, wave * share), end = first * steps + min(total, (wave + 1) * share);
+  // column `col` of token t's row of item q, from the sums of the two tiles
+  auto store = [&](int q, int t, int col, float a, float b) {
+    const int i = q / pairs, n = (q - i * pairs) * kCols + col, j = slot(i, t);
+    if (j < 0) return;
+    const float f = coef(i, t, j);
+    uint16_t *at = P.D + (static_cast<int64_t>(t0 + t) * P.k + j) * width + n;
+    if (MODE == kGated) {
+      const float gate = a * f;
+      *at = f32_to_bf16(gate * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(gate * -1.4426950408889634f)) * (b * f));
+    } else {
+      *at = f32_to_bf16(a * f);
+      if (n + 16 < width) at[16] = f32_to_bf16(b * f);
     }
-    __syncthreads();   // the sums are read before the ring is filled again
+  };
+  stream(begin, end,
+         [&](int q) {
+           const int i = q / pairs;
+           set_source(i, q - i * pairs);
+         },
+         [&](int q, int from, int to) {
+           const bool whole = from == 0 && to == steps;
+           const int nth = q == begin / steps ? 0 : 1;
+#pragma unroll
+           for (int t = 0; t < kHeld; t++) {
+             const float a = over_groups(acc[0][t / 4][t % 4]), b = over_groups(acc[1][t / 4][t % 4]);
+             if (!whole) {
+               if (lane < 16) part[wave][nth][0][t][r] = a;
+               else if (lane < 32) part[wave][nth][1][t][r] = b;
+             } else if (lane / 16 == t % 4 && t < tokens) {
+               store(q, t, r, a, b);
+             }
+           }
+         });
+  arrive<0>();
+  // items in parts: wave w's part is its first one where the item is its first
+  for (int o = threadIdx.x; o < total / steps * tokens * 16; o += S::WAVES * kWave) {
+    const int col = o % 16, t = o / 16 % tokens, local = o / 16 / tokens;
+    const int from = local * steps / share, to = (local * steps + steps - 1) / share;
+    if (from == to) continue;
+    float a = 0.f, b = 0.f;
+    for (int w = from; w <= to; w++) {
+      const int nth = w * share / steps == local ? 0 : 1;
+      a += part[w][nth][0][t][col];
+      b += part[w][nth][1][t][col];
+    }
+    store(first + local, t, col, a, b);
   }
 }
 
 template <class S, Epilogue MODE>
 hipError_t run(const Params &p, hipStream_t stream) {
-  const int steps = (p.K + kStep - 1) / kStep, width = MODE == kGated ? p.N / 2 : p.N, cols = MODE == kGated ? 16 : 32;
+  const int width = MODE == kGated ? p.N / 2 : p.N, cols = MODE == kGated ? 16 : 32;
   const int pairs = (width + cols - 1) / cols, chunk = p.T < S::kTokens ? p.T : S::kTokens;
-  const int groups = chunk * p.k < p.E ? chunk * p.k : p.E;   // (more of them, of one expert each, take turns)
-  // waves that share a pair of tiles: as many as leave each of the card's waves work
-  int ks = 1;
-  while (ks < S::WAVES && ks < steps && static_cast<int64_t>(pairs) * groups * ks < 256 * 8) ks *= 2;
-  const int per = S::WAVES / ks;
-  const dim3 grid(MODE == kWeighted ? pairs : (pairs + per - 1) / per, MODE == kWeighted ? 1 : groups, (p.T + S::kTokens - 1) / S::kTokens);
-  hipLaunchKernelGGL((gemv_kernel<S, MODE>), grid, dim3(S::WAVES * kWave), 0, stream, p, ks);
+  const int64_t items = static_cast<int64_t>(pairs) * (chunk * p.k < p.E ? chunk * p.k : p.E);
+  const int64_t resident = kCus * (2 * S::kRing > kLdsBytes ? 1 : 2);   // workgroups that run at once
+  const dim3 grid(static_cast<uint32_t>(MODE == kWeighted ? pairs : items < resident ? items : resident), 1, (p.T + S::kTokens - 1) / S::kTokens);
+  hipLaunchKernelGGL((gemv_kernel<S, MODE>), grid, dim3(S::WAVES * kWave), 0, stream, p);
   return hipGetLastError();
 }
 
 template <Epilogue MODE, Layout L>
 hipError_t run_layout(const Params &p, hipStream_t stream) {
   if (p.T == 1) return run<Shape<1, L, true, 8, 3>, MODE>(p, stream);
-  if (p.T <= 4) return run<Shape<1, L, false, 4, 3>, MODE>(p, stream);
-  if (p.T <= 8) return run<Shape<2, L, false, 4, 2>, MODE>(p, stream);
+  if (p.T <= 4) return run<Shape<1, L, false, 8, 2>, MODE>(p, stream);
+  if (p.T <= 8) return run<Shape<2, L, false, L == kRows32 ? 4 : 8, 2>, MODE>(p, stream);
   return run<Shape<4, L, false, 4, 2>, MODE>(p, stream);
 }
 
