@@ -19,6 +19,7 @@ single tokens with NVFP4 weights (:func:`moe_gemv_nvfp4`, :class:`MoETokenPlan`)
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes as C
 import os
@@ -551,20 +552,28 @@ class GradList:
     def __init__(self, tensors, out=None):
         fn = "GradList"
         self.tensors, self.out = list(tensors), None if out is None else list(out)
-        n = len(self.tensors)
-        _sized(fn, self.out is None or len(self.out) == n, "as many outputs as tensors are needed")
-        self.device = self.tensors[0].get_device() if n else None
-        self.items = (moe_tensor * max(n, 1))()
-        self.count = n
-        for i, t in enumerate(self.tensors):
-            o = t if self.out is None else self.out[i]
-            if t.dtype not in _DTYPES or o.dtype != t.dtype or not (t.is_contiguous() and o.is_contiguous()) \
-                    or t.get_device() != self.device or o.get_device() != self.device:
-                raise MoeError(fn, MOE_ERR_UNSUPPORTED, f"tensor {i}: dense f32 or bf16 tensors on one device are needed, outputs of the same type, "
-                               f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device} and {o.dtype} on {o.device}")
-            if o.numel() != t.numel():
-                raise MoeError(fn, MOE_ERR_SHAPE, f"tensor {i}: {t.numel()} elements, its output has {o.numel()}")
-            self.items[i] = (t.data_ptr(), None if o is t else o.data_ptr(), t.numel(), _DTYPES[t.dtype])
+        ts, outs = self.tensors, self.out
+        self.count = len(ts)
+        _sized(fn, outs is None or len(outs) == self.count, "as many outputs as tensors are needed")
+        self.device = ts[0].get_device() if ts else None
+        # (each question is put to all tensors at once: a model has hundreds, and this runs every step)
+        types, sizes = [t.dtype for t in ts], [t.numel() for t in ts]
+        every = ts if outs is None else ts + outs
+        if not (set(types) <= _DTYPES.keys() and (outs is None or [o.dtype for o in outs] == types)
+                and all([t.is_contiguous() for t in every]) and {t.get_device() for t in every} <= {self.device}):
+            raise MoeError(fn, MOE_ERR_UNSUPPORTED, "dense f32 or bf16 tensors on one device are needed, each output of its tensor's type, got "
+                           + ", ".join(f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}" for t in every[:8]))
+        if outs is not None and [o.numel() for o in outs] != sizes:
+            raise MoeError(fn, MOE_ERR_SHAPE, "each output needs its tensor's number of elements")
+        words = [0] * (4 * max(self.count, 1))   # of each moe_tensor: src, dst, n, dtype
+        n = 4 * self.count
+        words[0:n:4] = [t.data_ptr() for t in ts]
+        if outs is not None:
+            words[1:n:4] = [o.data_ptr() for o in outs]
+        words[2:n:4] = sizes
+        words[3:n:4] = [_DTYPES[d] for d in types]
+        self._words = array.array("q", words)
+        self.items = self._words.buffer_info()[0]
 
 
 def _grad_list(tensors, out=None) -> GradList:
