@@ -40,113 +40,149 @@ typedef short short4v __attribute__((ext_vector_type(4)));
 typedef short short8v __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) short4v lds_short4;
 
-constexpr int kStep = 64;            // elements of the contraction in a stage
+#define INLINED __attribute__((always_inline))
+
 constexpr int kPanelCols = 128;      // rows or columns of an operand in a panel
-constexpr int kPanel = kPanelCols * kStep * 2;   // bytes
-constexpr int kRowBytes = kStep * 2; // of a row along the contraction
 constexpr int kAcross = kPanelCols * 2;          // bytes of a row across the contraction
 
 // ---- one tile -----------------------------------------------------------------------------
 
+// Elements of the contraction in a stage, and how an operand lies in LDS.
+template <int STEP_>
+struct Stage {
+  static constexpr int STEP = STEP_;
+  static constexpr int kRowBytes = STEP * 2;            // of a row along the contraction
+  static constexpr int kPieces = kRowBytes / 16;        // in such a row
+  static constexpr int kPanel = kPanelCols * kRowBytes; // bytes
+  static constexpr int kCopyRows = 64 / kPieces;        // rows along, and
+  static constexpr int kPanelCopies = STEP / 4;         // copies of a panel: 1 KB each, four rows across
+};
+
 // PT, QT: the operand's rows run across the contraction.
-template <int BQ_, int BP_, int WQ_, int WP_, int STAGES_, bool PT_, bool QT_ = false>
-struct Tile {
+template <int BQ_, int BP_, int WQ_, int WP_, int STAGES_, bool PT_, bool QT_ = false, int STEP_ = 64>
+struct Tile : Stage<STEP_> {
+  using St = Stage<STEP_>;
   static constexpr int BQ = BQ_, BP = BP_, WQ = WQ_, WP = WP_, STAGES = STAGES_;
   static constexpr bool PT = PT_, QT = QT_;
   static constexpr int kWaves = WQ * WP, kThreadsT = kWaves * kWave;
   static constexpr int kHalves = BP / kPanelCols;            // panels of P
   static constexpr int kPerHalf = kPanelCols / WP / 16;      // a wave's 16-row tiles in each panel
   static constexpr int TP = kHalves * kPerHalf, TQ = BQ / WQ / 16;
-  static constexpr int kCopiesP = BP / 8 / kWaves;           // copies of 1 KB per wave and stage
-  static constexpr int kCopiesQ = (BQ / 8 + kWaves - 1) / kWaves;
+  static constexpr int kCopiesP = BP / St::kCopyRows / kWaves;   // per wave and stage
+  static constexpr int kCopiesQ = (BQ / St::kCopyRows + kWaves - 1) / kWaves;
   static constexpr int kCopies = kCopiesP + kCopiesQ;
-  static constexpr int kBytesP = BP * kRowBytes, kBytesQ = kCopiesQ * kWaves * 1024;
+  static constexpr int kBytesP = BP * St::kRowBytes, kBytesQ = kCopiesQ * kWaves * 1024;
   static constexpr int kStage = kBytesP + kBytesQ;
   static constexpr bool kLarge = BQ == 256 && BP == 256;     // contract_large
   static constexpr int kLds = STAGES * kStage;
-  static_assert(BP % kPanelCols == 0 && BP / 8 % kWaves == 0 && BQ % (16 * WQ) == 0 && kPerHalf >= 1, "tile split");
+  static_assert(BP % kPanelCols == 0 && BP / St::kCopyRows % kWaves == 0 && BQ % (16 * WQ) == 0 && kPerHalf >= 1, "tile split");
   static_assert(!QT || BQ % kPanelCols == 0, "whole panels");
-  static_assert(STAGES >= 2 && kCopies * (STAGES - 2) < 64, "copies under way fit the counter");
+  static_assert(STAGES >= 2 && kCopies * (STAGES - 1) < 64, "copies under way fit the counter");
 };
 
-// Copy number j of a wave's stage of P among all copies of the stage: in the large tile a wave copies
-// as many of either panel.
-template <class T>
-__device__ __forceinline__ int copy_p(int wave, int j) {
-  constexpr int kHalf = T::kCopiesP / 2;
-  return T::kLarge ? j / kHalf * 16 + wave * kHalf + j % kHalf : wave * T::kCopiesP + j;
+// f(integral_constant 0), ..., f(integral_constant N - 1).
+template <int N, class F, int I = 0>
+__device__ __forceinline__ void for_constants(F f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>());
+    for_constants<N, F, I + 1>(f);
+  }
 }
 
+// The place of piece c of row r along the contraction among the row's pieces, or back.
+template <class S>
+__device__ __forceinline__ int swizzle_along(int r, int c) {
+  return S::kPieces == 8 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
+}
 // What copy number c moves in this lane.  Along: 16-byte piece `piece` of row `row` of the operand.
 // Across: row `k` of the stage, columns from `col`.
+template <class S>
 __device__ __forceinline__ void place_along(int c, int &row, int &piece) {
   const int lane = threadIdx.x & 63;
-  row = c * 8 + lane / 8;
-  piece = (lane & 7) ^ ((row >> 1) & 7);
+  row = c * S::kCopyRows + lane / S::kPieces;
+  piece = swizzle_along<S>(row, lane % S::kPieces);
 }
 __device__ __forceinline__ int swizzle_across(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
+template <class S>
 __device__ __forceinline__ void place_across(int c, int &k, int &col) {
   const int lane = threadIdx.x & 63;
-  k = c % 16 * 4 + lane / 16;
+  k = c % S::kPanelCopies * 4 + lane / 16;
   const int pair = ((lane & 15) >> 1) ^ swizzle_across(k);
-  col = c / 16 * kPanelCols + pair * 16 + (lane & 1) * 8;
+  col = c / S::kPanelCopies * kPanelCols + pair * 16 + (lane & 1) * 8;
 }
 
 // Where one lane's copies of a stage come from: byte offsets of its pieces in the two buffers (kOob:
-// nothing) and what the buffers advance per stage.  `last`: elements of the contraction in the last stage.
+// nothing) and what the buffers advance per stage.  An operand across the contraction ends with its
+// buffer (`left`: bytes of it from the stage on), so the range check drops the rows past the contraction's
+// end; one along it has more rows there, and `last`, the elements of the contraction in the last stage.
 template <class T>
 struct Source {
   Buf p, q;
+  int64_t left_p, left_q;
   uint32_t vp[T::kCopiesP], vq[T::kCopiesQ];
   uint32_t step_p, step_q;
   int last;
 };
 
-// This lane's offset in copy c: nothing if the contraction ends before its piece.
-template <bool ACROSS>
-__device__ __forceinline__ uint32_t in_range(uint32_t voff, int c, bool is_last, int last) {
-  int a, b;
-  if (ACROSS) place_across(c, a, b);
-  else place_along(c, b, a), a *= 8;
-  return is_last && a >= last ? kOob : voff;
+__device__ __forceinline__ uint32_t range_of(int64_t left) {
+  return left <= 0 ? 0u : static_cast<uint32_t>(left < kOob ? left : static_cast<int64_t>(kOob));
 }
 
-template <class T, bool ONCE, int FROM, int TO>
-__device__ __forceinline__ void issue_p(const Source<T> &src, uint32_t lds, int wave, bool is_last) {
-#pragma unroll
-  for (int j = FROM; j < TO; j++) {
-    const int c = copy_p<T>(wave, j);
-    copy16<ONCE>(src.p, lds + c * 1024, in_range<T::PT>(src.vp[j], c, is_last, src.last));
+// On to stage `kb`.
+template <bool ACROSS>
+__device__ __forceinline__ void advance_one(Buf &b, int64_t &left, uint32_t step, bool past) {
+  b.base += step;
+  if (ACROSS) {
+    left -= step;
+    b.bytes = range_of(left);
+  } else if (past) {
+    b.bytes = 0;
   }
 }
 template <class T>
-__device__ __forceinline__ void issue_q(const Source<T> &src, uint32_t lds, int wave, bool is_last) {
-#pragma unroll
-  for (int j = 0; j < T::kCopiesQ; j++) {
-    const int c = wave * T::kCopiesQ + j;
-    copy16(src.q, lds + T::kBytesP + c * 1024, in_range<T::QT>(src.vq[j], c, is_last, src.last));
+__device__ __forceinline__ void advance_to(Source<T> &src, int kb, int steps) {
+  advance_one<T::PT>(src.p, src.left_p, src.step_p, kb >= steps);
+  advance_one<T::QT>(src.q, src.left_q, src.step_q, kb >= steps);
+}
+
+// This lane's offset in copy c of an operand along the contraction: nothing if that ends before its piece.
+template <class S>
+__device__ __forceinline__ uint32_t in_range(uint32_t voff, int c, bool is_last, int last) {
+  int row, piece;
+  place_along<S>(c, row, piece);
+  return is_last && piece * 8 >= last ? kOob : voff;
+}
+
+// Copy number j of a wave's stage: first those of P, then those of Q.
+template <class T, bool ONCE>
+__device__ __forceinline__ void issue_one(const Source<T> &src, uint32_t lds, int wave, int j, bool is_last) {
+  if (j < T::kCopiesP) {
+    const int c = wave * T::kCopiesP + j;
+    copy16<ONCE>(src.p, lds + c * 1024, T::PT ? src.vp[j] : in_range<T>(src.vp[j], c, is_last, src.last));
+  } else {
+    const int i = j - T::kCopiesP, c = wave * T::kCopiesQ + i;
+    copy16(src.q, lds + T::kBytesP + c * 1024, T::QT ? src.vq[i] : in_range<T>(src.vq[i], c, is_last, src.last));
   }
 }
 
 // The copies of stage `kb` into the buffer at `lds`; beyond the last stage they move nothing.
 template <class T, bool ONCE>
 __device__ __forceinline__ void issue(Source<T> &src, uint32_t lds, int wave, int kb, int steps) {
-  const bool is_last = kb == steps - 1 && src.last < kStep;
-  if (kb >= steps) src.p.bytes = src.q.bytes = 0;
-  issue_p<T, ONCE, 0, T::kCopiesP>(src, lds, wave, is_last);
-  issue_q<T>(src, lds, wave, is_last);
-  src.p.base += src.step_p;
-  src.q.base += src.step_q;
+#pragma unroll
+  for (int j = 0; j < T::kCopies; j++) issue_one<T, ONCE>(src, lds, wave, j, kb == steps - 1 && src.last < T::STEP);
+  advance_to<T>(src, kb + 1, steps);
 }
 
 // Elements [32 h + 8 g, + 8) of the stage, for lane group g, of row `row` of an operand along it ...
+template <class S>
 __device__ __forceinline__ bf16x8 along(const uint8_t *rows, int row, int h, int g) {
-  return *reinterpret_cast<const bf16x8 *>(rows + row * kRowBytes + ((4 * h + g) ^ ((row >> 1) & 7)) * 16);
+  return *reinterpret_cast<const bf16x8 *>(rows + row * S::kRowBytes + swizzle_along<S>(row, 4 * h + g) * 16);
 }
 // ... or of column r of the 16 from `tile` * 16 of an operand across it.
+template <class S>
 __device__ __forceinline__ bf16x8 across(const uint8_t *operand, int tile, int h, int g, int r) {
   const int k = 32 * h + 8 * g + (r >> 2);   // and k + 4, whose swizzle is the same
-  const uint8_t *at = operand + tile / 8 * kPanel + k * kAcross + ((tile % 8) ^ ((r >> 2) | (g & 1) << 2)) * 32 + (r & 3) * 8;
+  const uint8_t *at = operand + tile / 8 * S::kPanel + k * kAcross + ((tile % 8) ^ ((r >> 2) | (g & 1) << 2)) * 32 + (r & 3) * 8;
   const short4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)at);
   const short4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(at + 4 * kAcross));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -156,14 +192,14 @@ __device__ __forceinline__ bf16x8 across(const uint8_t *operand, int tile, int h
 template <class T>
 __device__ __forceinline__ bf16x8 fragment_p(const uint8_t *P, int wp, int half, int i, int h, int g, int r) {
   const int tile = half * (kPanelCols / 16) + wp * T::kPerHalf + i;
-  if constexpr (T::PT) return across(P, tile, h, g, r);
-  else return along(P, tile * 16 + r, h, g);
+  if constexpr (T::PT) return across<T>(P, tile, h, g, r);
+  else return along<T>(P, tile * 16 + r, h, g);
 }
 template <class T>
 __device__ __forceinline__ bf16x8 fragment_q(const uint8_t *Q, int wq, int j, int h, int g, int r) {
   const int tile = wq * T::TQ + j;
-  if constexpr (T::QT) return across(Q, tile, h, g, r);
-  else return along(Q, tile * 16 + r, h, g);
+  if constexpr (T::QT) return across<T>(Q, tile, h, g, r);
+  else return along<T>(Q, tile * 16 + r, h, g);
 }
 
 template <class T>
@@ -174,9 +210,16 @@ __device__ __forceinline__ void clear(float4v (&acc)[T::TP][T::TQ]) {
     for (int j = 0; j < T::TQ; j++) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
 }
 
+template <class T>
+__device__ __forceinline__ void mfma_row(const bf16x8 &p, const bf16x8 (&q)[T::TQ], float4v (&acc)[T::TQ]) {
+#pragma unroll
+  for (int j = 0; j < T::TQ; j++) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, q[j], acc[j], 0, 0, 0);
+}
+
 // The whole contraction of one tile; ACTIVE of the wave's TQ column tiles are in use.
 template <class T, bool ONCE, int ACTIVE>
 __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps, float4v (&acc)[T::TP][T::TQ]) {
+  static_assert(T::STEP == 64, "two MFMAs of 32");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x & 63, g = lane / 16, r = lane % 16;
   const int wp = wave % T::WP, wq = wave / T::WP;
@@ -210,91 +253,105 @@ __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps
 
 // ---- the large tile -------------------------------------------------------------------------
 //
-// 256 x 256 results in eight waves, two on each SIMD, each 128 P rows (64 of either panel) by 64 Q
-// rows.  A step has four phases per wave: read panel 0 of P and all of Q from LDS into registers, 32
-// MFMAs, read panel 1 of P, 32 MFMAs.  Two workgroup barriers a step, after an MFMA phase of waves
-// 0-3 and a reading phase of waves 4-7, keep the two halves of the workgroup one phase apart, so on
-// every SIMD one wave's matrix instructions run while the other reads.  A stage has two parts, X (Q,
-// panel 0 of P) and Y (panel 1 of P), whose buffers are free again at the next barrier after they were
-// read: part X of step b + 2 is copied in the reading phase of panel 1 of step b, part Y of step b + 1
-// in that of panel 0, about six phases before they are read.
+// 256 x 256 results in four waves, one on each SIMD, each 128 x 128: every element that a wave reads from
+// LDS then meets 128 others, and LDS has 768 cycles of work (512 of reads, 256 of copies) for the 1024
+// that the matrix cores take for a stage.  A stage holds 32 elements of the contraction, 32 KB, and there
+// are five of them, all of LDS: one that is read and four, 128 KB, under way, which the latency of HBM
+// needs (with two stages of 64 elements, 64 KB under way, the same loop took 2.2 us for 64 elements,
+// twice what the matrix cores take).  A wave's 256 accumulators are AGPRs, and it keeps the matrix core
+// busy by itself: while the 64 MFMAs of one stage run, the next stage's operands are read.  One barrier a
+// stage tells that the next one is there and that this one is read, so that its buffer takes the copies
+// of the fifth one after it, issued between the MFMAs.
 
-template <class T>
-__device__ __forceinline__ void mfma_half(const bf16x8 (&p)[2][T::kPerHalf], const bf16x8 (&q)[2][T::TQ], float4v (*acc)[T::TQ]) {
-  __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-  for (int h = 0; h < 2; h++)
-#pragma unroll
-    for (int i = 0; i < T::kPerHalf; i++)
-#pragma unroll
-      for (int j = 0; j < T::TQ; j++)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p[h][i], q[h][j], acc[i][j], 0, 0, 0);
-  __builtin_amdgcn_sched_barrier(0);
+// acc += p q^T, in accumulation registers.  (Of the builtin the compiler gives a wave's 256 accumulators to
+// both kinds of registers and moves 580 of them in every step.)  Nothing reads them between a tile's first
+// and last MFMA but the MFMA 64 later; settle() stands before what does.
+__device__ __forceinline__ void mfma_agpr(const bf16x8 &p, const bf16x8 &q, float4v &acc) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(p), "v"(q));
 }
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" : : : "memory"); }
 
-// Copies that may be under way at a barrier: the two parts issued after the one it waits for.
-template <class T>
-constexpr int kLaterCopies = T::kCopiesQ + T::kCopiesP;
-
-// BEHIND: waves 4-7, whose barriers follow their reading phases.  issue_x and issue_y issue the parts
-// of a step.
-template <class T, bool BEHIND, class X, class Y>
-__device__ __forceinline__ void large_loop(X issue_x, Y issue_y, const uint8_t *lds, int steps, int wave, float4v (&acc)[T::TP][T::TQ]) {
-  constexpr int kLater = kLaterCopies<T>;
+// issue(j, kb, at): copy number j (a constant) of stage kb into the buffer at LDS address `at`;
+// prepare(kb): the loads that stage kb's copies need, while the stage before is issued; advance(kb): on to stage kb.  `cols`: rows of Q in use; a wave whose 128 are all behind them only copies.
+template <class T, class I, class R, class A>
+__device__ __forceinline__ void contract_large(I issue, R prepare, A advance, const uint8_t *lds, int steps, int cols, float4v (&acc)[T::TP][T::TQ]) {
+  static_assert(T::kWaves == 4 && T::TP == 8 && T::TQ == 8 && T::STEP == 32 && T::kCopies == T::TP, "the schedule above");
+  constexpr int kLater = T::kCopies * (T::STAGES - 2);   // copies of the stages after the next one
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x & 63, g = lane / 16, r = lane % 16;
   const int wp = wave % T::WP, wq = wave / T::WP;
-  for (int kb = 0; kb < steps; kb++) {
-    const uint8_t *P = lds + (kb & 1) * T::kStage, *Q = P + T::kBytesP;
-    bf16x8 p[2][T::kPerHalf], q[2][T::TQ];
-    issue_y(kb + 1);
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-#pragma unroll
-      for (int j = 0; j < T::TQ; j++) q[h][j] = fragment_q<T>(Q, wq, j, h, g, r);
-#pragma unroll
-      for (int i = 0; i < T::kPerHalf; i++) p[h][i] = fragment_p<T>(P, wp, 0, i, h, g, r);
-    }
-    if (BEHIND) arrive<kLater>();    // part Y of this step is there
-    mfma_half<T>(p, q, acc);
-    if (!BEHIND) arrive<kLater>();
-    issue_x(kb + 2);
-#pragma unroll
-    for (int h = 0; h < 2; h++)
-#pragma unroll
-      for (int i = 0; i < T::kPerHalf; i++) p[h][i] = fragment_p<T>(P, wp, 1, i, h, g, r);
-    if (BEHIND) arrive<kLater>();    // part X of the next step is there
-    mfma_half<T>(p, q, acc + T::kPerHalf);
-    if (!BEHIND) arrive<kLater>();
-  }
-}
-
-// `cols`: rows of Q in use; a wave whose 64 are all behind them only copies.
-template <class T, class X, class Y>
-__device__ __forceinline__ void contract_large(X issue_x, Y issue_y, const uint8_t *lds, int steps, int cols, float4v (&acc)[T::TP][T::TQ]) {
-  static_assert(T::kWaves == 8 && T::WP == 2 && T::kHalves == 2 && T::STAGES == 2, "the schedule above");
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  constexpr int kLater = kLaterCopies<T>;
+  const uint32_t lds0 = lds_address(lds);
   clear<T>(acc);
-  issue_x(0);
-  issue_y(0);
-  issue_x(1);
-  arrive<kLater>();                  // part X of step 0 is there
-  if (wave / T::WP * T::TQ * 16 >= cols) {
+  auto copies = [&](int kb, int slot) INLINED {
+    prepare(kb + 1);
+    for_constants<T::kCopies>([&](auto j) INLINED { issue(j, kb, lds0 + slot * T::kStage); });
+    advance(kb + 1);
+  };
+#pragma unroll
+  for (int i = 0; i < T::STAGES; i++) copies(i, i);
+  auto after = [](int slot) { return slot == T::STAGES - 1 ? 0 : slot + 1; };
+  int slot = 0;
+  if (wq * T::TQ * 16 >= cols) {
+    arrive<kLater + T::kCopies>();
     for (int kb = 0; kb < steps; kb++) {
-      issue_y(kb + 1);
       arrive<kLater>();
-      issue_x(kb + 2);
-      arrive<kLater>();
+      copies(kb + T::STAGES, slot);
+      slot = after(slot);
     }
-  } else if (wave >= T::kWaves / 2) {
-    large_loop<T, true>(issue_x, issue_y, lds, steps, wave, acc);
-  } else {
-    large_loop<T, false>(issue_x, issue_y, lds, steps, wave, acc);
+    arrive<0>();
+    return;
   }
+  bf16x8 p[2][T::TP], q[2][T::TQ];
+  // a quarter of a stage's operands
+  auto read = [&](auto half, const uint8_t *stage, int i) INLINED {
+    constexpr int h = decltype(half)::value;
+#pragma unroll
+    for (int u = 2 * i; u < 2 * i + 2; u++) {
+      p[h][u] = fragment_p<T>(stage, wp, u / T::kPerHalf, u % T::kPerHalf, 0, g, r);
+      q[h][u] = fragment_q<T>(stage + T::kBytesP, wq, u, 0, g, r);
+    }
+  };
+  // stage kb, whose operands are in p[h] and q[h]
+  auto stage_of = [&](auto half, int kb) INLINED {
+    constexpr int h = decltype(half)::value;
+    arrive<kLater>();                // the next stage is there, and no wave reads this one any more
+    prepare(kb + T::STAGES + 1);
+    const int next = after(slot);
+    for_constants<T::TP>([&](auto row) INLINED {
+      constexpr int i = decltype(row)::value;
+#pragma unroll
+      for (int j = 0; j < T::TQ; j++) {
+        mfma_agpr(p[h][i], q[h][j], acc[i][j]);
+        if (j == 1 && i < 4) {       // (behind MFMAs, which need not wait for these reads)
+          __builtin_amdgcn_sched_barrier(0);
+          read(std::integral_constant<int, 1 - h>(), lds + next * T::kStage, i);   // (past the end: zeros)
+        }
+        if (j == 4) issue(row, kb + T::STAGES, lds0 + slot * T::kStage);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    advance(kb + T::STAGES + 1);
+    slot = next;
+  };
+  arrive<kLater + T::kCopies>();     // stage 0 is there
+#pragma unroll
+  for (int i = 0; i < 4; i++) read(std::integral_constant<int, 0>(), lds, i);
+  for (int kb = 0; kb < steps; kb += 2) {
+    stage_of(std::integral_constant<int, 0>(), kb);
+    stage_of(std::integral_constant<int, 1>(), kb + 1);   // (an odd number of stages: one of zeros)
+  }
+  settle();
   arrive<0>();
 }
 
 // ---- results --------------------------------------------------------------------------------
+
+// Rounded to nearest even by the hardware's conversion, two at a time (by integer operations a large
+// tile's results took 5 us).
+__device__ __forceinline__ uint2 rounded4(const float4v &v) {
+  typedef __bf16 bf16x4v __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(uint2, __builtin_convertvector(v, bf16x4v));
+}
 
 __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
@@ -316,7 +373,7 @@ __device__ __forceinline__ void turn(uint8_t *lds, V value, S store) {
 #pragma unroll
     for (int j = 0; j < kTurn; j++)
 #pragma unroll
-      for (int ti = 0; ti < NT; ti++) *reinterpret_cast<uint2 *>(mine + (j * 16 + r) * kStride + ti * 32 + lg * 8) = bf16x4(value(ti, j0 + j));
+      for (int ti = 0; ti < NT; ti++) *reinterpret_cast<uint2 *>(mine + (j * 16 + r) * kStride + ti * 32 + lg * 8) = rounded4(value(ti, j0 + j));
     wave_order();
 #pragma unroll
     for (int c = 0; c < kPieces; c++) {
@@ -384,21 +441,22 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
 
   Source<T> src;
-  const int steps = (P.K + kStep - 1) / kStep;
-  src.last = P.K - (steps - 1) * kStep;
+  const int steps = (P.K + T::STEP - 1) / T::STEP;
+  src.last = P.K - (steps - 1) * T::STEP;
   src.p.base = reinterpret_cast<uint64_t>(P.B) + static_cast<uint64_t>(g.group) * P.N * P.K * 2;
-  src.p.bytes = static_cast<uint32_t>(P.N) * P.K * 2;
-  src.step_p = T::PT ? static_cast<uint32_t>(P.N) * kStep * 2 : kRowBytes;
+  src.left_p = static_cast<int64_t>(P.N) * P.K * 2;
+  src.p.bytes = range_of(src.left_p);
+  src.step_p = T::PT ? static_cast<uint32_t>(P.N) * T::STEP * 2 : T::kRowBytes;
 #pragma unroll
   for (int j = 0; j < T::kCopiesP; j++) {
-    const int c = copy_p<T>(wave, j);
+    const int c = wave * T::kCopiesP + j;
     if (T::PT) {
       int k, col;
-      place_across(c, k, col);
+      place_across<T>(c, k, col);
       src.vp[j] = n0 + col < P.N ? (static_cast<uint32_t>(k) * P.N + n0 + col) * 2 : kOob;
     } else {
       int row, piece;
-      place_along(c, row, piece);
+      place_along<T>(c, row, piece);
       const int i = n0 + (MODE == kGated ? row % kPanelCols : row);
       const int n = MODE == kGated ? i + row / kPanelCols * width : i;
       src.vp[j] = i < width ? static_cast<uint32_t>(n) * P.K * 2 + piece * 16 : kOob;
@@ -408,11 +466,11 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
   const bool gather = P.A_rows != nullptr;
   src.q.base = reinterpret_cast<uint64_t>(P.A) + (gather ? 0 : static_cast<uint64_t>(first) * P.K * 2);
   src.q.bytes = static_cast<uint32_t>((gather ? P.rows_A : count) * P.K * 2);
-  src.step_q = kRowBytes;
+  src.step_q = T::kRowBytes;
 #pragma unroll
   for (int j = 0; j < T::kCopiesQ; j++) {
     int row, piece;
-    place_along(wave * T::kCopiesQ + j, row, piece);
+    place_along<T>(wave * T::kCopiesQ + j, row, piece);
     src.vq[j] = kOob;
     if (row < count) {
       const int64_t a = gather ? clamped(P.A_rows[first + row], P.rows_A) : row;
@@ -424,23 +482,11 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
   // the weights of a group of one chunk are read by this workgroup alone
   const bool once = g.total == 1 && P.stream_weights;
   if constexpr (T::kLarge) {
-    const uint32_t lds0 = lds_address(lds);
     auto large = [&](auto streamed) {
       constexpr bool kOnce = decltype(streamed)::value;
       contract_large<T>(
-          [&](int kb) {
-            if (kb >= steps) src.p.bytes = src.q.bytes = 0;
-            const uint32_t at = lds0 + (kb & 1) * T::kStage;
-            const bool is_last = kb == steps - 1 && src.last < kStep;
-            issue_q<T>(src, at, wave, is_last);
-            issue_p<T, kOnce, 0, T::kCopiesP / 2>(src, at, wave, is_last);
-            src.q.base += src.step_q;
-          },
-          [&](int kb) {
-            if (kb >= steps) src.p.bytes = 0;
-            issue_p<T, kOnce, T::kCopiesP / 2, T::kCopiesP>(src, lds0 + (kb & 1) * T::kStage, wave, kb == steps - 1 && src.last < kStep);
-            src.p.base += src.step_p;
-          },
+          [&](auto j, int kb, uint32_t at) INLINED { issue_one<T, kOnce>(src, at, wave, j, kb == steps - 1 && src.last < T::STEP); },
+          [](int) INLINED {}, [&](int kb) INLINED { advance_to<T>(src, kb, steps); },
           lds, steps, count, acc);
     };
     if (once) large(std::true_type());
@@ -506,7 +552,7 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
         dg[c / 4][c & 3] = y * uv * (s * (1.0f + gv * (1.0f - s)));
         du[c / 4][c & 3] = y * (gv * s);
       }
-      const uint2 a = bf16x4(dg[0]), b = bf16x4(dg[1]), c = bf16x4(du[0]), d = bf16x4(du[1]);
+      const uint2 a = rounded4(dg[0]), b = rounded4(dg[1]), c = rounded4(du[0]), d = rounded4(du[1]);
       store16<T::kLarge>(P.D + at, make_uint4(a.x, a.y, b.x, b.y));
       store16<T::kLarge>(P.D + at + P.N, make_uint4(c.x, c.y, d.x, d.y));
     });
@@ -521,7 +567,7 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
 // and the eight partial tiles are added in order through LDS.  Gated: a 16-row tile of the weights
 // holds 8 gate rows and the 8 up rows that belong to them, which end in lane groups two apart.
 template <int P_, int WAVES_, int STAGES_>
-struct Split {
+struct Split : Stage<64> {
   static constexpr int Q = 16, P = P_, WAVES = WAVES_, STAGES = STAGES_;
   static constexpr int TP = P / 16;
   static constexpr int kCopiesP = P / 8, kCopies = kCopiesP + Q / 8;
@@ -542,7 +588,7 @@ __global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams
   const int width = MODE == kGated ? P.N / 2 : P.N, n0 = nt * T::TP * kTile;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x & 63, lg = lane / 16, r = lane % 16;
-  const int steps = (P.K + kStep - 1) / kStep, last = P.K - (steps - 1) * kStep;
+  const int steps = (P.K + T::STEP - 1) / T::STEP, last = P.K - (steps - 1) * T::STEP;
   const bool gather = P.A_rows != nullptr;
   const Buf bp = {reinterpret_cast<uint64_t>(P.B) + static_cast<uint64_t>(g.group) * P.N * P.K * 2, static_cast<uint32_t>(P.N) * P.K * 2};
   const Buf bq = {reinterpret_cast<uint64_t>(P.A) + (gather ? 0 : static_cast<uint64_t>(first) * P.K * 2),
@@ -551,7 +597,7 @@ __global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams
 #pragma unroll
   for (int j = 0; j < T::kCopiesP; j++) {
     int row, piece;
-    place_along(j, row, piece);
+    place_along<T>(j, row, piece);
     const int i = n0 + row / 16 * kTile + row % kTile;
     const int n = MODE == kGated ? i + row % 16 / 8 * width : i;
     vp[j] = i < width ? static_cast<uint32_t>(n) * P.K * 2 + piece * 16 : kOob;
@@ -559,7 +605,7 @@ __global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams
 #pragma unroll
   for (int j = 0; j < T::Q / 8; j++) {
     int row, piece;
-    place_along(j, row, piece);
+    place_along<T>(j, row, piece);
     vq[j] = kOob;
     if (row < count) {
       const int64_t a = gather ? clamped(P.A_rows[first + row], P.rows_A) : row;
@@ -575,13 +621,13 @@ __global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams
     const bool past = kb >= steps, is_last = kb == steps - 1;
 #pragma unroll
     for (int j = 0; j < T::kCopiesP; j++) {
-      const uint32_t v = in_range<false>(vp[j], j, is_last, last);
-      copy16<true>(bp, at + j * 1024, past || v == kOob ? kOob : v + kb * kRowBytes);
+      const uint32_t v = in_range<T>(vp[j], j, is_last, last);
+      copy16<true>(bp, at + j * 1024, past || v == kOob ? kOob : v + kb * T::kRowBytes);
     }
 #pragma unroll
     for (int j = 0; j < T::Q / 8; j++) {
-      const uint32_t v = in_range<false>(vq[j], j, is_last, last);
-      copy16(bq, at + T::P * kRowBytes + j * 1024, past || v == kOob ? kOob : v + kb * kRowBytes);
+      const uint32_t v = in_range<T>(vq[j], j, is_last, last);
+      copy16(bq, at + T::P * T::kRowBytes + j * 1024, past || v == kOob ? kOob : v + kb * T::kRowBytes);
     }
   };
   float4v acc[T::TP] = {};
@@ -594,9 +640,9 @@ __global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams
     bf16x8 q[2], p[2][T::TP];
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-      q[h] = along(S + T::P * kRowBytes, r, h, lg);
+      q[h] = along<T>(S + T::P * T::kRowBytes, r, h, lg);
 #pragma unroll
-      for (int t = 0; t < T::TP; t++) p[h][t] = along(S, t * 16 + r, h, lg);
+      for (int t = 0; t < T::TP; t++) p[h][t] = along<T>(S, t * 16 + r, h, lg);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // the buffer is read before it is filled again
     issue_step(i + T::STAGES, slot);
@@ -618,7 +664,7 @@ __global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams
     const int64_t p = first + r;
     if (MODE == kPlain) {
       const int n = n0 + t * 16 + 4 * lg;
-      if (r < count && n < P.N) *reinterpret_cast<uint2 *>(P.D + p * P.N + n) = bf16x4(sum);
+      if (r < count && n < P.N) *reinterpret_cast<uint2 *>(P.D + p * P.N + n) = rounded4(sum);
     } else {
       float4v other, act;
 #pragma unroll
@@ -627,8 +673,8 @@ __global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams
 #pragma unroll
       for (int c = 0; c < 4; c++) act[c] = sum[c] * sigmoid(sum[c]) * other[c];   // of gate lanes
       if (r >= count || i >= width) continue;
-      if (P.Z != nullptr) *reinterpret_cast<uint2 *>(P.Z + p * P.N + lg / 2 * width + i) = bf16x4(sum);
-      if (lg < 2) *reinterpret_cast<uint2 *>(P.D + p * width + i) = bf16x4(act);
+      if (P.Z != nullptr) *reinterpret_cast<uint2 *>(P.Z + p * P.N + lg / 2 * width + i) = rounded4(sum);
+      if (lg < 2) *reinterpret_cast<uint2 *>(P.D + p * width + i) = rounded4(act);
     }
   }
 }
@@ -638,9 +684,9 @@ __global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams
 typedef const __attribute__((address_space(4))) int32_t *const_rows;   // read through scalar loads
 
 // One tile of D: Q is Y's columns n, P is X's columns k, the contraction the tokens of group e.
-template <class T, bool BF16>
+template <class T, bool BF16, bool GATHER>
 __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P) {
-  static_assert(T::PT && T::QT && T::STAGES == 2, "the schedule below");
+  static_assert(T::PT && T::QT && (T::kLarge || (T::STAGES == 2 && T::STEP == 64)), "the schedules");
   __shared__ __align__(1024) uint8_t lds[T::kLds];
   const int n_tiles = (P.N + T::BQ - 1) / T::BQ, k_tiles = (P.K + T::BP - 1) / T::BP, per = n_tiles * k_tiles;
   int64_t w;
@@ -651,79 +697,88 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
   const int n0 = nt * T::BQ, k0 = kt * T::BP;
   int lo = __builtin_amdgcn_readfirstlane(P.offsets[e]), hi = __builtin_amdgcn_readfirstlane(P.offsets[e + 1]);
   groups::clamp_pair(lo, hi, P.R);
-  const int rows = hi - lo, steps = (rows + kStep - 1) / kStep;
+  const int rows = hi - lo, steps = (rows + T::STEP - 1) / T::STEP;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & 63;
-  const bool gather = P.X_rows != nullptr;
   const_rows index = (const_rows)(uintptr_t)P.X_rows;
 
   Source<T> src;
-  src.last = rows - (steps - 1) * kStep;
-  // columns are checked by the offsets below, rows by `last`, so the ranges may be wide
+  src.last = 0;   // (both operands lie across the contraction)
   src.q.base = reinterpret_cast<uint64_t>(P.Y) + static_cast<uint64_t>(lo) * P.N * 2;
-  src.p.base = reinterpret_cast<uint64_t>(P.X) + (gather ? 0 : static_cast<uint64_t>(lo) * P.K * 2);
-  src.q.bytes = src.p.bytes = kOob;
-  src.step_q = static_cast<uint32_t>(P.N) * kStep * 2;
-  src.step_p = gather ? 0 : static_cast<uint32_t>(P.K) * kStep * 2;
+  src.p.base = reinterpret_cast<uint64_t>(P.X) + (GATHER ? 0 : static_cast<uint64_t>(lo) * P.K * 2);
+  src.left_q = static_cast<int64_t>(rows) * P.N * 2;
+  src.left_p = (GATHER ? P.rows_X : rows) * P.K * 2;
+  src.q.bytes = range_of(src.left_q);
+  src.p.bytes = range_of(src.left_p);
+  src.step_q = static_cast<uint32_t>(P.N) * T::STEP * 2;
+  src.step_p = GATHER ? 0 : static_cast<uint32_t>(P.K) * T::STEP * 2;
 #pragma unroll
   for (int j = 0; j < T::kCopiesQ; j++) {
     int k, col;
-    place_across(wave * T::kCopiesQ + j, k, col);
+    place_across<T>(wave * T::kCopiesQ + j, k, col);
     src.vq[j] = n0 + col < P.N ? (static_cast<uint32_t>(k) * P.N + n0 + col) * 2 : kOob;
   }
 #pragma unroll
   for (int j = 0; j < T::kCopiesP; j++) {
     int k, col;
-    place_across(copy_p<T>(wave, j), k, col);
-    src.vp[j] = k0 + col < P.K ? (static_cast<uint32_t>(gather ? 0 : k) * P.K + k0 + col) * 2 : kOob;
+    place_across<T>(wave * T::kCopiesP + j, k, col);
+    src.vp[j] = k0 + col < P.K ? (static_cast<uint32_t>(GATHER ? 0 : k) * P.K + k0 + col) * 2 : kOob;
   }
   const uint32_t lds0 = lds_address(lds);
-  // copies FROM to TO of X's stage kb; its gathered row numbers come through the scalar cache, so
-  // that no vector load stands between the copies
-  auto issue_x_rows = [&](auto from, auto to, int kb) {
-    constexpr int kFrom = decltype(from)::value, kTo = decltype(to)::value;
-    const uint32_t at = lds0 + (kb & 1) * T::kStage;
-    const bool is_last = kb == steps - 1 && src.last < kStep;
-    if (!gather) {
-      issue_p<T, false, kFrom, kTo>(src, at, wave, is_last);
-      return;
-    }
+  // The byte in X of the gathered rows of a stage's copies, four rows each, come through the scalar
+  // cache, so that no vector load stands between the copies, and a stage ahead, so that none waits for
+  // them.  Past the group's end: a row past X's (its range is at most 2^31 - 4096 bytes, so no sum wraps).
+  int row_of[GATHER ? T::kCopiesP : 1][4], next_row_of[GATHER ? T::kCopiesP : 1][4];
+  auto load_rows = [&](int kb) INLINED {
+    if (!GATHER) return;
 #pragma unroll
-    for (int j = kFrom; j < kTo; j++) {
-      const int c = copy_p<T>(wave, j), row0 = lo + kb * kStep + c % 16 * 4;
-      uint32_t row = 0;
+    for (int j = 0; j < T::kCopiesP; j++) {
+      const int row0 = lo + kb * T::STEP + (wave * T::kCopiesP + j) % T::kPanelCopies * 4;
+#pragma unroll
+      for (int q = 0; q < 4; q++) next_row_of[j][q] = index[min(row0 + q, P.R - 1)];
+    }
+  };
+  auto take_rows = [&]() INLINED {
+    if (!GATHER) return;
+#pragma unroll
+    for (int j = 0; j < T::kCopiesP; j++)
+#pragma unroll
+      for (int q = 0; q < 4; q++) row_of[j][q] = next_row_of[j][q];
+  };
+  load_rows(0);
+  take_rows();
+  auto issue_copy = [&](auto number, int kb, uint32_t at) INLINED {
+    constexpr int j = decltype(number)::value;
+    if constexpr (!GATHER || j >= T::kCopiesP) {
+      issue_one<T, false>(src, at, wave, j, false);
+    } else {
+      const int c = wave * T::kCopiesP + j, row0 = lo + kb * T::STEP + c % T::kPanelCopies * 4, most = static_cast<int>(P.rows_X);
+      int row = 0;
 #pragma unroll
       for (int q = 0; q < 4; q++) {
-        const int v = index[min(row0 + q, P.R - 1)];
-        if (lane / 16 == q) row = static_cast<uint32_t>(clamped(v, P.rows_X));
+        const int v = row0 + q < hi ? min(max(row_of[j][q], 0), most - 1) : most;
+        if (lane / 16 == q) row = v;
       }
-      const uint32_t v = in_range<true>(src.vp[j], c, is_last, src.last);
-      copy16(src.p, at + c * 1024, v == kOob ? kOob : v + row * static_cast<uint32_t>(P.K) * 2);
+      copy16(src.p, at + c * 1024, src.vp[j] + static_cast<uint32_t>(row) * static_cast<uint32_t>(P.K) * 2);
+    }
+  };
+  auto advance = [&](int kb) INLINED {
+    if (GATHER) {
+      advance_one<false>(src.p, src.left_p, 0, false);
+      advance_one<true>(src.q, src.left_q, src.step_q, false);
+      take_rows();
+    } else {
+      advance_to<T>(src, kb, steps);
     }
   };
   float4v acc[T::TP][T::TQ];
-  using std::integral_constant;
   if constexpr (T::kLarge) {
-    contract_large<T>(
-        [&](int kb) {
-          if (kb >= steps) src.p.bytes = src.q.bytes = 0;
-          issue_q<T>(src, lds0 + (kb & 1) * T::kStage, wave, kb == steps - 1 && src.last < kStep);
-          issue_x_rows(integral_constant<int, 0>(), integral_constant<int, T::kCopiesP / 2>(), kb);
-          src.q.base += src.step_q;
-        },
-        [&](int kb) {
-          if (kb >= steps) src.p.bytes = 0;
-          issue_x_rows(integral_constant<int, T::kCopiesP / 2>(), integral_constant<int, T::kCopiesP>(), kb);
-          src.p.base += src.step_p;
-        },
-        lds, steps, P.N - n0, acc);
+    contract_large<T>(issue_copy, load_rows, advance, lds, steps, P.N - n0, acc);
   } else {
     const int g = lane / 16, r = lane % 16, wp = wave % T::WP, wq = wave / T::WP;
-    auto issue_stage = [&](int kb) {
-      if (kb >= steps) src.p.bytes = src.q.bytes = 0;
-      issue_q<T>(src, lds0 + (kb & 1) * T::kStage, wave, kb == steps - 1 && src.last < kStep);
-      issue_x_rows(integral_constant<int, 0>(), integral_constant<int, T::kCopiesP>(), kb);
-      src.q.base += src.step_q;
-      src.p.base += src.step_p;
+    auto issue_stage = [&](int kb) INLINED {
+      load_rows(kb + 1);
+      for_constants<T::kCopies>([&](auto j) INLINED { issue_copy(j, kb, lds0 + (kb & 1) * T::kStage); });
+      advance(kb + 1);
     };
     clear<T>(acc);
     issue_stage(0);
@@ -739,11 +794,7 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
 #pragma unroll
       for (int i = 0; i < T::TP; i++)
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const bf16x8 p = fragment_p<T>(Ps, wp, i / T::kPerHalf, i % T::kPerHalf, h, g, r);
-#pragma unroll
-          for (int j = 0; j < T::TQ; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, q[h][j], acc[i][j], 0, 0, 0);
-        }
+        for (int h = 0; h < 2; h++) mfma_row<T>(fragment_p<T>(Ps, wp, i / T::kPerHalf, i % T::kPerHalf, h, g, r), q[h], acc[i]);
     }
     arrive<0>();
   }
@@ -795,7 +846,10 @@ template <class T, bool BF16>
 hipError_t run_wgrad(const WgradParams &p, hipStream_t stream) {
   const int64_t items = static_cast<int64_t>(p.E) * ((p.N + T::BQ - 1) / T::BQ) * ((p.K + T::BP - 1) / T::BP);
   const int64_t grid = (items + kXcds - 1) / kXcds * kXcds;
-  hipLaunchKernelGGL((wgrad_kernel<T, BF16>), dim3(static_cast<uint32_t>(grid)), dim3(T::kThreadsT), 0, stream, p);
+  if (p.X_rows != nullptr)
+    hipLaunchKernelGGL((wgrad_kernel<T, BF16, true>), dim3(static_cast<uint32_t>(grid)), dim3(T::kThreadsT), 0, stream, p);
+  else
+    hipLaunchKernelGGL((wgrad_kernel<T, BF16, false>), dim3(static_cast<uint32_t>(grid)), dim3(T::kThreadsT), 0, stream, p);
   return hipGetLastError();
 }
 
@@ -803,7 +857,7 @@ constexpr int64_t kCacheBytes = 256 << 20;   // MI355X's memory-side cache
 constexpr int kManyTiles = 192, kLargeRows = 44, kCus = 256;
 
 template <bool PT>
-using Large = Tile<256, 256, 4, 2, 2, PT>;
+using Large = Tile<256, 256, 2, 2, 5, PT, false, 32>;
 
 }  // namespace
 
@@ -819,7 +873,7 @@ hipError_t launch_gemm(GemmParams p, Epilogue epilogue, bool transposed, hipStre
   const bool middle = mean > 2 * kLargeRows && tiles(128, 128) >= kManyTiles;
   if (epilogue == kGated) {
     if (large) return run_gemm<Large<false>, kGated>(p, stream);
-    if (mean <= 16 && p.K >= 4 * kStep) {
+    if (mean <= 16 && p.K >= 256) {
       if (one_round(16, 16)) return run_split<Split<16, 8, 3>, kGated>(p, stream);
       if (one_round(16, 32)) return run_split<Split<32, 8, 3>, kGated>(p, stream);
     }
@@ -837,7 +891,7 @@ hipError_t launch_gemm(GemmParams p, Epilogue epilogue, bool transposed, hipStre
     return run_gemm<Tile<64, 128, 1, 4, 3, true>, kPlain>(p, stream);
   }
   if (large) return run_gemm<Large<false>, kPlain>(p, stream);
-  if (mean <= 16 && p.K >= 4 * kStep) {
+  if (mean <= 16 && p.K >= 256) {
     if (one_round(16, 16)) return run_split<Split<16, 8, 3>, kPlain>(p, stream);
     if (one_round(16, 32)) return run_split<Split<32, 8, 3>, kPlain>(p, stream);
   }
@@ -848,7 +902,7 @@ hipError_t launch_gemm(GemmParams p, Epilogue epilogue, bool transposed, hipStre
 hipError_t launch_wgrad(const WgradParams &p, bool bf16, hipStream_t stream) {
   const int64_t large = static_cast<int64_t>(p.E) * ((p.N + 255) / 256) * ((p.K + 255) / 256);
   if (large >= kManyTiles) {
-    using T = Tile<256, 256, 4, 2, 2, true, true>;
+    using T = Tile<256, 256, 2, 2, 5, true, true, 32>;
     return bf16 ? run_wgrad<T, true>(p, stream) : run_wgrad<T, false>(p, stream);
   }
   using T = Tile<128, 128, 2, 2, 2, true, true>;
