@@ -195,9 +195,15 @@ __device__ __forceinline__ bf16x8 fragment_p(const uint8_t *P, int wp, int half,
   if constexpr (T::PT) return across<T>(P, tile, h, g, r);
   else return along<T>(P, tile * 16 + r, h, g);
 }
+// (The large tile deals its 16-row tiles to the waves in turn, so that few rows are few for every wave.)
+template <class T>
+__device__ __forceinline__ int tile_q(int wq, int j) { return T::kLarge ? j * T::WQ + wq : wq * T::TQ + j; }
+// Row number `row` of a wave's TQ * 16 as a row of the tile.
+template <class T>
+__device__ __forceinline__ int row_of_tile(int wq, int row) { return tile_q<T>(wq, row / 16) * 16 + row % 16; }
 template <class T>
 __device__ __forceinline__ bf16x8 fragment_q(const uint8_t *Q, int wq, int j, int h, int g, int r) {
-  const int tile = wq * T::TQ + j;
+  const int tile = tile_q<T>(wq, j);
   if constexpr (T::QT) return across<T>(Q, tile, h, g, r);
   else return along<T>(Q, tile * 16 + r, h, g);
 }
@@ -219,7 +225,7 @@ __device__ __forceinline__ void mfma_row(const bf16x8 &p, const bf16x8 (&q)[T::T
 // The whole contraction of one tile; ACTIVE of the wave's TQ column tiles are in use.
 template <class T, bool ONCE, int ACTIVE>
 __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps, float4v (&acc)[T::TP][T::TQ]) {
-  static_assert(T::STEP == 64, "two MFMAs of 32");
+  constexpr int kHalvesK = T::STEP / 32;   // MFMAs along the contraction
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x & 63, g = lane / 16, r = lane % 16;
   const int wp = wave % T::WP, wq = wave / T::WP;
@@ -233,15 +239,15 @@ __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps
     const int next = slot == 0 ? T::STAGES - 1 : slot - 1;
     issue<T, ONCE>(src, lds0 + next * T::kStage, wave, kb + T::STAGES - 1, steps);
     const uint8_t *P = lds + slot * T::kStage, *Q = P + T::kBytesP;
-    bf16x8 q[2][ACTIVE];
+    bf16x8 q[kHalvesK][ACTIVE];
 #pragma unroll
-    for (int h = 0; h < 2; h++)
+    for (int h = 0; h < kHalvesK; h++)
 #pragma unroll
       for (int j = 0; j < ACTIVE; j++) q[h][j] = fragment_q<T>(Q, wq, j, h, g, r);
 #pragma unroll
     for (int i = 0; i < T::TP; i++)
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
+      for (int h = 0; h < kHalvesK; h++) {
         const bf16x8 p = fragment_p<T>(P, wp, i / T::kPerHalf, i % T::kPerHalf, h, g, r);
 #pragma unroll
         for (int j = 0; j < ACTIVE; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, q[h][j], acc[i][j], 0, 0, 0);
@@ -272,9 +278,10 @@ __device__ __forceinline__ void mfma_agpr(const bf16x8 &p, const bf16x8 &q, floa
 __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" : : : "memory"); }
 
 // issue(j, kb, at): copy number j (a constant) of stage kb into the buffer at LDS address `at`;
-// prepare(kb): the loads that stage kb's copies need, while the stage before is issued; advance(kb): on to stage kb.  `cols`: rows of Q in use; a wave whose 128 are all behind them only copies.
-template <class T, class I, class R, class A>
-__device__ __forceinline__ void contract_large(I issue, R prepare, A advance, const uint8_t *lds, int steps, int cols, float4v (&acc)[T::TP][T::TQ]) {
+// prepare(kb): the loads that stage kb's copies need, while the stage before is issued; advance(kb): on to
+// stage kb.  ACTIVE of a wave's 8 column tiles are in use.
+template <class T, int ACTIVE, class I, class R, class A>
+__device__ __forceinline__ void contract_large(I issue, R prepare, A advance, const uint8_t *lds, int steps, float4v (&acc)[T::TP][T::TQ]) {
   static_assert(T::kWaves == 4 && T::TP == 8 && T::TQ == 8 && T::STEP == 32 && T::kCopies == T::TP, "the schedule above");
   constexpr int kLater = T::kCopies * (T::STAGES - 2);   // copies of the stages after the next one
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -282,66 +289,65 @@ __device__ __forceinline__ void contract_large(I issue, R prepare, A advance, co
   const int wp = wave % T::WP, wq = wave / T::WP;
   const uint32_t lds0 = lds_address(lds);
   clear<T>(acc);
-  auto copies = [&](int kb, int slot) INLINED {
-    prepare(kb + 1);
-    for_constants<T::kCopies>([&](auto j) INLINED { issue(j, kb, lds0 + slot * T::kStage); });
-    advance(kb + 1);
-  };
 #pragma unroll
-  for (int i = 0; i < T::STAGES; i++) copies(i, i);
-  auto after = [](int slot) { return slot == T::STAGES - 1 ? 0 : slot + 1; };
-  int slot = 0;
-  if (wq * T::TQ * 16 >= cols) {
-    arrive<kLater + T::kCopies>();
-    for (int kb = 0; kb < steps; kb++) {
-      arrive<kLater>();
-      copies(kb + T::STAGES, slot);
-      slot = after(slot);
-    }
-    arrive<0>();
-    return;
+  for (int i = 0; i < T::STAGES; i++) {
+    prepare(i + 1);
+    for_constants<T::kCopies>([&](auto j) INLINED { issue(j, i, lds0 + i * T::kStage); });
+    advance(i + 1);
   }
-  bf16x8 p[2][T::TP], q[2][T::TQ];
-  // a quarter of a stage's operands
-  auto read = [&](auto half, const uint8_t *stage, int i) INLINED {
+  int slot = 0;
+  bf16x8 p[2][T::TP], q[2][ACTIVE];
+  // number n of the next stage's operands: P's and Q's tiles in turn
+  auto read = [&](auto half, const uint8_t *stage, int n) INLINED {
     constexpr int h = decltype(half)::value;
-#pragma unroll
-    for (int u = 2 * i; u < 2 * i + 2; u++) {
-      p[h][u] = fragment_p<T>(stage, wp, u / T::kPerHalf, u % T::kPerHalf, 0, g, r);
-      q[h][u] = fragment_q<T>(stage + T::kBytesP, wq, u, 0, g, r);
-    }
+    const int u = n / 2;
+    if (n % 2 == 0) p[h][u] = fragment_p<T>(stage, wp, u / T::kPerHalf, u % T::kPerHalf, 0, g, r);
+    else if (u < ACTIVE) q[h][u] = fragment_q<T>(stage + T::kBytesP, wq, u, 0, g, r);
   };
-  // stage kb, whose operands are in p[h] and q[h]
+  // Stage kb, whose operands are in p[h] and q[h].  A wave issues an instruction in four cycles and an MFMA
+  // takes sixteen, so what stands between two of them is at most a read or a copy.
   auto stage_of = [&](auto half, int kb) INLINED {
     constexpr int h = decltype(half)::value;
     arrive<kLater>();                // the next stage is there, and no wave reads this one any more
     prepare(kb + T::STAGES + 1);
-    const int next = after(slot);
+    const int next = slot == T::STAGES - 1 ? 0 : slot + 1;
     for_constants<T::TP>([&](auto row) INLINED {
       constexpr int i = decltype(row)::value;
 #pragma unroll
-      for (int j = 0; j < T::TQ; j++) {
+      for (int j = 0; j < ACTIVE; j++) {
         mfma_agpr(p[h][i], q[h][j], acc[i][j]);
-        if (j == 1 && i < 4) {       // (behind MFMAs, which need not wait for these reads)
-          __builtin_amdgcn_sched_barrier(0);
-          read(std::integral_constant<int, 1 - h>(), lds + next * T::kStage, i);   // (past the end: zeros)
+        // (past the end: zeros)
+        constexpr int kReads = 4, kPer = ACTIVE >= 8 ? 1 : ACTIVE >= 4 ? 2 : 4;   // reads of a row of MFMAs, after one of them
+        if (i < 4 && j >= 1 && (j - 1) * kPer < kReads) {
+#pragma unroll
+          for (int n = 0; n < kPer; n++) read(std::integral_constant<int, 1 - h>(), lds + next * T::kStage, i * kReads + (j - 1) * kPer + n);
         }
-        if (j == 4) issue(row, kb + T::STAGES, lds0 + slot * T::kStage);
+        if (j == (ACTIVE > 4 ? 6 : ACTIVE - 1)) issue(row, kb + T::STAGES, lds0 + slot * T::kStage);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
     });
     advance(kb + T::STAGES + 1);
     slot = next;
   };
   arrive<kLater + T::kCopies>();     // stage 0 is there
 #pragma unroll
-  for (int i = 0; i < 4; i++) read(std::integral_constant<int, 0>(), lds, i);
+  for (int i = 0; i < 2 * T::TP; i++) read(std::integral_constant<int, 0>(), lds, i);
   for (int kb = 0; kb < steps; kb += 2) {
     stage_of(std::integral_constant<int, 0>(), kb);
     stage_of(std::integral_constant<int, 1>(), kb + 1);   // (an odd number of stages: one of zeros)
   }
   settle();
   arrive<0>();
+}
+
+// run(ACTIVE) for `rows` rows of Q in use.  The last chunk of a group of, say, 540 rows has 28: 2 of a
+// wave's 8 tiles.
+template <class T, class F>
+__device__ __forceinline__ void with_active(int rows, F run) {
+  const int tiles = (rows + 16 * T::WQ - 1) / (16 * T::WQ);
+  if (tiles > 4) run(std::integral_constant<int, 8>());
+  else if (tiles > 2) run(std::integral_constant<int, 4>());
+  else run(std::integral_constant<int, 2>());
 }
 
 // ---- results --------------------------------------------------------------------------------
@@ -479,19 +485,15 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
   }
 
   float4v acc[T::TP][T::TQ];
-  // the weights of a group of one chunk are read by this workgroup alone
-  const bool once = g.total == 1 && P.stream_weights;
   if constexpr (T::kLarge) {
-    auto large = [&](auto streamed) {
-      constexpr bool kOnce = decltype(streamed)::value;
-      contract_large<T>(
-          [&](auto j, int kb, uint32_t at) INLINED { issue_one<T, kOnce>(src, at, wave, j, kb == steps - 1 && src.last < T::STEP); },
-          [](int) INLINED {}, [&](int kb) INLINED { advance_to<T>(src, kb, steps); },
-          lds, steps, count, acc);
-    };
-    if (once) large(std::true_type());
-    else large(std::false_type());
+    with_active<T>(count, [&](auto active) INLINED {
+      contract_large<T, decltype(active)::value>(
+          [&](auto j, int kb, uint32_t at) INLINED { issue_one<T, false>(src, at, wave, j, kb == steps - 1 && src.last < T::STEP); },
+          [](int) INLINED {}, [&](int kb) INLINED { advance_to<T>(src, kb, steps); }, lds, steps, acc);
+    });
   } else {
+    // the weights of a group of one chunk are read by this workgroup alone
+    const bool once = g.total == 1 && P.stream_weights;
     // Q tiles behind the last row are left out
     auto run = [&](auto active) {
       constexpr int kActive = decltype(active)::value;
@@ -507,12 +509,12 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
 
   const int wp = wave % T::WP, wq = wave / T::WP;
   constexpr int kCols = kPanelCols / T::WP;           // a wave's columns of a panel
-  const int t0 = wq * T::TQ * 16;                     // its first row of the tile
   if (MODE == kPlain) {
     turn<T, T::TP>(lds, [&](int ti, int j) { return acc[ti][j]; },
                    [&](int row, int col, const uint4 &v) {
+                     const int t = row_of_tile<T>(wq, row);
                      const int n = n0 + col / kCols * kPanelCols + wp * kCols + col % kCols;
-                     if (t0 + row < count && n < P.N) store16<T::kLarge>(P.D + static_cast<int64_t>(first + t0 + row) * P.N + n, v);
+                     if (t < count && n < P.N) store16<T::kLarge>(P.D + static_cast<int64_t>(first + t) * P.N + n, v);
                    });
   } else if (MODE == kGated) {
     const int i0 = n0 + wp * kCols;
@@ -521,8 +523,9 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
       for (int half = 0; half < T::kHalves; half++)
         turn<T, T::kPerHalf>(lds, [&](int ti, int j) { return acc[half * T::kPerHalf + ti][j]; },
                              [&](int row, int col, const uint4 &v) {
-                               if (t0 + row < count && i0 + col < width)
-                                 store16<T::kLarge>(P.Z + static_cast<int64_t>(first + t0 + row) * P.N + half * width + i0 + col, v);
+                               const int t = row_of_tile<T>(wq, row);
+                               if (t < count && i0 + col < width)
+                                 store16<T::kLarge>(P.Z + static_cast<int64_t>(first + t) * P.N + half * width + i0 + col, v);
                              });
     }
     turn<T, T::kPerHalf>(lds,
@@ -536,14 +539,16 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
                            return act;
                          },
                          [&](int row, int col, const uint4 &v) {
-                           if (t0 + row < count && i0 + col < width)
-                             store16<T::kLarge>(P.D + static_cast<int64_t>(first + t0 + row) * width + i0 + col, v);
+                           const int t = row_of_tile<T>(wq, row);
+                           if (t < count && i0 + col < width)
+                             store16<T::kLarge>(P.D + static_cast<int64_t>(first + t) * width + i0 + col, v);
                          });
   } else {
     turn_f32<T, T::TP>(lds, acc, [&](int row, int col, const float4v &lo, const float4v &hi) {
       const int n = n0 + col / kCols * kPanelCols + wp * kCols + col % kCols;
-      if (t0 + row >= count || n >= P.N) return;
-      const int64_t at = static_cast<int64_t>(first + t0 + row) * 2 * P.N + n;
+      const int t = row_of_tile<T>(wq, row);
+      if (t >= count || n >= P.N) return;
+      const int64_t at = static_cast<int64_t>(first + t) * 2 * P.N + n;
       const uint4 gate = *reinterpret_cast<const uint4 *>(P.Z + at), up = *reinterpret_cast<const uint4 *>(P.Z + at + P.N);
       float4v dg[2], du[2];
 #pragma unroll
@@ -681,12 +686,16 @@ __global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams
 
 // ---- the weight gradient -----------------------------------------------------------------------
 
-typedef const __attribute__((address_space(4))) int32_t *const_rows;   // read through scalar loads
+// Read through scalar loads.
+typedef const __attribute__((address_space(4))) int32_t *const_rows;
+typedef int int16x __attribute__((ext_vector_type(16)));
+typedef int int16x_unaligned __attribute__((ext_vector_type(16), aligned(4)));
+typedef const __attribute__((address_space(4))) int16x_unaligned *const_rows16;
 
 // One tile of D: Q is Y's columns n, P is X's columns k, the contraction the tokens of group e.
 template <class T, bool BF16, bool GATHER>
 __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P) {
-  static_assert(T::PT && T::QT && (T::kLarge || (T::STAGES == 2 && T::STEP == 64)), "the schedules");
+  static_assert(T::PT && T::QT, "columns of X and Y");
   __shared__ __align__(1024) uint8_t lds[T::kLds];
   const int n_tiles = (P.N + T::BQ - 1) / T::BQ, k_tiles = (P.K + T::BP - 1) / T::BP, per = n_tiles * k_tiles;
   int64_t w;
@@ -724,41 +733,41 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
     src.vp[j] = k0 + col < P.K ? (static_cast<uint32_t>(GATHER ? 0 : k) * P.K + k0 + col) * 2 : kOob;
   }
   const uint32_t lds0 = lds_address(lds);
-  // The byte in X of the gathered rows of a stage's copies, four rows each, come through the scalar
-  // cache, so that no vector load stands between the copies, and a stage ahead, so that none waits for
-  // them.  Past the group's end: a row past X's (its range is at most 2^31 - 4096 bytes, so no sum wraps).
-  int row_of[GATHER ? T::kCopiesP : 1][4], next_row_of[GATHER ? T::kCopiesP : 1][4];
+  // The numbers of the gathered rows of a stage's copies, four each, come through the scalar cache, so
+  // that no vector load stands between the copies, and a stage ahead, so that none waits for them.  A lane
+  // takes the one of its row; past the group's end it takes none.  (A number outside X is outside the
+  // buffer's range, or wraps to another place in it.)
+  constexpr int kRows = 4 * T::kCopiesP;
+  static_assert(kRows == 16 && T::kPanelCopies % T::kCopiesP == 0, "a wave's rows are 16 neighbours");
+  int16x row_of = {}, next_row_of = {};
   auto load_rows = [&](int kb) INLINED {
     if (!GATHER) return;
+    const int row0 = lo + kb * T::STEP + wave * T::kCopiesP % T::kPanelCopies * 4;
+    if (row0 + kRows <= P.R) {
+      next_row_of = *reinterpret_cast<const_rows16>(index + row0);
+    } else {   // (near the end of the list only: the wait for this load is one for the copies under way too)
+      const int mine = P.X_rows[min(row0 + lane % kRows, P.R - 1)];
 #pragma unroll
-    for (int j = 0; j < T::kCopiesP; j++) {
-      const int row0 = lo + kb * T::STEP + (wave * T::kCopiesP + j) % T::kPanelCopies * 4;
-#pragma unroll
-      for (int q = 0; q < 4; q++) next_row_of[j][q] = index[min(row0 + q, P.R - 1)];
+      for (int q = 0; q < kRows; q++) next_row_of[q] = __builtin_amdgcn_readlane(mine, q);
     }
   };
-  auto take_rows = [&]() INLINED {
-    if (!GATHER) return;
-#pragma unroll
-    for (int j = 0; j < T::kCopiesP; j++)
-#pragma unroll
-      for (int q = 0; q < 4; q++) row_of[j][q] = next_row_of[j][q];
-  };
+  auto take_rows = [&]() INLINED { row_of = next_row_of; };
   load_rows(0);
   take_rows();
+  const uint32_t row_bytes = static_cast<uint32_t>(P.K) * 2;
   auto issue_copy = [&](auto number, int kb, uint32_t at) INLINED {
     constexpr int j = decltype(number)::value;
     if constexpr (!GATHER || j >= T::kCopiesP) {
       issue_one<T, false>(src, at, wave, j, false);
     } else {
-      const int c = wave * T::kCopiesP + j, row0 = lo + kb * T::STEP + c % T::kPanelCopies * 4, most = static_cast<int>(P.rows_X);
-      int row = 0;
+      const int c = wave * T::kCopiesP + j, k = kb * T::STEP + c % T::kPanelCopies * 4 + lane / 16;
+      int row[4] = {row_of[4 * j], row_of[4 * j + 1], row_of[4 * j + 2], row_of[4 * j + 3]};
 #pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const int v = row0 + q < hi ? min(max(row_of[j][q], 0), most - 1) : most;
-        if (lane / 16 == q) row = v;
-      }
-      copy16(src.p, at + c * 1024, src.vp[j] + static_cast<uint32_t>(row) * static_cast<uint32_t>(P.K) * 2);
+      for (int q = 0; q < 4; q++) asm("" : "+s"(row[q]));   // (or they become one element with a variable index)
+      const int a = lane / 16 & 1 ? row[1] : row[0], b = lane / 16 & 1 ? row[3] : row[2];
+      uint32_t from = src.vp[j] + static_cast<uint32_t>(lane / 32 ? b : a) * row_bytes;
+      asm volatile("" : "+v"(from));   // (or the compiler branches around the product, four times a stage)
+      copy16(src.p, at + c * 1024, k < rows ? from : kOob);
     }
   };
   auto advance = [&](int kb) INLINED {
@@ -772,46 +781,50 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
   };
   float4v acc[T::TP][T::TQ];
   if constexpr (T::kLarge) {
-    contract_large<T>(issue_copy, load_rows, advance, lds, steps, P.N - n0, acc);
+    with_active<T>(P.N - n0, [&](auto active) INLINED { contract_large<T, decltype(active)::value>(issue_copy, load_rows, advance, lds, steps, acc); });
   } else {
     const int g = lane / 16, r = lane % 16, wp = wave % T::WP, wq = wave / T::WP;
-    auto issue_stage = [&](int kb) INLINED {
+    constexpr int kHalvesK = T::STEP / 32;
+    auto issue_stage = [&](int kb, int slot) INLINED {
       load_rows(kb + 1);
-      for_constants<T::kCopies>([&](auto j) INLINED { issue_copy(j, kb, lds0 + (kb & 1) * T::kStage); });
+      for_constants<T::kCopies>([&](auto j) INLINED { issue_copy(j, kb, lds0 + slot * T::kStage); });
       advance(kb + 1);
     };
     clear<T>(acc);
-    issue_stage(0);
-    for (int kb = 0; kb < steps; kb++) {
-      arrive<0>();
-      issue_stage(kb + 1);
-      const uint8_t *Ps = lds + (kb & 1) * T::kStage, *Qs = Ps + T::kBytesP;
-      bf16x8 q[2][T::TQ];
 #pragma unroll
-      for (int h = 0; h < 2; h++)
+    for (int i = 0; i < T::STAGES - 1; i++) issue_stage(i, i);
+    int slot = 0;
+    for (int kb = 0; kb < steps; kb++) {
+      arrive<T::kCopies *(T::STAGES - 2)>();
+      issue_stage(kb + T::STAGES - 1, slot == 0 ? T::STAGES - 1 : slot - 1);
+      const uint8_t *Ps = lds + slot * T::kStage, *Qs = Ps + T::kBytesP;
+      bf16x8 q[kHalvesK][T::TQ];
+#pragma unroll
+      for (int h = 0; h < kHalvesK; h++)
 #pragma unroll
         for (int j = 0; j < T::TQ; j++) q[h][j] = fragment_q<T>(Qs, wq, j, h, g, r);
 #pragma unroll
       for (int i = 0; i < T::TP; i++)
 #pragma unroll
-        for (int h = 0; h < 2; h++) mfma_row<T>(fragment_p<T>(Ps, wp, i / T::kPerHalf, i % T::kPerHalf, h, g, r), q[h], acc[i]);
+        for (int h = 0; h < kHalvesK; h++) mfma_row<T>(fragment_p<T>(Ps, wp, i / T::kPerHalf, i % T::kPerHalf, h, g, r), q[h], acc[i]);
+      slot = slot == T::STAGES - 1 ? 0 : slot + 1;
     }
     arrive<0>();
   }
-  const int wp = wave % T::WP, wq = wave / T::WP, t0 = n0 + wq * T::TQ * 16;
+  const int wp = wave % T::WP, wq = wave / T::WP;
   constexpr int kCols = kPanelCols / T::WP;
   auto column = [&](int col) { return k0 + col / kCols * kPanelCols + wp * kCols + col % kCols; };
   if (BF16) {
     uint16_t *D = static_cast<uint16_t *>(P.D);
     turn<T, T::TP>(lds, [&](int ti, int j) { return acc[ti][j]; },
                    [&](int row, int col, const uint4 &v) {
-                     const int n = t0 + row, k = column(col);
+                     const int n = n0 + row_of_tile<T>(wq, row), k = column(col);
                      if (n < P.N && k < P.K) store16<true>(D + (static_cast<int64_t>(e) * P.N + n) * P.K + k, v);
                    });
   } else {
     float *D = static_cast<float *>(P.D);
     turn_f32<T, T::TP>(lds, acc, [&](int row, int col, const float4v &a, const float4v &b) {
-      const int n = t0 + row, k = column(col);
+      const int n = n0 + row_of_tile<T>(wq, row), k = column(col);
       if (n >= P.N || k >= P.K) return;
       float *at = D + (static_cast<int64_t>(e) * P.N + n) * P.K + k;
       store16<true>(at, __builtin_bit_cast(uint4, a));
