@@ -390,11 +390,11 @@ __device__ __forceinline__ void turn(uint8_t *lds, V value, S store) {
   }
 }
 
-// The same with binary32 values, handed over as 8 at a time.
-template <class T, int NT, class S>
+// The same with binary32 values, handed over COUNT = 4 or 8 at a time, the address of the first.
+template <class T, int NT, int COUNT, class S>
 __device__ __forceinline__ void turn_f32(uint8_t *lds, const float4v (&acc)[NT][T::TQ], S store) {
-  constexpr int kRow = NT * 64, kStride = kRow + 16, kPieces = kRow / 128;   // bytes
-  static_assert(kPieces >= 1 && kPieces * 128 == kRow && T::kWaves * 16 * kStride <= T::kLds, "staging");
+  constexpr int kRow = NT * 64, kStride = kRow + 16, kPieces = kRow / (COUNT * 16);   // bytes
+  static_assert(kPieces >= 1 && kPieces * COUNT * 16 == kRow && T::kWaves * 16 * kStride <= T::kLds, "staging");
   const int lane = threadIdx.x & 63, lg = lane / 16, r = lane % 16;
   uint8_t *mine = lds + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * 16 * kStride;
 #pragma unroll
@@ -404,9 +404,8 @@ __device__ __forceinline__ void turn_f32(uint8_t *lds, const float4v (&acc)[NT][
     wave_order();
 #pragma unroll
     for (int c = 0; c < kPieces; c++) {
-      const int at = c * kWave + lane, row = at / (kRow / 32), col = at % (kRow / 32) * 8;
-      const float4v *v = reinterpret_cast<const float4v *>(mine + row * kStride + col * 4);
-      store(j * 16 + row, col, v[0], v[1]);
+      const int at = c * kWave + lane, row = at / (kRow / 4 / COUNT), col = at % (kRow / 4 / COUNT) * COUNT;
+      store(j * 16 + row, col, reinterpret_cast<const float4v *>(mine + row * kStride + col * 4));
     }
     wave_order();
   }
@@ -544,7 +543,8 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
                              store16<T::kLarge>(P.D + static_cast<int64_t>(first + t) * width + i0 + col, v);
                          });
   } else {
-    turn_f32<T, T::TP>(lds, acc, [&](int row, int col, const float4v &lo, const float4v &hi) {
+    turn_f32<T, T::TP, 8>(lds, acc, [&](int row, int col, const float4v *v) {
+      const float4v lo = v[0], hi = v[1];
       const int n = n0 + col / kCols * kPanelCols + wp * kCols + col % kCols;
       const int t = row_of_tile<T>(wq, row);
       if (t >= count || n >= P.N) return;
@@ -823,12 +823,9 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
                    });
   } else {
     float *D = static_cast<float *>(P.D);
-    turn_f32<T, T::TP>(lds, acc, [&](int row, int col, const float4v &a, const float4v &b) {
+    turn_f32<T, T::TP, 4>(lds, acc, [&](int row, int col, const float4v *v) {
       const int n = n0 + row_of_tile<T>(wq, row), k = column(col);
-      if (n >= P.N || k >= P.K) return;
-      float *at = D + (static_cast<int64_t>(e) * P.N + n) * P.K + k;
-      store16<true>(at, __builtin_bit_cast(uint4, a));
-      store16<true>(at + 4, __builtin_bit_cast(uint4, b));
+      if (n < P.N && k < P.K) store16<true>(D + (static_cast<int64_t>(e) * P.N + n) * P.K + k, __builtin_bit_cast(uint4, *v));
     });
   }
 }
@@ -867,7 +864,7 @@ hipError_t run_wgrad(const WgradParams &p, hipStream_t stream) {
 }
 
 constexpr int64_t kCacheBytes = 256 << 20;   // MI355X's memory-side cache
-constexpr int kManyTiles = 192, kLargeRows = 44, kCus = 256;
+constexpr int kCus = 256;
 
 template <bool PT>
 using Large = Tile<256, 256, 2, 2, 5, PT, false, 32>;
@@ -879,42 +876,57 @@ hipError_t launch_gemm(GemmParams p, Epilogue epilogue, bool transposed, hipStre
   if (hit == 0) return hipSuccess;
   const int64_t mean = p.R / hit;
   p.stream_weights = static_cast<int64_t>(p.E) * p.N * p.K * 2 > kCacheBytes / 2;
-  auto tiles = [&](int q, int c) { return groups::max_chunks(p.R, p.E, q) * ((p.N + c - 1) / c); };
-  // q rows by c columns of groups of the mean size: at most one tile for each CU
-  auto one_round = [&](int q, int c) { return hit * ((mean + q - 1) / q) * ((p.N + c - 1) / c) <= kCus; };
-  const bool large = mean > kLargeRows && tiles(256, 256) >= kManyTiles;
-  const bool middle = mean > 2 * kLargeRows && tiles(128, 128) >= kManyTiles;
+  // tiles of q rows by c columns, for groups of the mean size
+  auto items = [&](int q, int c) { return hit * ((mean + q - 1) / q) * ((p.N + c - 1) / c); };
+  // Which tile; times in us, "a | b" for this choice and the next one below, weights 4096 x 6144 each.
+  // - 256 x 256 where groups have more than one 128-row chunk and the tiles nearly fill the CUs, one each:
+  //   16 groups of 160 rows 201 | 231 (transposed 161 | 243, gated 215 | 260), of 128 182 | 171 (144 | 145,
+  //   190 | 206); 24 groups of 512 rows, 784 x 1048: 192 tiles, 35 | 44; 8 of 512, 2048 x 2048: 128 tiles, 46 | 39.
+  const bool large = mean > 128 && items(256, 256) >= kCus * 3 / 4;
+  // - 128 x 128 where 64 rows are not enough and there is more than one for each CU: 16 groups of 96 rows
+  //   183 | 206, of 64 151 | 145; 8 of 256, 2048 x 2048: 256 tiles, 28 | 25, of 512: 512 tiles, 38 | 46.
+  const bool middle = mean > 64 && items(128, 128) > kCus;
+  // - The contraction split over a workgroup's waves, 16 x 16 while that is one round of the CUs: one group
+  //   of 16 rows 13.1 | 16.1, of 24 20.4 | 15.4; then 16 x 32 for one round, or two where several chunks
+  //   share weights: one of 64 rows 27 | 39, of 96 39 | 40 (gated 28 | 54, 39 | 53); 8 of one row, 2048 x
+  //   2048: 512 tiles of one chunk each, 16.4 | 13.7.
+  const int split = transposed ? 0 : items(16, 16) <= kCus ? 16 : items(16, 32) <= (mean > 16 ? 2 : 1) * kCus ? 32 : 0;
+  // - 32 x 128 for one round: one group of 128 rows, transposed, 31 | 44, of 512 50 | 46.
+  const bool low = items(32, 128) <= kCus;
   if (epilogue == kGated) {
     if (large) return run_gemm<Large<false>, kGated>(p, stream);
-    if (mean <= 16 && p.K >= 256) {
-      if (one_round(16, 16)) return run_split<Split<16, 8, 3>, kGated>(p, stream);
-      if (one_round(16, 32)) return run_split<Split<32, 8, 3>, kGated>(p, stream);
-    }
-    if (one_round(32, 256)) return run_gemm<Tile<32, 256, 1, 4, 3, false>, kGated>(p, stream);
+    if (split == 16) return run_split<Split<16, 8, 3>, kGated>(p, stream);
+    if (split == 32) return run_split<Split<32, 8, 3>, kGated>(p, stream);
     return run_gemm<Tile<64, 256, 1, 8, 3, false>, kGated>(p, stream);
   }
   if (epilogue == kGatedBackward) {
     if (large) return run_gemm<Large<true>, kGatedBackward>(p, stream);
     if (middle) return run_gemm<Tile<128, 128, 2, 2, 2, true>, kGatedBackward>(p, stream);
+    if (low) return run_gemm<Tile<32, 128, 1, 4, 3, true>, kGatedBackward>(p, stream);
     return run_gemm<Tile<64, 128, 1, 4, 3, true>, kGatedBackward>(p, stream);
   }
   if (transposed) {
     if (large) return run_gemm<Large<true>, kPlain>(p, stream);
     if (middle) return run_gemm<Tile<128, 128, 2, 2, 2, true>, kPlain>(p, stream);
+    if (low) return run_gemm<Tile<32, 128, 1, 4, 3, true>, kPlain>(p, stream);
     return run_gemm<Tile<64, 128, 1, 4, 3, true>, kPlain>(p, stream);
   }
   if (large) return run_gemm<Large<false>, kPlain>(p, stream);
-  if (mean <= 16 && p.K >= 256) {
-    if (one_round(16, 16)) return run_split<Split<16, 8, 3>, kPlain>(p, stream);
-    if (one_round(16, 32)) return run_split<Split<32, 8, 3>, kPlain>(p, stream);
-  }
+  if (split == 16) return run_split<Split<16, 8, 3>, kPlain>(p, stream);
+  if (split == 32) return run_split<Split<32, 8, 3>, kPlain>(p, stream);
   if (middle) return run_gemm<Tile<128, 128, 2, 2, 2, false>, kPlain>(p, stream);
+  if (low) return run_gemm<Tile<32, 128, 1, 4, 3, false>, kPlain>(p, stream);
   return run_gemm<Tile<64, 128, 1, 4, 3, false>, kPlain>(p, stream);
 }
 
 hipError_t launch_wgrad(const WgradParams &p, bool bf16, hipStream_t stream) {
-  const int64_t large = static_cast<int64_t>(p.E) * ((p.N + 255) / 256) * ((p.K + 255) / 256);
-  if (large >= kManyTiles) {
+  // Large tiles, one for each CU at a time, need a contraction that pays for their start and end, and
+  // enough tiles or enough of it that the last round counts little.  In us, large | small, D binary32:
+  // 16 groups of 384 rows, 4096 x 6144, 477 | 500, of 256 403 | 397; 8 of 1024, 2048 x 2048, 76 | 82, of 512
+  // 54 | 54 (bf16 46 | 41); one of 4096, 4096 x 6144, 207 | 230, of 1024 72 | 65; one of 4096, 2048 x 2048:
+  // 64 tiles, 92 | 53.
+  const int64_t tiles = static_cast<int64_t>(p.E) * ((p.N + 255) / 256) * ((p.K + 255) / 256), mean = p.R / p.E;
+  if (mean >= 384 && tiles >= kCus * 3 / 4 && tiles * mean >= kCus * 2048) {
     using T = Tile<256, 256, 2, 2, 5, true, true, 32>;
     return bf16 ? run_wgrad<T, true>(p, stream) : run_wgrad<T, false>(p, stream);
   }

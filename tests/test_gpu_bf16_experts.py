@@ -67,11 +67,12 @@ def _weights(g, sizes, N, K, make=_ints, **kw):
     return W
 
 
-# which kernel takes them: 16- and 32-row split tiles, 64-row tiles, 128 and 256 squared, and their edges
+# which kernel takes them, row-major: 16- and 32-row split tiles, 32- and 64-row tiles, 128 and 256 squared, and their edges
 PRODUCTS = {
     "one row": ([1], 8, 8), "split 16": ([1, 0, 3], 24, 264), "split 16, two chunks": ([30, 0, 2], 40, 520), "split 32": ([5], 4808, 512),
-    "small": ([20, 0, 40, 7], 200, 72), "small, full chunks": ([64, 128, 1], 136, 64), "many small": ([3] * 90 + [0] * 30, 72, 136),
-    "middle": ([130, 200, 0, 95], 6400, 136), "middle, one step": ([256, 128], 12800, 40), "large": ([300, 0, 517, 45], 10240, 200),
+    "split 32, two chunks": ([40, 20, 0], 2056, 136), "split 32, short": ([20, 0, 40, 7], 1000, 72), "32 rows": ([64, 128, 1], 2600, 64),
+    "64 rows": ([20] * 40 + [0, 70], 1024, 136), "full chunks": ([64, 128, 1], 13000, 64), "many small": ([3] * 90 + [0] * 30, 72, 136),
+    "middle": ([130, 200, 0, 95], 6400, 136), "middle, one step": ([256, 128], 12800, 40), "large": ([300, 0, 517, 45], 12808, 200),
     "large, one step": ([600, 90], 16392, 8), "large, two steps": ([256, 512], 12288, 128), "1024 experts": ([1] * 1000 + [0] * 20 + [50] * 4, 16, 72),
 }
 
@@ -94,8 +95,8 @@ def test_product(name, transposed, gather):
 
 GATED = {
     "one row": ([1], 8, 8), "split 16": ([1, 0, 3], 24, 264), "split 16, two chunks": ([30, 0, 2], 40, 520), "split 32": ([5], 2408, 512),
-    "32 rows": ([40, 0, 20], 264, 72), "64 rows": ([20] * 40 + [0, 70], 1024, 136), "short K": ([9, 100], 136, 8),
-    "large": ([300, 0, 517, 45], 5000, 200), "large, one step": ([600, 90], 8200, 64),
+    "split 32, two chunks": ([40, 0, 20], 1032, 72), "64 rows": ([20] * 40 + [0, 70], 1024, 136), "short K": ([9, 100], 136, 8),
+    "large": ([300, 0, 517, 45], 6408, 200), "large, one step": ([600, 90], 8200, 64),
 }
 
 
@@ -118,8 +119,8 @@ def test_gated(name, gather):
     assert torch.equal(act, again)
 
 
-BACKWARD = {"one row": ([1], 8, 8), "small": ([20, 0, 40, 7], 200, 72), "full chunks": ([64, 128, 1], 136, 64), "many small": ([3] * 90 + [0] * 30, 72, 136),
-            "middle": ([130, 200, 0, 95], 6400, 136), "large": ([300, 0, 517, 45], 10240, 200), "large, one step": ([600, 90], 16392, 8)}
+BACKWARD = {"one row": ([1], 8, 8), "small": ([20, 0, 40, 7], 200, 72), "32 rows": ([64, 128, 1], 136, 64), "64 rows": ([20] * 40 + [0, 70], 1024, 136),
+            "many small": ([3] * 90 + [0] * 30, 72, 136), "middle": ([130, 200, 0, 95], 6400, 136), "large": ([300, 0, 517, 45], 12808, 200), "large, one step": ([600, 90], 16392, 8)}
 
 
 @pytest.mark.parametrize("name", BACKWARD)
@@ -141,7 +142,7 @@ def test_gated_backward(name):
 
 
 WGRADS = {"one row": ([1], 8, 8), "small": ([20, 0, 40, 7], 200, 72), "whole steps": ([64, 128, 0, 1], 136, 264), "long": ([3000], 72, 136),
-          "many": ([3, 0, 65] * 30, 40, 24), "large": ([300, 0, 517, 45, 64], 2568, 1032), "large, one step": ([10] * 200, 256, 264)}
+          "many": ([3, 0, 65] * 30, 40, 24), "wide": ([300, 0, 517, 45, 64], 2568, 1032), "large": ([5000, 8, 0, 40, 4609], 2568, 1032), "large, one group": ([2825], 3336, 3592)}
 
 
 @pytest.mark.parametrize("gather", [False, True], ids=["own rows", "gathered"])
