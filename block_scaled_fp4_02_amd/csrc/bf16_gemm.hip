@@ -418,16 +418,41 @@ __device__ __forceinline__ float element(const uint4 &v, int i) {
 
 // ---- the product ----------------------------------------------------------------------------
 
-// The item of this workgroup: group g, its chunk of `size` rows and n tile.
-__device__ __forceinline__ bool find_item(const GemmParams &P, int size, groups::Chunk &g, int &chunk, int &nt) {
+// Items of the large tile, of which a CU holds one at a time: where the items that an XCD has beyond whole
+// rounds of its CUs are at most half a round (a quarter), each is cut into two (four) along Q, for a
+// last round of half (a quarter of) the time.  Part `part` of the tile has rows from part * Q / parts on.
+constexpr int kXcdCus = 32, kMostParts = 24;   // more workgroups for an XCD's cut items
+__device__ __forceinline__ bool part_of(int b, int64_t count, int64_t &w, int &part, int &parts) {
+  const int64_t per = (count + kXcds - 1) / kXcds, first = b % kXcds * per;
+  const int64_t mine = min(per, count - first), whole = mine <= 0 ? 0 : mine / kXcdCus * kXcdCus, rest = mine - whole, i = b / kXcds;
+  parts = rest <= kXcdCus / 4 ? 4 : rest <= kXcdCus / 2 ? 2 : 1;
+  part = 0;
+  if (i < whole) {
+    parts = 1;
+    w = first + i;
+    return true;
+  }
+  const int64_t at = (i - whole) / parts;
+  part = static_cast<int>((i - whole) % parts);
+  w = first + whole + at;
+  return at < rest;
+}
+
+// The item of this workgroup: group g, `count` rows of it from row `first` on, and n tile.
+template <int SIZE, bool LARGE>
+__device__ __forceinline__ bool find_item(const GemmParams &P, groups::Chunk &g, int &first, int &count, int &nt) {
   int64_t w = 0;
-  int i;
+  int i, chunk, part = 0, parts = 1;
   auto index = [&](int total) {
-    return item_of(blockIdx.x, static_cast<int64_t>(total) * P.n_tiles, w) ? static_cast<int>(w / P.n_tiles) : -1;
+    const int64_t items = static_cast<int64_t>(total) * P.n_tiles;
+    return (LARGE ? part_of(blockIdx.x, items, w, part, parts) : item_of(blockIdx.x, items, w)) ? static_cast<int>(w / P.n_tiles) : -1;
   };
-  if (!groups::find_chunk_of_all(P.offsets, P.E, P.R, size, index, i, g)) return false;
+  if (!groups::find_chunk_of_all(P.offsets, P.E, P.R, SIZE, index, i, g)) return false;
   place_in_band(static_cast<int>(w - static_cast<int64_t>(i - g.index) * P.n_tiles), g.total, P.n_tiles, chunk, nt);
-  return true;
+  const int size = SIZE / parts;
+  first = g.lo + chunk * SIZE + part * size;
+  count = min(size, g.hi - first);
+  return count > 0;
 }
 
 // Row number v of an operand of `rows` rows, kept inside it.
@@ -438,9 +463,8 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
   static_assert(MODE != kGated || (T::kHalves == 2 && !T::PT), "gate and up panels");
   __shared__ __align__(1024) uint8_t lds[T::kLds];
   groups::Chunk g;
-  int chunk, nt;
-  if (!find_item(P, T::BQ, g, chunk, nt)) return;
-  const int first = g.lo + chunk * T::BQ, count = min(T::BQ, g.hi - first);
+  int first, count, nt;
+  if (!find_item<T::BQ, T::kLarge>(P, g, first, count, nt)) return;
   const int width = MODE == kGated ? P.N / 2 : P.N;   // columns of act, or of y
   const int n0 = nt * (MODE == kGated ? kPanelCols : T::BP);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -586,9 +610,8 @@ __global__ __launch_bounds__(T::WAVES *kWave) void split_kernel(const GemmParams
   static_assert(MODE != kGatedBackward, "weights along the contraction");
   __shared__ __align__(1024) uint8_t lds[T::kLds];
   groups::Chunk g;
-  int chunk, nt;
-  if (!find_item(P, T::Q, g, chunk, nt)) return;
-  const int first = g.lo + chunk * T::Q, count = min(T::Q, g.hi - first);
+  int first, count, nt;
+  if (!find_item<T::Q, false>(P, g, first, count, nt)) return;
   constexpr int kTile = MODE == kGated ? 8 : 16;      // columns of the result in a 16-row tile
   const int width = MODE == kGated ? P.N / 2 : P.N, n0 = nt * T::TP * kTile;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -699,11 +722,13 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
   __shared__ __align__(1024) uint8_t lds[T::kLds];
   const int n_tiles = (P.N + T::BQ - 1) / T::BQ, k_tiles = (P.K + T::BP - 1) / T::BP, per = n_tiles * k_tiles;
   int64_t w;
-  if (!item_of(blockIdx.x, static_cast<int64_t>(P.E) * per, w)) return;
+  int part = 0, parts = 1;
+  if (!(T::kLarge ? part_of(blockIdx.x, static_cast<int64_t>(P.E) * per, w, part, parts) : item_of(blockIdx.x, static_cast<int64_t>(P.E) * per, w))) return;
   const int e = static_cast<int>(w / per);
   int nt, kt;
   place_in_band(static_cast<int>(w - static_cast<int64_t>(e) * per), n_tiles, k_tiles, nt, kt);
-  const int n0 = nt * T::BQ, k0 = kt * T::BP;
+  const int n0 = nt * T::BQ + part * (T::BQ / parts), k0 = kt * T::BP, n1 = min(n0 + T::BQ / parts, P.N);
+  if (n0 >= n1) return;
   int lo = __builtin_amdgcn_readfirstlane(P.offsets[e]), hi = __builtin_amdgcn_readfirstlane(P.offsets[e + 1]);
   groups::clamp_pair(lo, hi, P.R);
   const int rows = hi - lo, steps = (rows + T::STEP - 1) / T::STEP;
@@ -724,7 +749,7 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
   for (int j = 0; j < T::kCopiesQ; j++) {
     int k, col;
     place_across<T>(wave * T::kCopiesQ + j, k, col);
-    src.vq[j] = n0 + col < P.N ? (static_cast<uint32_t>(k) * P.N + n0 + col) * 2 : kOob;
+    src.vq[j] = n0 + col < n1 ? (static_cast<uint32_t>(k) * P.N + n0 + col) * 2 : kOob;
   }
 #pragma unroll
   for (int j = 0; j < T::kCopiesP; j++) {
@@ -781,7 +806,7 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
   };
   float4v acc[T::TP][T::TQ];
   if constexpr (T::kLarge) {
-    with_active<T>(P.N - n0, [&](auto active) INLINED { contract_large<T, decltype(active)::value>(issue_copy, load_rows, advance, lds, steps, acc); });
+    with_active<T>(n1 - n0, [&](auto active) INLINED { contract_large<T, decltype(active)::value>(issue_copy, load_rows, advance, lds, steps, acc); });
   } else {
     const int g = lane / 16, r = lane % 16, wp = wave % T::WP, wq = wave / T::WP;
     constexpr int kHalvesK = T::STEP / 32;
@@ -819,13 +844,13 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
     turn<T, T::TP>(lds, [&](int ti, int j) { return acc[ti][j]; },
                    [&](int row, int col, const uint4 &v) {
                      const int n = n0 + row_of_tile<T>(wq, row), k = column(col);
-                     if (n < P.N && k < P.K) store16<true>(D + (static_cast<int64_t>(e) * P.N + n) * P.K + k, v);
+                     if (n < n1 && k < P.K) store16<true>(D + (static_cast<int64_t>(e) * P.N + n) * P.K + k, v);
                    });
   } else {
     float *D = static_cast<float *>(P.D);
     turn_f32<T, T::TP, 4>(lds, acc, [&](int row, int col, const float4v *v) {
       const int n = n0 + row_of_tile<T>(wq, row), k = column(col);
-      if (n < P.N && k < P.K) store16<true>(D + (static_cast<int64_t>(e) * P.N + n) * P.K + k, __builtin_bit_cast(uint4, *v));
+      if (n < n1 && k < P.K) store16<true>(D + (static_cast<int64_t>(e) * P.N + n) * P.K + k, __builtin_bit_cast(uint4, *v));
     });
   }
 }
@@ -836,8 +861,8 @@ template <class T, Epilogue MODE>
 hipError_t run_gemm(GemmParams p, hipStream_t stream) {
   p.n_tiles = MODE == kGated ? (p.N / 2 + kPanelCols - 1) / kPanelCols : (p.N + T::BP - 1) / T::BP;
   const int64_t items = groups::max_chunks(p.R, p.E, T::BQ) * p.n_tiles;
-  const int64_t grid = (items + kXcds - 1) / kXcds * kXcds;
-  if (grid > 0) hipLaunchKernelGGL((gemm_kernel<T, MODE>), dim3(static_cast<uint32_t>(grid)), dim3(T::kThreadsT), 0, stream, p);
+  const int64_t grid = ((items + kXcds - 1) / kXcds + (T::kLarge ? kMostParts : 0)) * kXcds;
+  if (items > 0) hipLaunchKernelGGL((gemm_kernel<T, MODE>), dim3(static_cast<uint32_t>(grid)), dim3(T::kThreadsT), 0, stream, p);
   return hipGetLastError();
 }
 
@@ -855,7 +880,7 @@ hipError_t run_split(GemmParams p, hipStream_t stream) {
 template <class T, bool BF16>
 hipError_t run_wgrad(const WgradParams &p, hipStream_t stream) {
   const int64_t items = static_cast<int64_t>(p.E) * ((p.N + T::BQ - 1) / T::BQ) * ((p.K + T::BP - 1) / T::BP);
-  const int64_t grid = (items + kXcds - 1) / kXcds * kXcds;
+  const int64_t grid = ((items + kXcds - 1) / kXcds + (T::kLarge ? kMostParts : 0)) * kXcds;
   if (p.X_rows != nullptr)
     hipLaunchKernelGGL((wgrad_kernel<T, BF16, true>), dim3(static_cast<uint32_t>(grid)), dim3(T::kThreadsT), 0, stream, p);
   else
