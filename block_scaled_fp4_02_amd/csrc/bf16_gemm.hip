@@ -11,14 +11,16 @@
 // (weight rows n; columns k of dW) gives the MFMA's rows, of which a lane holds 4 consecutive ones, so
 // results are contiguous along P; the "column" operand Q (tokens; rows n of dW) gives its columns.
 //
-// A stage holds 64 elements of the contraction of both operands, in panels of 128 rows or columns
-// (16 KB), copied from memory straight into LDS (16 bytes per lane, no registers).  An operand whose
-// rows run along the contraction keeps 128 bytes of a row together in 8 pieces; row r has piece c at
-// place c ^ ((r >> 1) & 7), so the 16 rows that 16 lanes read together fall on all 64 banks once.  An
-// operand whose rows run across it (b transposed, both operands of dW) keeps 256 bytes of each of 64
-// rows, in 8 pairs of pieces of 16 columns, and is read through the transposing LDS load: 16 lanes
-// read four rows of a pair and each gets one column's four elements.  Row k has pair c at place c ^
-// (k & 3 | (k >> 3 & 1) << 2): the eight rows that 32 lanes read together fall on all banks once.
+// A stage holds 64 elements of the contraction of both operands (32 in the large tile), in panels of 128
+// rows or columns, copied from memory straight into LDS (16 bytes per lane, no registers).  An operand
+// whose rows run along the contraction keeps 128 bytes of a row together in 8 pieces (64 in 4); row r has
+// piece c at place c ^ ((r >> 1) & 7) (c ^ (-(r >> 2) & 3)), so the 16 lanes that read together, which are
+// rows 0-3 and 12-15 of one lane group and 4-11 of the next, or the other way round, fall on all 64 banks
+// once.  (With c ^ ((r >> 2) & 3) half of the LDS cycles of the large tile were conflicts; now 3 %.)  An
+// operand whose rows run across it (b transposed, both operands of dW) keeps 256 bytes of each row of the
+// stage, in 8 pairs of pieces of 16 columns, and is read through the transposing LDS load: 16 lanes read
+// four rows of a pair and each gets one column's four elements.  Row k has pair c at place c ^ (k & 3 |
+// (k >> 3 & 1) << 2): the eight rows that 32 lanes read together fall on all banks once.
 // The copies are range-checked and what lies outside an operand arrives as zeros, in both
 // operands, so nothing outside (a NaN, an infinity) meets a zero.
 #include "bf16_gemm.hpp"
@@ -92,7 +94,7 @@ __device__ __forceinline__ void for_constants(F f) {
 // The place of piece c of row r along the contraction among the row's pieces, or back.
 template <class S>
 __device__ __forceinline__ int swizzle_along(int r, int c) {
-  return S::kPieces == 8 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
+  return S::kPieces == 8 ? c ^ ((r >> 1) & 7) : c ^ (-(r >> 2) & 3);
 }
 // What copy number c moves in this lane.  Along: 16-byte piece `piece` of row `row` of the operand.
 // Across: row `k` of the stage, columns from `col`.
