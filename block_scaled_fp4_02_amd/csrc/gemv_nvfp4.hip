@@ -178,6 +178,7 @@ __device__ __forceinline__ void consume(const uint8_t *stage, int K, int step, f
       const uint32_t lo = *reinterpret_cast<const uint32_t *>(stage + S::kScales + t * 512 + r * 16 + g * 4);
       const uint32_t hi = *reinterpret_cast<const uint32_t *>(stage + S::kScales + t * 512 + 256 + r * 16 + g * 4);
       w[t].scale = r * (K / 16) % 4 ? lo >> 16 | hi << 16 : lo;
+      if (step * kStep + g * 64 + 32 >= K) w[t].scale &= 0xffff;   // the next row's scales, which may be NaN
     }
   }
 #pragma unroll
@@ -276,12 +277,13 @@ __global__ __launch_bounds__(S::WAVES *kWave) void gemv_kernel(const Params P) {
   constexpr int kCols = MODE == kGated ? 16 : 32;   // columns of the result in a pair of tiles
   const int pairs = (width + kCols - 1) / kCols, steps = (P.K + kStep - 1) / kStep;
 
-  // SINGLE: slot j's expert is in lane j (-1: dropped); every wave writes the same factors
+  // SINGLE: slot j's expert is in lane j (-1: dropped); every wave writes the same ids and factors
   int my_id = -1;
   if (SINGLE && lane < P.k) {
     const int id = P.ids ? P.ids[lane] : 0;
     const bool in = id >= 0 && id < P.E;
     if (in) my_id = id;
+    groups.id[lane] = my_id;
     groups.coef[lane] = in ? P.B_gs[id] * (MODE == kWeighted && P.topk_w ? P.topk_w[lane] : 1.0f) : 0.f;
   }
   if (SINGLE) wave_order();
@@ -421,6 +423,7 @@ __global__ __launch_bounds__(S::WAVES *kWave) void gemv_kernel(const Params P) {
   auto store = [&](int q, int t, int col, float a, float b) {
     const int i = q / pairs, n = (q - i * pairs) * kCols + col, j = slot(i, t);
     if (j < 0) return;
+    if (SINGLE && groups.id[i] < 0) a = b = 0.f;   // (no weights times an infinity is a NaN)
     const float f = coef(i, t, j);
     uint16_t *at = P.D + (static_cast<int64_t>(t0 + t) * P.k + j) * width + n;
     if (MODE == kGated) {

@@ -142,6 +142,37 @@ def test_a_tokens_nan_stays_in_it():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T", [1, 3])
+def test_a_dropped_slots_row_is_zero_whatever_its_tokens_hold(T):
+    g = _gen(14)
+    W, x = _exact_weights(g, 4, 32, 256), torch.randint(-3, 4, (3 * T, 256), generator=g, device="cuda").to(BF16)
+    ids = torch.tensor([[1, -1, 3]] * T, dtype=torch.int32, device="cuda")
+    for epilogue in (moe.MOE_EPI_NONE, moe.MOE_EPI_SWIGLU, moe.MOE_EPI_FINALIZE):
+        want = moe.gemv_nvfp4_alloc(x, W, ids, epilogue=epilogue)
+        for bad in (float("inf"), float("nan")):
+            y = x.clone()
+            y[1::3] = bad
+            for V in _layouts(W):
+                assert torch.equal(moe.gemv_nvfp4_alloc(y, V, ids, epilogue=epilogue), want)
+    y = moe.gemv_nvfp4_alloc(torch.full((T, 256), float("inf"), dtype=BF16, device="cuda"), W, ids)   # the token itself
+    assert not y[1::3].any() and not y[::3].isfinite().any()
+
+
+@pytest.mark.parametrize("T", [1, 3, 6, 12])
+@pytest.mark.parametrize("K", [32, 64, 96, 256, 288])
+def test_a_weight_rows_nan_scale_stays_in_it(K, T):
+    g = _gen(15)
+    W, x = _exact_weights(g, 2, 48, K), torch.randint(-3, 4, (T, K), generator=g, device="cuda").to(BF16)
+    ids = torch.tensor([[1]] * T, dtype=torch.int32, device="cuda")
+    want = moe.gemv_nvfp4_alloc(x, W, ids)
+    W.sf[1, 5], W.sf[1, 32], W.sf[0] = 0x7f, 0xff, 0x7f
+    for V in _layouts(W):
+        got = moe.gemv_nvfp4_alloc(x, V, ids)
+        assert got[:, [5, 32]].isnan().all()
+        got[:, [5, 32]] = want[:, [5, 32]]
+        assert torch.equal(got, want)
+
+
 def test_repeats_and_layouts_give_the_same_bits():
     """Partial sums are taken in one order and joined in order, whichever layout holds the weights."""
     g = _gen(12)
