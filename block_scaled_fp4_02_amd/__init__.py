@@ -547,7 +547,9 @@ def moe_grouped_wgrad_bf16(args: moe_wgrad_bf16_args, stream=None):
 class GradList:
     """The tensors of a gradient norm and its clipping, checked and laid out for the library once: `tensors`
     f32 or bf16, dense, on one device; `out` (of the same sizes and types) receives the clipped values, None:
-    `tensors` themselves.  It holds the tensors, and may serve any number of calls."""
+    `tensors` themselves.  It may serve any number of calls, as long as the tensors keep their memory (a
+    tensor given other memory through `.data` or `.grad = ` needs a new GradList).  Clipping needs outputs that do not
+    overlap each other or another tensor; the same one twice is refused."""
 
     def __init__(self, tensors, out=None):
         fn = "GradList"
@@ -567,9 +569,11 @@ class GradList:
             raise MoeError(fn, MOE_ERR_SHAPE, "each output needs its tensor's number of elements")
         words = [0] * (4 * max(self.count, 1))   # of each moe_tensor: src, dst, n, dtype
         n = 4 * self.count
-        words[0:n:4] = [t.data_ptr() for t in ts]
+        written = words[0:n:4] = [t.data_ptr() for t in ts]
         if outs is not None:
-            words[1:n:4] = [o.data_ptr() for o in outs]
+            written = words[1:n:4] = [o.data_ptr() for o in outs]
+        # (empty tensors may share an address)
+        self.distinct = len(set(written)) == self.count or len({p for p, s in zip(written, sizes) if s}) == sum(s > 0 for s in sizes)
         words[2:n:4] = sizes
         words[3:n:4] = [_DTYPES[d] for d in types]
         self._words = array.array("q", words)
@@ -603,6 +607,8 @@ def moe_grad_norm(tensors, norm, ws=None, stream=None):
 def moe_grad_clip(tensors, norm, max_norm, out=None, stream=None):
     """out (None: `tensors`, or what the GradList has) = tensors * min(1, max_norm / (norm + 1e-6))."""
     g = _grad_list(tensors, out)
+    if not g.distinct:
+        raise MoeError("moe_grad_clip", MOE_ERR_UNSUPPORTED, "a tensor that is written may be in the list once only")
     _dense("moe_grad_clip", ("norm", norm, _F32))
     _sized("moe_grad_clip", norm.numel() >= 1 and g.device in (None, norm.get_device()), "norm [1] on the tensors' device is needed")
     _current("moe_grad_clip", norm.get_device(), stream)
@@ -989,6 +995,8 @@ def clip_grad_norm(tensors, max_norm, out=None, stream=None) -> torch.Tensor:
     """Clips `tensors` (a list, or a GradList) by their global norm, in place or into `out`, and returns the
     norm before it, [1] f32 on the device."""
     g = _grad_list(tensors, out)
+    if g.count:
+        _current("clip_grad_norm", g.device, stream)
     device = torch.device("cuda", g.device if g.count else torch.cuda.current_device())
     with _allocating(stream):
         norm = torch.empty(1, dtype=torch.float32, device=device)

@@ -127,7 +127,13 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const Table t, double *p
 constexpr int kSumThreads = 1024;
 __global__ __launch_bounds__(kSumThreads) void sum_kernel(const double *partial, int64_t n, float *norm) {
   double sum = 0.0;
-  for (int64_t a = threadIdx.x; a < n; a += kSumThreads) sum += partial[a];
+  for (int64_t a = threadIdx.x; a < n; a += 8 * kSumThreads) {   // (eight loads at once)
+    double v[8];
+#pragma unroll
+    for (int u = 0; u < 8; u++) v[u] = a + u * kSumThreads < n ? partial[a + u * kSumThreads] : 0.0;
+#pragma unroll
+    for (int u = 0; u < 8; u++) sum += v[u];
+  }
   sum = block_sum<kSumThreads>(sum);
   if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(sum));
 }

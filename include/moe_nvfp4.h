@@ -448,7 +448,8 @@ moe_status moe_balance_loss_backward(const float *logits, int T, int E, const in
  *                   of its output): y is the gradient of the activations; with g, u of Z bf16
  *                   [R, 2N] and s = 1 / (1 + exp(-g)), D bf16 [R, 2N] receives
  *                   D[p, i] = bf16(y u s (1 + g (1 - s))),  D[p, N + i] = bf16(y g s).
- * Rows p >= expert_offsets[E] of D and Z are not written.  The gradient with respect to the block's
+ * Rows p >= expert_offsets[E] of D and Z are not written.  D of the backward pass may be Z itself (its values
+ * are replaced); apart from that no output overlaps another tensor.  The gradient with respect to the block's
  * rows is the product MOE_EPI_NONE of that D with W1 [E, 2I, H] transposed (moe_finalize with unit
  * weights sums a token's rows).
  * Supported: N % 8 == 0 (SWIGLU: N % 16 == 0), K % 8 == 0, N, K <= 2^20, N * K <= 2^30 - 2048,
@@ -505,8 +506,8 @@ moe_status moe_grouped_wgrad_bf16(const moe_wgrad_bf16_args *args, hipStream_t s
  *                  element is one).
  *   moe_grad_clip  dst = x s with s = min(1, max_norm / (*norm + 1e-6)), in binary32, rounded once to
  *                  the tensor's type; dst NULL: in place.  A NaN norm makes s NaN, an infinite one 0;
- *                  in place with s = 1 nothing is written.  A dst other than NULL and src may not
- *                  overlap any src.
+ *                  in place with s = 1 nothing is written.  What is written (dst, or src in
+ *                  place) may overlap no other tensor of the list, nor its own src but as the same address.
  * dtype: MOE_DTYPE_BF16 or MOE_DTYPE_F32, of src and dst.  A tensor need be aligned to its elements
  * only; where src and dst lie on 16 bytes it is read and written 16 bytes at a time.  Several processes' shares
  * of one model: sum the squares of their norms, and clip by the root of it.

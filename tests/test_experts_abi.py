@@ -164,6 +164,11 @@ def test_binding_refuses_what_kernels_cannot_read():
     refused(SHAPE, moe._grad_list, tensors=moe.GradList([z(4)]), out=[z(4)])
     refused(UNSUPPORTED, moe.moe_grad_norm, tensors=[z(4)], norm=z(1, dt=f32))          # not on the GPU
     refused(UNSUPPORTED, moe.moe_grad_clip, tensors=[z(4)], norm=z(1), max_norm=1.0)
+    refused(UNSUPPORTED, moe.clip_grad_norm, tensors=[z(4)], max_norm=1.0)
+    t, u = z(4), z(4)
+    for kw in (dict(tensors=[t, u, t]), dict(tensors=[t, u], out=[z(8)[:4]] * 2), dict(tensors=moe.GradList([u, u]))):   # written twice
+        refused(UNSUPPORTED, moe.moe_grad_clip, norm=z(1, dt=f32), max_norm=1.0, **kw)
+    assert moe.GradList([t, u, t], [z(4), z(4), z(4)]).distinct and moe.GradList([z(0), t, z(0)]).distinct
     for f, cls in ((moe.moe_grouped_gemm_bf16, gemm_args), (moe.moe_grouped_wgrad_bf16, moe.moe_wgrad_bf16_args), (moe.moe_gemv_nvfp4, moe.moe_gemv_args)):
         a = cls()
         a.device = -1

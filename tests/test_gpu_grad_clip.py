@@ -49,7 +49,7 @@ def _check(ts, most, norm, out):
 
 
 SIZES = {"one": [1], "none": [], "empty ones": [0, 5, 0, 0, 3], "odd": [1, 7, 8, 9, 15, 16383, 16384, 16385, 3], "all empty": [0, 0],
-         "table edge": [5] * 96, "past the table": [3, 40000] * 60 + [1], "large": [3_000_001, 70_000_000]}
+         "table edge": [5] * 320, "past the table": [3, 40000] * 160 + [1], "three tables": [3, 0, 9] * 300, "large": [3_000_001, 70_000_000]}
 
 
 @pytest.mark.parametrize("most", [0.5, 1e6, 0.0, math.inf])
