@@ -73,7 +73,7 @@ PRODUCTS = {
     "split 32, two chunks": ([40, 20, 0], 2056, 136), "split 32, short": ([20, 0, 40, 7], 1000, 72), "32 rows": ([64, 128, 1], 2600, 64),
     "64 rows": ([20] * 40 + [0, 70], 1024, 136), "full chunks": ([64, 128, 1], 13000, 64), "many small": ([3] * 90 + [0] * 30, 72, 136),
     "middle": ([130, 200, 0, 95], 6400, 136), "middle, one step": ([256, 128], 12800, 40), "large": ([300, 0, 517, 45], 12808, 200),
-    "large, one step": ([600, 90], 16392, 8), "large, two steps": ([256, 512], 12288, 128), "1024 experts": ([1] * 1000 + [0] * 20 + [50] * 4, 16, 72),
+    "large, one step": ([600, 90], 16392, 8), "large, halves": ([256, 512, 100], 22528, 64), "large, two steps": ([256, 512], 12288, 128), "1024 experts": ([1] * 1000 + [0] * 20 + [50] * 4, 16, 72),
 }
 
 
@@ -96,7 +96,7 @@ def test_product(name, transposed, gather):
 GATED = {
     "one row": ([1], 8, 8), "split 16": ([1, 0, 3], 24, 264), "split 16, two chunks": ([30, 0, 2], 40, 520), "split 32": ([5], 2408, 512),
     "split 32, two chunks": ([40, 0, 20], 1032, 72), "64 rows": ([20] * 40 + [0, 70], 1024, 136), "short K": ([9, 100], 136, 8),
-    "large": ([300, 0, 517, 45], 6408, 200), "large, one step": ([600, 90], 8200, 64),
+    "large": ([300, 0, 517, 45], 6408, 200), "large, one step": ([600, 90], 8200, 64), "large, halves": ([256, 512, 100], 11264, 72),
 }
 
 
@@ -139,10 +139,13 @@ def test_gated_backward(name):
     assert fits.float().mean() > 0.9 and torch.isfinite(dZ[:n][fits]).all()
     assert ref.close(dZ[:n][fits], want[fits], err[fits])
     assert (dZ[n:] == MARK).all()
+    moe.moe_grouped_gemm_bf16(moe.make_gemm_bf16_args(dY, W2, off, R, moe.MOE_EPI_SWIGLU_BACKWARD, Z, Z, B_layout=TR))   # in place
+    assert torch.equal(Z[:n].nan_to_num(7.0), dZ[:n].nan_to_num(7.0))
 
 
 WGRADS = {"one row": ([1], 8, 8), "small": ([20, 0, 40, 7], 200, 72), "whole steps": ([64, 128, 0, 1], 136, 264), "long": ([3000], 72, 136),
-          "many": ([3, 0, 65] * 30, 40, 24), "wide": ([300, 0, 517, 45, 64], 2568, 1032), "large": ([5000, 8, 0, 40, 4609], 2568, 1032), "large, one group": ([2825], 3336, 3592)}
+          "many": ([3, 0, 65] * 30, 40, 24), "wide": ([300, 0, 517, 45, 64], 2568, 1032), "large": ([5000, 8, 0, 40, 4609], 2568, 1032), "large, one group": ([2825], 3336, 3592),
+          "large, halves": ([1500, 1600], 2816, 4096)}
 
 
 @pytest.mark.parametrize("gather", [False, True], ids=["own rows", "gathered"])
@@ -173,6 +176,23 @@ def test_a_groups_nan_stays_in_it():
         assert torch.equal(D[:70].double(), ref.bf16(want[:70])) and torch.equal(D[103:].double(), ref.bf16(want[103:])) and D[bad].isnan().all()
     D = moe.grouped_wgrad_bf16_alloc(Y, A, off, 173)
     assert torch.equal(D[0].double(), dw[0]) and torch.equal(D[2].double(), dw[2]) and D[1].isnan().all()
+
+
+@pytest.mark.parametrize("sizes", [[3], [40, 20], [700, 900]])
+def test_denormals_count(sizes):
+    """Elements and weights below the least normal number, and results there."""
+    g, off, n, N, K = _gen(5), _offsets(sizes), sum(sizes), 12808, 40
+    A, W, Y = _ints(g, n, K), _ints(g, len(sizes), N, K), _ints(g, n, N)
+    want, dw = ref.product(A, W, off)[0], ref.wgrad(Y, A, off)[0]
+    tiny, big = 2.0 ** -130, 2.0 ** 100
+    for a, w in ((tiny, big), (big, tiny), (tiny, 1.0)):
+        B = (W.float() * w).to(BF16)
+        for layout, V in ((0, B), (TR, B.transpose(1, 2).contiguous())):
+            D = torch.empty(n, N, dtype=BF16, device="cuda")
+            moe.moe_grouped_gemm_bf16(moe.make_gemm_bf16_args((A.float() * a).to(BF16), V, off, n, 0, D, B_layout=layout))
+            assert torch.equal(D.double(), ref.bf16(want * (a * w))), (a, w, layout)
+        D = moe.grouped_wgrad_bf16_alloc((Y.float() * w).to(BF16), (A.float() * a).to(BF16), off, n)
+        assert torch.equal(D.double(), dw * (a * w)), (a, w)
 
 
 def test_no_rows():
