@@ -26,8 +26,6 @@
 #include "gemv_nvfp4.hpp"
 #include "lds_tiles.hpp"
 
-#include <limits.h>
-
 #include <type_traits>
 
 #pragma clang fp contract(off)
@@ -45,17 +43,17 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kStep = 256;         // elements of K in a step
 constexpr int kPackBlock = 2304;   // bytes of one (16-row tile, step) block of packed weights
 constexpr int kMaxSlots = 32;
-constexpr int NT = 2;              // tiles of 16 weight rows that a wave takes together
 constexpr int kCodes = kStep / 2;  // bytes of a row's codes in a step
-constexpr int kCus = 256, kLdsBytes = 160 << 10;
+constexpr int kCus = 256;
 
 // Row-major weights, K a multiple of 64, or of 32 (rows of scales then start at even bytes); packed.
 enum Layout { kRows64, kRows32, kPacked };
 
-// TB: blocks of four tokens.  SINGLE: one token, whose slots are the groups.
-template <int TB_, Layout L_, bool SINGLE_, int WAVES_, int STAGES_>
+// NT: tiles of 16 weight rows that a wave takes together.  TB: blocks of four tokens.  SINGLE: one token,
+// whose slots are the groups.
+template <int NT_, int TB_, Layout L_, bool SINGLE_, int WAVES_, int STAGES_>
 struct Shape {
-  static constexpr int TB = TB_, WAVES = WAVES_, STAGES = STAGES_;
+  static constexpr int NT = NT_, TB = TB_, WAVES = WAVES_, STAGES = STAGES_;
   static constexpr Layout L = L_;
   static constexpr bool SINGLE = SINGLE_;
   static constexpr int kTokens = TB * 4, kPairs = SINGLE ? kMaxSlots : kTokens * kMaxSlots;
@@ -119,7 +117,7 @@ __device__ __forceinline__ void multiply(const Weights &w, const Elements (&x)[T
 // The tiles and tokens that a wave's copies come from.
 template <class S>
 struct Source {
-  Buf code[NT], scale[NT], x;
+  Buf code[S::NT], scale[S::NT], x;
   uint32_t row[S::kXCopies];   // byte in x of the token that this lane's copies move (kOob: none)
 };
 
@@ -128,7 +126,7 @@ template <class S>
 __device__ __forceinline__ void issue(const Source<S> &src, int K, uint32_t at, int step, bool none) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int c = 0; c < NT * 2; c++) {
+  for (int c = 0; c < S::NT * 2; c++) {
     uint32_t from;
     if (S::L == kPacked) {
       from = none ? kOob : step * kPackBlock + c % 2 * 1024 + lane * 16;
@@ -161,10 +159,10 @@ __device__ __forceinline__ void issue(const Source<S> &src, int K, uint32_t at, 
 
 // acc += the products of the step in the stage at `stage`.
 template <class S>
-__device__ __forceinline__ void consume(const uint8_t *stage, int K, int step, float4v (&acc)[NT][S::TB], Weights (&w)[NT], Elements (&x)[S::TB]) {
+__device__ __forceinline__ void consume(const uint8_t *stage, int K, int step, float4v (&acc)[S::NT][S::TB], Weights (&w)[S::NT], Elements (&x)[S::TB]) {
   const int lane = threadIdx.x & 63, g = lane / 16, r = lane % 16;
 #pragma unroll
-  for (int t = 0; t < NT; t++) {
+  for (int t = 0; t < S::NT; t++) {
 #pragma unroll
     for (int q = 0; q < 2; q++) {
       const int at = S::L == kPacked ? q * 1024 + lane * 16 : r * kCodes + ((2 * g + q) ^ ((r >> 1) & 7)) * 16;
@@ -264,8 +262,9 @@ __device__ __forceinline__ void build_groups(const Params &P, int t0, int tokens
 // all of them at the end, in the order of its steps.
 template <class S, Epilogue MODE>
 __global__ __launch_bounds__(S::WAVES *kWave) void gemv_kernel(const Params P) {
-  constexpr int TB = S::TB, kHeld = S::SINGLE ? 1 : S::kTokens;
+  constexpr int NT = S::NT, TB = S::TB, kHeld = S::SINGLE ? 1 : S::kTokens;
   constexpr bool SINGLE = S::SINGLE;
+  static_assert(MODE == kWeighted || NT == 2, "pairs of tiles");
   __shared__ __align__(1024) uint8_t ring[S::kRing];
   __shared__ float part[S::WAVES][2][NT][kHeld][16];   // of a wave's first item, of its last one
   __shared__ Groups<S::kPairs, kHeld> groups;
@@ -274,7 +273,7 @@ __global__ __launch_bounds__(S::WAVES *kWave) void gemv_kernel(const Params P) {
   const int count = SINGLE ? P.k : __builtin_amdgcn_readfirstlane(groups.count);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & 63, r = lane % 16;
   const int width = MODE == kGated ? P.N / 2 : P.N;
-  constexpr int kCols = MODE == kGated ? 16 : 32;   // columns of the result in a pair of tiles
+  constexpr int kCols = MODE == kGated ? 16 : NT * 16;   // columns of the result in the tiles
   const int pairs = (width + kCols - 1) / kCols, steps = (P.K + kStep - 1) / kStep;
 
   // SINGLE: slot j's expert is in lane j (-1: dropped); every wave writes the same ids and factors
@@ -444,7 +443,7 @@ __global__ __launch_bounds__(S::WAVES *kWave) void gemv_kernel(const Params P) {
            const int nth = q == begin / steps ? 0 : 1;
 #pragma unroll
            for (int t = 0; t < kHeld; t++) {
-             const float a = over_groups(acc[0][t / 4][t % 4]), b = over_groups(acc[1][t / 4][t % 4]);
+             const float a = over_groups(acc[0][t / 4][t % 4]), b = over_groups(acc[NT - 1][t / 4][t % 4]);
              if (!whole) {
                if (lane < 16) part[wave][nth][0][t][r] = a;
                else if (lane < 32) part[wave][nth][1][t][r] = b;
@@ -471,21 +470,33 @@ __global__ __launch_bounds__(S::WAVES *kWave) void gemv_kernel(const Params P) {
 
 template <class S, Epilogue MODE>
 hipError_t run(const Params &p, hipStream_t stream) {
-  const int width = MODE == kGated ? p.N / 2 : p.N, cols = MODE == kGated ? 16 : 32;
+  const int width = MODE == kGated ? p.N / 2 : p.N, cols = MODE == kGated ? 16 : S::NT * 16;
   const int pairs = (width + cols - 1) / cols, chunk = p.T < S::kTokens ? p.T : S::kTokens;
   const int64_t items = static_cast<int64_t>(pairs) * (chunk * p.k < p.E ? chunk * p.k : p.E);
-  const int64_t resident = kCus * (2 * S::kRing > kLdsBytes ? 1 : 2);   // workgroups that run at once
-  const dim3 grid(static_cast<uint32_t>(MODE == kWeighted ? pairs : items < resident ? items : resident), 1, (p.T + S::kTokens - 1) / S::kTokens);
+  const dim3 grid(static_cast<uint32_t>(MODE == kWeighted ? pairs : items < kCus ? items : kCus), 1, (p.T + S::kTokens - 1) / S::kTokens);
   hipLaunchKernelGGL((gemv_kernel<S, MODE>), grid, dim3(S::WAVES * kWave), 0, stream, p);
   return hipGetLastError();
 }
 
+// The fewest blocks of four tokens that hold them, up to 16 tokens: 1 token through 8 of 64 experts, 4096 x
+// 6144, 24 us without groups, 28 with, 31 with two blocks, 64 with four; 4 tokens 85, 90, 190 with one, two,
+// four; 8 tokens 148, 295 with two, four.  Eight waves with two stages each (three: 25 us) where LDS has
+// room for them, else four.
+template <Epilogue MODE, Layout L, int NT>
+hipError_t run_tokens(const Params &p, hipStream_t stream) {
+  if (p.T == 1) return run<Shape<NT, 1, L, true, 8, 2>, MODE>(p, stream);
+  if (p.T <= 4) return run<Shape<NT, 1, L, false, 8, 2>, MODE>(p, stream);
+  if (p.T <= 8) return run<Shape<NT, 2, L, false, L == kRows32 ? 4 : 8, 2>, MODE>(p, stream);
+  return run<Shape<NT, 4, L, false, 4, 2>, MODE>(p, stream);
+}
+
+// A weighted sum's workgroup has its columns for all groups: one tile of them where pairs of tiles are at most
+// half of the CUs.  8 of 64 experts, us with one tile | two: 4096 x 2048, one token 11.1 | 15.2, sixteen 162 |
+// 261; 6144 x 2048 18.0 | 18.2, eight tokens 118 | 96.
 template <Epilogue MODE, Layout L>
 hipError_t run_layout(const Params &p, hipStream_t stream) {
-  if (p.T == 1) return run<Shape<1, L, true, 8, 3>, MODE>(p, stream);
-  if (p.T <= 4) return run<Shape<1, L, false, 8, 2>, MODE>(p, stream);
-  if (p.T <= 8) return run<Shape<2, L, false, L == kRows32 ? 4 : 8, 2>, MODE>(p, stream);
-  return run<Shape<4, L, false, 4, 2>, MODE>(p, stream);
+  if (MODE == kWeighted && p.N <= kCus / 2 * 32) return run_tokens<MODE, L, MODE == kWeighted ? 1 : 2>(p, stream);
+  return run_tokens<MODE, L, 2>(p, stream);
 }
 
 }  // namespace

@@ -54,7 +54,8 @@ def _layouts(W):
 # T, k, E, N, K
 CASES = {"one token": (1, 8, 16, 64, 512), "one slot": (1, 1, 1, 16, 32), "few experts": (4, 2, 3, 48, 256), "five": (5, 3, 7, 96, 288),
          "eight": (8, 8, 8, 32, 1024), "nine": (9, 4, 40, 80, 96), "sixteen": (16, 8, 24, 32, 768), "seventeen": (17, 2, 5, 64, 2080),
-         "many": (130, 6, 11, 32, 256), "32 slots": (3, 32, 40, 32, 64), "wide": (2, 2, 4, 4112, 160), "long": (1, 2, 4, 32, 20512)}
+         "many": (130, 6, 11, 32, 256), "32 slots": (3, 32, 40, 32, 64), "wide": (2, 2, 4, 4112, 160), "long": (1, 2, 4, 32, 20512),
+         "wide, one token": (1, 3, 4, 4128, 256), "wide, six": (6, 2, 4, 4128, 512), "wide, six, short": (6, 2, 4, 4128, 96), "wide, twelve": (12, 2, 4, 4128, 256)}
 
 
 @pytest.mark.parametrize("how", ["distinct", "any"])
