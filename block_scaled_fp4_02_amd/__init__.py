@@ -559,19 +559,20 @@ class GradList:
         _sized(fn, outs is None or len(outs) == self.count, "as many outputs as tensors are needed")
         self.device = ts[0].get_device() if ts else None
         # (each question is put to all tensors at once: a model has hundreds, and this runs every step)
-        types, sizes = [t.dtype for t in ts], [t.numel() for t in ts]
+        T = torch.Tensor
+        types, sizes = [t.dtype for t in ts], list(map(T.numel, ts))
         every = ts if outs is None else ts + outs
         if not (set(types) <= _DTYPES.keys() and (outs is None or [o.dtype for o in outs] == types)
-                and all([t.is_contiguous() for t in every]) and {t.get_device() for t in every} <= {self.device}):
+                and all(map(T.is_contiguous, every)) and set(map(T.get_device, every)) <= {self.device}):
             raise MoeError(fn, MOE_ERR_UNSUPPORTED, "dense f32 or bf16 tensors on one device are needed, each output of its tensor's type, got "
                            + ", ".join(f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}" for t in every[:8]))
-        if outs is not None and [o.numel() for o in outs] != sizes:
+        if outs is not None and list(map(T.numel, outs)) != sizes:
             raise MoeError(fn, MOE_ERR_SHAPE, "each output needs its tensor's number of elements")
         words = [0] * (4 * max(self.count, 1))   # of each moe_tensor: src, dst, n, dtype
         n = 4 * self.count
-        written = words[0:n:4] = [t.data_ptr() for t in ts]
+        written = words[0:n:4] = list(map(T.data_ptr, ts))
         if outs is not None:
-            written = words[1:n:4] = [o.data_ptr() for o in outs]
+            written = words[1:n:4] = list(map(T.data_ptr, outs))
         # (empty tensors may share an address)
         self.distinct = len(set(written)) == self.count or len({p for p, s in zip(written, sizes) if s}) == sum(s > 0 for s in sizes)
         words[2:n:4] = sizes
