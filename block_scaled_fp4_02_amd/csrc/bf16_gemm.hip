@@ -279,11 +279,13 @@ __device__ __forceinline__ void mfma_agpr(const bf16x8 &p, const bf16x8 &q, floa
 }
 __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" : : : "memory"); }
 
-// issue(j, kb, at): copy number j (a constant) of stage kb into the buffer at LDS address `at`;
-// prepare(kb): the loads that stage kb's copies need, while the stage before is issued; advance(kb): on to
-// stage kb.  ACTIVE of a wave's 8 column tiles are in use.
-template <class T, int ACTIVE, class I, class R, class A>
-__device__ __forceinline__ void contract_large(I issue, R prepare, A advance, const uint8_t *lds, int steps, float4v (&acc)[T::TP][T::TQ]) {
+// issue(j, kb, at): copy number j (a constant) of stage kb into the buffer at LDS address `at`; locate(j, kb,
+// phase): before it the address, in kPhases steps that stand between different MFMAs; prepare(kb): the
+// loads that stage kb's copies need, while the stage before is issued; advance(kb): on to stage kb.  ACTIVE of a wave's
+// 8 column tiles are in use.
+constexpr int kPhases = 4;
+template <class T, int ACTIVE, class I, class L, class R, class A>
+__device__ __forceinline__ void contract_large(I issue, L locate, R prepare, A advance, const uint8_t *lds, int steps, float4v (&acc)[T::TP][T::TQ]) {
   static_assert(T::kWaves == 4 && T::TP == 8 && T::TQ == 8 && T::STEP == 32 && T::kCopies == T::TP, "the schedule above");
   constexpr int kLater = T::kCopies * (T::STAGES - 2);   // copies of the stages after the next one
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -294,7 +296,10 @@ __device__ __forceinline__ void contract_large(I issue, R prepare, A advance, co
 #pragma unroll
   for (int i = 0; i < T::STAGES; i++) {
     prepare(i + 1);
-    for_constants<T::kCopies>([&](auto j) INLINED { issue(j, i, lds0 + i * T::kStage); });
+    for_constants<T::kCopies>([&](auto j) INLINED {
+      for_constants<kPhases>([&](auto phase) INLINED { locate(j, i, phase); });
+      issue(j, i, lds0 + i * T::kStage);
+    });
     advance(i + 1);
   }
   int slot = 0;
@@ -324,7 +329,12 @@ __device__ __forceinline__ void contract_large(I issue, R prepare, A advance, co
 #pragma unroll
           for (int n = 0; n < kPer; n++) read(std::integral_constant<int, 1 - h>(), lds + next * T::kStage, i * kReads + (j - 1) * kPer + n);
         }
-        if (j == (ACTIVE > 4 ? 6 : ACTIVE - 1)) issue(row, kb + T::STAGES, lds0 + slot * T::kStage);
+        // P's copies, whose addresses may take work, beside the rows of MFMAs that have no reads
+        constexpr std::integral_constant<int, (i + T::kCopiesQ) % T::kCopies> copy;
+        for_constants<kPhases>([&](auto phase) INLINED {
+          if (j == (ACTIVE > 4 ? 2 + decltype(phase)::value : ACTIVE - 1)) locate(copy, kb + T::STAGES, phase);
+        });
+        if (j == (ACTIVE > 4 ? 6 : ACTIVE - 1)) issue(copy, kb + T::STAGES, lds0 + slot * T::kStage);
         __builtin_amdgcn_sched_barrier(0);
       }
     });
@@ -514,7 +524,7 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
     with_active<T>(count, [&](auto active) INLINED {
       contract_large<T, decltype(active)::value>(
           [&](auto j, int kb, uint32_t at) INLINED { issue_one<T, false>(src, at, wave, j, kb == steps - 1 && src.last < T::STEP); },
-          [](int) INLINED {}, [&](int kb) INLINED { advance_to<T>(src, kb, steps); }, lds, steps, acc);
+          [](auto, int, auto) INLINED {}, [](int) INLINED {}, [&](int kb) INLINED { advance_to<T>(src, kb, steps); }, lds, steps, acc);
     });
   } else {
     // the weights of a group of one chunk are read by this workgroup alone
@@ -782,20 +792,33 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
   load_rows(0);
   take_rows();
   const uint32_t row_bytes = static_cast<uint32_t>(P.K) * 2;
+  // The gathered copy's offset, in steps: all at once between two MFMAs they kept the next one waiting (16
+  // groups of 512 rows, 4096 x 6144, 572 us; now 538, and 510 where the rows need no gathering).
+  uint32_t from = 0, other = 0;
+  auto locate = [&](auto number, int kb, auto phase) INLINED {
+    constexpr int j = decltype(number)::value, step = decltype(phase)::value;
+    if constexpr (GATHER && j < T::kCopiesP) {
+      const int k = kb * T::STEP + (wave * T::kCopiesP + j) % T::kPanelCopies * 4 + lane / 16;
+      if (step == 0) {
+        int row[4] = {row_of[4 * j], row_of[4 * j + 1], row_of[4 * j + 2], row_of[4 * j + 3]};
+#pragma unroll
+        for (int q = 0; q < 4; q++) asm("" : "+s"(row[q]));   // (or they become one element with a variable index)
+        from = lane / 16 & 1 ? row[1] : row[0];
+        other = lane / 16 & 1 ? row[3] : row[2];
+      } else if (step == 1) {
+        from = lane / 32 ? other : from;
+      } else if (step == 2) {
+        from = src.vp[j] + from * row_bytes;
+      } else {
+        from = k < rows ? from : kOob;
+      }
+      asm volatile("" : "+v"(from));   // (or the compiler branches around the product, four times a stage)
+    }
+  };
   auto issue_copy = [&](auto number, int kb, uint32_t at) INLINED {
     constexpr int j = decltype(number)::value;
-    if constexpr (!GATHER || j >= T::kCopiesP) {
-      issue_one<T, false>(src, at, wave, j, false);
-    } else {
-      const int c = wave * T::kCopiesP + j, k = kb * T::STEP + c % T::kPanelCopies * 4 + lane / 16;
-      int row[4] = {row_of[4 * j], row_of[4 * j + 1], row_of[4 * j + 2], row_of[4 * j + 3]};
-#pragma unroll
-      for (int q = 0; q < 4; q++) asm("" : "+s"(row[q]));   // (or they become one element with a variable index)
-      const int a = lane / 16 & 1 ? row[1] : row[0], b = lane / 16 & 1 ? row[3] : row[2];
-      uint32_t from = src.vp[j] + static_cast<uint32_t>(lane / 32 ? b : a) * row_bytes;
-      asm volatile("" : "+v"(from));   // (or the compiler branches around the product, four times a stage)
-      copy16(src.p, at + c * 1024, k < rows ? from : kOob);
-    }
+    if constexpr (GATHER && j < T::kCopiesP) copy16(src.p, at + (wave * T::kCopiesP + j) * 1024, from);
+    else issue_one<T, false>(src, at, wave, j, false);
   };
   auto advance = [&](int kb) INLINED {
     if (GATHER) {
@@ -808,13 +831,16 @@ __global__ __launch_bounds__(T::kThreadsT) void wgrad_kernel(const WgradParams P
   };
   float4v acc[T::TP][T::TQ];
   if constexpr (T::kLarge) {
-    with_active<T>(n1 - n0, [&](auto active) INLINED { contract_large<T, decltype(active)::value>(issue_copy, load_rows, advance, lds, steps, acc); });
+    with_active<T>(n1 - n0, [&](auto active) INLINED { contract_large<T, decltype(active)::value>(issue_copy, locate, load_rows, advance, lds, steps, acc); });
   } else {
     const int g = lane / 16, r = lane % 16, wp = wave % T::WP, wq = wave / T::WP;
     constexpr int kHalvesK = T::STEP / 32;
     auto issue_stage = [&](int kb, int slot) INLINED {
       load_rows(kb + 1);
-      for_constants<T::kCopies>([&](auto j) INLINED { issue_copy(j, kb, lds0 + slot * T::kStage); });
+      for_constants<T::kCopies>([&](auto j) INLINED {
+        for_constants<kPhases>([&](auto phase) INLINED { locate(j, kb, phase); });
+        issue_copy(j, kb, lds0 + slot * T::kStage);
+      });
       advance(kb + 1);
     };
     clear<T>(acc);
