@@ -224,7 +224,7 @@ __device__ __forceinline__ void mfma_row(const bf16x8 &p, const bf16x8 (&q)[T::T
   for (int j = 0; j < T::TQ; j++) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, q[j], acc[j], 0, 0, 0);
 }
 
-// The whole contraction of one tile; ACTIVE of the wave's TQ column tiles are in use.
+// The whole contraction of one tile of the smaller kinds; ACTIVE of the wave's TQ column tiles are in use.
 template <class T, bool ONCE, int ACTIVE>
 __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps, float4v (&acc)[T::TP][T::TQ]) {
   constexpr int kHalvesK = T::STEP / 32;   // MFMAs along the contraction
@@ -270,6 +270,12 @@ __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps
 // busy by itself: while the 64 MFMAs of one stage run, the next stage's operands are read.  One barrier a
 // stage tells that the next one is there and that this one is read, so that its buffer takes the copies
 // of the fifth one after it, issued between the MFMAs.
+//
+// Dense 8192^3 on random data 815 to 960 us (1.14 to 1.35 PFLOP/s; torch.matmul beside it 844 to 884), where
+// the board's power sets the clock: on zeros 629 to 683.  A tile's start and end take about 10 us in which its
+// matrix cores idle (the first copies, 128 KB of results by every CU at once), so a contraction of
+// 512 leaves 34 % of the cycles to them, one of 6144 60 %.  Tiles of 128 x 256, 256 x 128 and 128 x 128, two
+// to a CU, were slower for every product of that size.
 
 // acc += p q^T, in accumulation registers.  (Of the builtin the compiler gives a wave's 256 accumulators to
 // both kinds of registers and moves 580 of them in every step.)  Nothing reads them between a tile's first
@@ -432,7 +438,7 @@ __device__ __forceinline__ float element(const uint4 &v, int i) {
 
 // Items of the large tile, of which a CU holds one at a time: where the items that an XCD has beyond whole
 // rounds of its CUs are at most half a round (a quarter), each is cut into two (four) along Q, for a
-// last round of half (a quarter of) the time.  Part `part` of the tile has rows from part * Q / parts on.
+// last round of about half (a quarter of) the time: 384 tiles of 8192 rows 501 us whole, 453 cut.  Part `part` of the tile has rows from part * Q / parts on.
 constexpr int kXcdCus = 32, kMostParts = 24;   // more workgroups for an XCD's cut items
 __device__ __forceinline__ bool part_of(int b, int64_t count, int64_t &w, int &part, int &parts) {
   const int64_t per = (count + kXcds - 1) / kXcds, first = b % kXcds * per;
@@ -527,7 +533,9 @@ __global__ __launch_bounds__(T::kThreadsT) void gemm_kernel(const GemmParams P) 
           [](auto, int, auto) INLINED {}, [](int) INLINED {}, [&](int kb) INLINED { advance_to<T>(src, kb, steps); }, lds, steps, acc);
     });
   } else {
-    // the weights of a group of one chunk are read by this workgroup alone
+    // the weights of a group of one chunk are read by this workgroup alone: where they do not stay in the
+    // memory-side cache between calls, past the caches (32 groups of 32 rows, 1.6 GB, 280 us, 293 through them; 16 of 20,
+    // 53 MB, the other way 25 and 16)
     const bool once = g.total == 1 && P.stream_weights;
     // Q tiles behind the last row are left out
     auto run = [&](auto active) {
@@ -932,10 +940,11 @@ hipError_t launch_gemm(GemmParams p, Epilogue epilogue, bool transposed, hipStre
   // tiles of q rows by c columns, for groups of the mean size
   auto items = [&](int q, int c) { return hit * ((mean + q - 1) / q) * ((p.N + c - 1) / c); };
   // Which tile; times in us, "a | b" for this choice and the next one below, weights 4096 x 6144 each.
-  // - 256 x 256 where groups have more than one 128-row chunk and the tiles nearly fill the CUs, one each:
-  //   16 groups of 160 rows 201 | 231 (transposed 161 | 243, gated 215 | 260), of 128 182 | 171 (144 | 145,
-  //   190 | 206); 24 groups of 512 rows, 784 x 1048: 192 tiles, 35 | 44; 8 of 512, 2048 x 2048: 128 tiles, 46 | 39.
-  const bool large = mean > 128 && items(256, 256) >= kCus * 3 / 4;
+  // - 256 x 256 where groups have more than one 128-row chunk and the tiles are more than half of the CUs, one
+  //   each: 16 groups of 160 rows 201 | 231 (transposed 161 | 243, gated 215 | 260), of 128 182 | 171 (144 | 145,
+  //   190 | 206); 9 of 256: 144 tiles, 190 | 257; 17 of 256, 2048 x 2048: 136 tiles, 50 | 62, 8 of 512: 128 tiles,
+  //   46 | 39; 24 of 384, 784 x 1048: 192 tiles, 31 | 25, of 512 35 | 44.
+  const bool large = mean > 128 && items(256, 256) > kCus / 2;
   // - 128 x 128 where 64 rows are not enough and there is more than one for each CU: 16 groups of 96 rows
   //   183 | 206, of 64 151 | 145; 8 of 256, 2048 x 2048: 256 tiles, 28 | 25, of 512: 512 tiles, 38 | 46.
   const bool middle = mean > 64 && items(128, 128) > kCus;

@@ -7,6 +7,7 @@
 // in a launch, so nothing is copied to the device and a captured launch holds what it needs.  A
 // workgroup takes one chunk of kChunk elements of one tensor.  Squares are taken and summed in 64 bits:
 // gfx950's vector units do that as fast as in 32, and no gradient is too large or too small for it.
+// 1.2 GB of binary32: norm 194 us (6.2 TB/s), clipping 454 us (5.3 TB/s read and written; a copy 4.95).
 #include "grad_clip.hpp"
 
 #pragma clang fp contract(off)
@@ -19,7 +20,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 constexpr int kTable = 320;      // (10 KB of arguments: 301 tensors of 4 million elements 46 us with 96 a launch, 22 with all in one)
-constexpr int kChunkBits = 14;
+constexpr int kChunkBits = 14;   // (600 million binary32 elements, norm and clipping, 1341 us, with 15 1315; 1.2 billion bf16 1287 and 1320)
 constexpr int64_t kChunk = int64_t(1) << kChunkBits;
 
 enum { kBf16 = 1, kWide = 2 };   // kWide: 16 bytes at a time
@@ -178,7 +179,8 @@ __device__ __forceinline__ void scale(const Entry &e, int64_t lo, int64_t hi, fl
 
 __global__ __launch_bounds__(kThreads) void clip_kernel(const Table t, const float *norm, float max_norm) {
   int64_t lo, hi;
-  // from the last chunk back: what the norm read last is still in the memory-side cache
+  // from the last chunk back: what the norm read last is still in the memory-side cache (600 million binary32
+  // elements in place 1382 -> 1352 us, with stores past the caches 1341)
   const Entry e = find(t, t.chunks - 1 - blockIdx.x, lo, hi);
   float s = max_norm / (*norm + 1e-6f);
   if (s >= 1.0f || max_norm == INFINITY) s = 1.0f;   // (otherwise a NaN norm stays one)
