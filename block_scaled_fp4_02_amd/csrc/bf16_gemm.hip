@@ -274,7 +274,7 @@ __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps
 // Dense 8192^3 on random data 815 to 960 us (1.14 to 1.35 PFLOP/s; torch.matmul beside it 844 to 884), where
 // the board's power sets the clock: on zeros 629 to 683.  A tile's start and end take about 10 us in which its
 // matrix cores idle (the first copies, 128 KB of results by every CU at once), so a contraction of
-// 512 leaves 34 % of the cycles to them, one of 6144 60 %.  Tiles of 128 x 256, 256 x 128 and 128 x 128, two
+// 512 leaves 36 % of the cycles to them, one of 6144 60 %.  Tiles of 128 x 256, 256 x 128 and 128 x 128, two
 // to a CU, were slower for every product of that size.
 
 // acc += p q^T, in accumulation registers.  (Of the builtin the compiler gives a wave's 256 accumulators to
