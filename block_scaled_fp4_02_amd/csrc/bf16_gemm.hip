@@ -953,7 +953,8 @@ hipError_t launch_gemm(GemmParams p, Epilogue epilogue, bool transposed, hipStre
   //   share weights: one of 64 rows 27 | 39, of 96 39 | 40 (gated 28 | 54, 39 | 53); 8 of one row, 2048 x
   //   2048: 512 tiles of one chunk each, 16.4 | 13.7.
   const int split = transposed ? 0 : items(16, 16) <= kCus ? 16 : items(16, 32) <= (mean > 16 ? 2 : 1) * kCus ? 32 : 0;
-  // - 32 x 128 for one round: one group of 128 rows, transposed, 31 | 44, of 512 50 | 46.
+  // - 32 x 128 for one round: one group of 128 rows 31 | 42 (transposed 32 | 45, backward 33 | 45), 8 of 64, 2048
+  //   x 2048, 14.6 | 17.4; 8 of 32, 4096 x 2048, 21.8 | 22.1; two rounds, transposed: one of 512 rows 50 | 46.
   const bool low = items(32, 128) <= kCus;
   if (epilogue == kGated) {
     if (large) return run_gemm<Large<false>, kGated>(p, stream);
