@@ -278,12 +278,18 @@ __device__ __forceinline__ void contract(Source<T> &src, uint8_t *lds, int steps
 // to a CU, were slower for every product of that size.
 
 // acc += p q^T, in accumulation registers.  (Of the builtin the compiler gives a wave's 256 accumulators to
-// both kinds of registers and moves 580 of them in every step.)  Nothing reads them between a tile's first
-// and last MFMA but the MFMA 64 later; settle() stands before what does.
+// both kinds of registers and moves 580 of them in every step.)  The compiler does not know these statements as
+// MFMAs and waits for no result of theirs.  Nothing in the loop reads one but the MFMA of the next stage, and SETTLE, with
+// the last MFMA before a place where the loop may end, waits in the same statement: an MFMA's result is there
+// after 8 wait states, and the results before it are older.  (A wait after the loop, in a statement of its own, came behind
+// moves of accumulators.  This one takes 32 cycles of every two stages' 2048: dense 8192^3 785 us, 782
+// without; 16 groups of 512 rows, transposed, 345 and 342.  A branch around it took longer, 790 and 354, and
+// accumulators as operands of a statement after the loop are moved first.)
+template <bool SETTLE>
 __device__ __forceinline__ void mfma_agpr(const bf16x8 &p, const bf16x8 &q, float4v &acc) {
-  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(p), "v"(q));
+  if constexpr (SETTLE) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0\n\ts_nop 7" : "+a"(acc) : "v"(p), "v"(q));
+  else asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(p), "v"(q));
 }
-__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" : : : "memory"); }
 
 // issue(j, kb, at): copy number j (a constant) of stage kb into the buffer at LDS address `at`; locate(j, kb,
 // phase): before it the address, in kPhases steps that stand between different MFMAs; prepare(kb): the
@@ -326,9 +332,11 @@ __device__ __forceinline__ void contract_large(I issue, L locate, R prepare, A a
     const int next = slot == T::STAGES - 1 ? 0 : slot + 1;
     for_constants<T::TP>([&](auto row) INLINED {
       constexpr int i = decltype(row)::value;
+      constexpr bool kSettle = h == 1 && i == T::TP - 1;   // the loop ends behind its second stage
 #pragma unroll
       for (int j = 0; j < ACTIVE; j++) {
-        mfma_agpr(p[h][i], q[h][j], acc[i][j]);
+        if (kSettle && j == ACTIVE - 1) mfma_agpr<kSettle>(p[h][i], q[h][j], acc[i][j]);
+        else mfma_agpr<false>(p[h][i], q[h][j], acc[i][j]);
         // (past the end: zeros)
         constexpr int kReads = 4, kPer = ACTIVE >= 8 ? 1 : ACTIVE >= 4 ? 2 : 4;   // reads of a row of MFMAs, after one of them
         if (i < 4 && j >= 1 && (j - 1) * kPer < kReads) {
@@ -354,7 +362,6 @@ __device__ __forceinline__ void contract_large(I issue, L locate, R prepare, A a
     stage_of(std::integral_constant<int, 0>(), kb);
     stage_of(std::integral_constant<int, 1>(), kb + 1);   // (an odd number of stages: one of zeros)
   }
-  settle();
   arrive<0>();
 }
 
