@@ -52,7 +52,7 @@ EXPORTED = [
     "moe_balance_loss_workspace", "moe_balance_loss", "moe_balance_loss_backward",
     "moe_grouped_gemm_bf16_can_implement", "moe_grouped_gemm_bf16",
     "moe_grouped_wgrad_bf16_can_implement", "moe_grouped_wgrad_bf16",
-    "moe_grad_norm_workspace", "moe_grad_norm", "moe_grad_clip",
+    "moe_grad_norm_workspace", "moe_grad_norm", "moe_grad_clip", "moe_grad_clip_can_implement",
     "moe_gemv_nvfp4_can_implement", "moe_gemv_nvfp4",
 ]
 
@@ -174,6 +174,7 @@ def lib():
             "moe_grad_norm_workspace": (sz, [P, i32]),
             "moe_grad_norm": (i32, [P, i32, P, P, sz, P]),
             "moe_grad_clip": (i32, [P, i32, P, C.c_float, P]),
+            "moe_grad_clip_can_implement": (i32, [P, i32, P]),
             "moe_gemv_nvfp4_can_implement": (i32, [gemv_p]),
             "moe_gemv_nvfp4": (i32, [gemv_p, P]),
         }
@@ -548,8 +549,9 @@ class GradList:
     """The tensors of a gradient norm and its clipping, checked and laid out for the library once: `tensors`
     f32 or bf16, dense, on one device; `out` (of the same sizes and types) receives the clipped values, None:
     `tensors` themselves.  It may serve any number of calls, as long as the tensors keep their memory (a
-    tensor given other memory through `.data` or `.grad = ` needs a new GradList).  Clipping needs outputs that do not
-    overlap each other or another tensor; the same one twice is refused."""
+    tensor given other memory through `.data` or `.grad = ` needs a new GradList).  Clipping refuses (the norm
+    does not) what it would write, outputs or `tensors` themselves, where that overlaps anything else of the list: of each
+    tensor, its output may be the tensor itself, or lie apart from all."""
 
     def __init__(self, tensors, out=None):
         fn = "GradList"
@@ -570,15 +572,15 @@ class GradList:
             raise MoeError(fn, MOE_ERR_SHAPE, "each output needs its tensor's number of elements")
         words = [0] * (4 * max(self.count, 1))   # of each moe_tensor: src, dst, n, dtype
         n = 4 * self.count
-        written = words[0:n:4] = list(map(T.data_ptr, ts))
+        words[0:n:4] = map(T.data_ptr, ts)
         if outs is not None:
-            written = words[1:n:4] = list(map(T.data_ptr, outs))
-        # (empty tensors may share an address)
-        self.distinct = len(set(written)) == self.count or len({p for p, s in zip(written, sizes) if s}) == sum(s > 0 for s in sizes)
+            words[1:n:4] = map(T.data_ptr, outs)
         words[2:n:4] = sizes
         words[3:n:4] = [_DTYPES[d] for d in types]
         self._words = array.array("q", words)
         self.items = self._words.buffer_info()[0]
+        scratch = self._words[:]
+        self.distinct = moe_grad_clip_can_implement(self, scratch) != MOE_ERR_UNSUPPORTED
 
 
 def _grad_list(tensors, out=None) -> GradList:
@@ -586,6 +588,15 @@ def _grad_list(tensors, out=None) -> GradList:
         _sized("GradList", out is None, "a GradList has its outputs")
         return tensors
     return GradList(tensors, out)
+
+
+def moe_grad_clip_can_implement(tensors: GradList, scratch: array.array) -> int:
+    return lib().moe_grad_clip_can_implement(tensors.items, tensors.count, scratch.buffer_info()[0])
+
+
+def _clippable(fn: str, g: GradList):
+    if not g.distinct:
+        raise MoeError(fn, MOE_ERR_UNSUPPORTED, "what is written may overlap nothing else of the list, and be in it once only")
 
 
 def moe_grad_norm_workspace(tensors) -> int:
@@ -608,8 +619,7 @@ def moe_grad_norm(tensors, norm, ws=None, stream=None):
 def moe_grad_clip(tensors, norm, max_norm, out=None, stream=None):
     """out (None: `tensors`, or what the GradList has) = tensors * min(1, max_norm / (norm + 1e-6))."""
     g = _grad_list(tensors, out)
-    if not g.distinct:
-        raise MoeError("moe_grad_clip", MOE_ERR_UNSUPPORTED, "a tensor that is written may be in the list once only")
+    _clippable("moe_grad_clip", g)
     _dense("moe_grad_clip", ("norm", norm, _F32))
     _sized("moe_grad_clip", norm.numel() >= 1 and g.device in (None, norm.get_device()), "norm [1] on the tensors' device is needed")
     _current("moe_grad_clip", norm.get_device(), stream)
@@ -998,6 +1008,7 @@ def clip_grad_norm(tensors, max_norm, out=None, stream=None) -> torch.Tensor:
     g = _grad_list(tensors, out)
     if g.count:
         _current("clip_grad_norm", g.device, stream)
+        _clippable("clip_grad_norm", g)
     device = torch.device("cuda", g.device if g.count else torch.cuda.current_device())
     with _allocating(stream):
         norm = torch.empty(1, dtype=torch.float32, device=device)

@@ -8,6 +8,8 @@
 
 #include <math.h>
 
+#include <algorithm>
+
 namespace moe {
 namespace {
 
@@ -88,6 +90,51 @@ moe_status check_tensors(const moe_tensor *tensors, int count) {
     if (total > int64_t(1) << 37) return MOE_ERR_SHAPE;
   }
   return MOE_OK;
+}
+
+struct Range {
+  uint64_t start, end;   // of bytes; the end's low bit (elements have at least two bytes): written
+};
+
+// Whether nothing that clipping writes overlaps another range that is read or written, but a src that it
+// replaces.  scratch: 4 words a tensor.
+bool written_apart(const moe_tensor *tensors, int count, uint64_t *scratch) {
+  auto each_range = [&](auto take) {
+    for (int i = 0; i < count; i++) {
+      const moe_tensor &t = tensors[i];
+      if (t.n == 0) continue;
+      const uint64_t src = reinterpret_cast<uint64_t>(t.src), dst = t.dst ? reinterpret_cast<uint64_t>(t.dst) : src;
+      const uint64_t bytes = static_cast<uint64_t>(t.n) * (t.dtype == MOE_DTYPE_BF16 ? 2 : 4);
+      take(dst, dst + bytes, 1);
+      if (src != dst) take(src, src + bytes, 0);
+    }
+  };
+  // ranges are all apart where each end, in order, is no further than the next start, in order
+  uint64_t *const starts = scratch, *const ends = scratch + 2 * static_cast<int64_t>(count);
+  int64_t n = 0;
+  each_range([&](uint64_t start, uint64_t end, int) {
+    starts[n] = start;
+    ends[n++] = end;
+  });
+  std::sort(starts, starts + n);
+  std::sort(ends, ends + n);
+  bool apart = true;
+  for (int64_t i = 1; i < n; i++) apart &= ends[i - 1] <= starts[i];
+  if (apart) return true;
+  // what is only read may overlap: each range against those that start before it
+  Range *const ranges = reinterpret_cast<Range *>(scratch);
+  n = 0;
+  each_range([&](uint64_t start, uint64_t end, int write) { ranges[n++] = {start, end | write}; });
+  std::sort(ranges, ranges + n, [](const Range &a, const Range &b) { return a.start < b.start; });
+  uint64_t any_end = 0, written_end = 0;
+  for (int64_t i = 0; i < n; i++) {
+    const uint64_t end = ranges[i].end & ~uint64_t(1);
+    const bool write = ranges[i].end & 1;
+    if (ranges[i].start < (write ? any_end : written_end)) return false;
+    any_end = std::max(any_end, end);
+    if (write) written_end = std::max(written_end, end);
+  }
+  return true;
 }
 
 moe_status check_gemv(const moe_gemv_args *a) {
@@ -172,6 +219,13 @@ moe_status moe_grad_clip(const moe_tensor *tensors, int count, const float *norm
   if (!(max_norm >= 0.0f)) return MOE_ERR_SHAPE;
   if (!norm) return MOE_ERR_NULL;
   return launch_status(grad::launch_clip(tensors, count, norm, max_norm, stream));
+}
+
+moe_status moe_grad_clip_can_implement(const moe_tensor *tensors, int count, uint64_t *scratch) {
+  const moe_status st = check_tensors(tensors, count);
+  if (st != MOE_OK) return st;
+  if (count > 0 && !scratch) return MOE_ERR_NULL;
+  return written_apart(tensors, count, scratch) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
 moe_status moe_gemv_nvfp4_can_implement(const moe_gemv_args *args) { return check_gemv(args); }

@@ -527,6 +527,10 @@ moe_status moe_grad_norm(const moe_tensor *tensors, int count, float *norm, void
                          hipStream_t stream);
 moe_status moe_grad_clip(const moe_tensor *tensors, int count, const float *norm, float max_norm,
                          hipStream_t stream);
+/* Whether moe_grad_clip takes the list, once for any number of calls: its checks, and MOE_ERR_UNSUPPORTED where what
+ * is written overlaps another tensor, which moe_grad_clip itself does not look for.  `scratch`: host memory
+ * of 4 * count words. */
+moe_status moe_grad_clip_can_implement(const moe_tensor *tensors, int count, uint64_t *scratch);
 
 /* ---------------------------------------------------------------------------
  * 11. One or a few tokens with NVFP4 weights, activations in bf16.
