@@ -74,7 +74,7 @@ moe_status check_wgrad_bf16(const moe_wgrad_bf16_args *a) {
   return MOE_OK;
 }
 
-// Every tensor of the list; `write`: its dst or src is written.
+// Every tensor of the list, its dst too where only the norm is asked for: one list serves both calls.
 moe_status check_tensors(const moe_tensor *tensors, int count) {
   if (count < 0 || count > 1 << 20) return MOE_ERR_SHAPE;
   if (count > 0 && tensors == nullptr) return MOE_ERR_NULL;

@@ -509,7 +509,7 @@ moe_status moe_grouped_wgrad_bf16(const moe_wgrad_bf16_args *args, hipStream_t s
  *                  in place with s = 1 nothing is written.  What is written (dst, or src in
  *                  place) may overlap no other tensor of the list, nor its own src but as the same address.
  * dtype: MOE_DTYPE_BF16 or MOE_DTYPE_F32, of src and dst.  A tensor need be aligned to its elements
- * only; where src and dst lie on 16 bytes it is read and written 16 bytes at a time.  Several processes' shares
+ * only (dst as well, in either call); where src and dst lie on 16 bytes it is read and written 16 bytes at a time.  Several processes' shares
  * of one model: sum the squares of their norms, and clip by the root of it.
  * Limits: 0 <= count <= 2^20, at most 2^37 elements in all, max_norm >= 0 (not NaN; infinity clips
  * nothing).  ws: moe_grad_norm_workspace(tensors, count) bytes, 16-byte aligned (contents on entry
