@@ -932,71 +932,39 @@ hipError_t run_wgrad(const WgradParams &p, hipStream_t stream) {
 }
 
 constexpr int64_t kCacheBytes = 256 << 20;   // MI355X's memory-side cache
-constexpr int kCus = 256;
 
 template <bool PT>
 using Large = Tile<256, 256, 2, 2, 5, PT, false, 32>;
 
+template <Epilogue MODE, bool PT>
+hipError_t run_tile(GemmTile tile, const GemmParams &p, hipStream_t stream) {
+  if (tile == kSquare256) return run_gemm<Large<PT>, MODE>(p, stream);
+  if constexpr (!PT) {
+    if (tile == kSplit16) return run_split<Split<16, 8, 3>, MODE>(p, stream);
+    if (tile == kSplit32) return run_split<Split<32, 8, 3>, MODE>(p, stream);
+  }
+  if constexpr (MODE == kGated) {
+    return run_gemm<Tile<64, 256, 1, 8, 3, PT>, MODE>(p, stream);
+  } else {
+    if (tile == kSquare128) return run_gemm<Tile<128, 128, 2, 2, 2, PT>, MODE>(p, stream);
+    if (tile == kRows32) return run_gemm<Tile<32, 128, 1, 4, 3, PT>, MODE>(p, stream);
+    return run_gemm<Tile<64, 128, 1, 4, 3, PT>, MODE>(p, stream);
+  }
+}
+
 }  // namespace
 
 hipError_t launch_gemm(GemmParams p, Epilogue epilogue, bool transposed, hipStream_t stream) {
-  const int64_t hit = p.R < p.E ? p.R : p.E;   // at most so many experts have rows
-  if (hit == 0) return hipSuccess;
-  const int64_t mean = p.R / hit;
+  if (p.R == 0) return hipSuccess;
   p.stream_weights = static_cast<int64_t>(p.E) * p.N * p.K * 2 > kCacheBytes / 2;
-  // tiles of q rows by c columns, for groups of the mean size
-  auto items = [&](int q, int c) { return hit * ((mean + q - 1) / q) * ((p.N + c - 1) / c); };
-  // Which tile; times in us, "a | b" for this choice and the next one below, weights 4096 x 6144 each.
-  // - 256 x 256 where groups have more than one 128-row chunk and the tiles are more than half of the CUs, one
-  //   each: 16 groups of 160 rows 201 | 231 (transposed 161 | 243, gated 215 | 260), of 128 182 | 171 (144 | 145,
-  //   190 | 206); 9 of 256: 144 tiles, 190 | 257; 17 of 256, 2048 x 2048: 136 tiles, 50 | 62, 8 of 512: 128 tiles,
-  //   46 | 39; 24 of 384, 784 x 1048: 192 tiles, 31 | 25, of 512 35 | 44.
-  const bool large = mean > 128 && items(256, 256) > kCus / 2;
-  // - 128 x 128 where 64 rows are not enough and there is more than one for each CU: 16 groups of 96 rows
-  //   183 | 206, of 64 151 | 145; 8 of 256, 2048 x 2048: 256 tiles, 28 | 25, of 512: 512 tiles, 38 | 46.
-  const bool middle = mean > 64 && items(128, 128) > kCus;
-  // - The contraction split over a workgroup's waves, 16 x 16 while that is one round of the CUs: one group
-  //   of 16 rows 13.1 | 16.1, of 24 20.4 | 15.4; then 16 x 32 for one round, or two where several chunks
-  //   share weights: one of 64 rows 27 | 39, of 96 39 | 40 (gated 28 | 54, 39 | 53); 8 of one row, 2048 x
-  //   2048: 512 tiles of one chunk each, 16.4 | 13.7.
-  const int split = transposed ? 0 : items(16, 16) <= kCus ? 16 : items(16, 32) <= (mean > 16 ? 2 : 1) * kCus ? 32 : 0;
-  // - 32 x 128 for one round: one group of 128 rows 31 | 42 (transposed 32 | 45, backward 33 | 45), 8 of 64, 2048
-  //   x 2048, 14.6 | 17.4; 8 of 32, 4096 x 2048, 21.8 | 22.1; two rounds, transposed: one of 512 rows 50 | 46.
-  const bool low = items(32, 128) <= kCus;
-  if (epilogue == kGated) {
-    if (large) return run_gemm<Large<false>, kGated>(p, stream);
-    if (split == 16) return run_split<Split<16, 8, 3>, kGated>(p, stream);
-    if (split == 32) return run_split<Split<32, 8, 3>, kGated>(p, stream);
-    return run_gemm<Tile<64, 256, 1, 8, 3, false>, kGated>(p, stream);
-  }
-  if (epilogue == kGatedBackward) {
-    if (large) return run_gemm<Large<true>, kGatedBackward>(p, stream);
-    if (middle) return run_gemm<Tile<128, 128, 2, 2, 2, true>, kGatedBackward>(p, stream);
-    if (low) return run_gemm<Tile<32, 128, 1, 4, 3, true>, kGatedBackward>(p, stream);
-    return run_gemm<Tile<64, 128, 1, 4, 3, true>, kGatedBackward>(p, stream);
-  }
-  if (transposed) {
-    if (large) return run_gemm<Large<true>, kPlain>(p, stream);
-    if (middle) return run_gemm<Tile<128, 128, 2, 2, 2, true>, kPlain>(p, stream);
-    if (low) return run_gemm<Tile<32, 128, 1, 4, 3, true>, kPlain>(p, stream);
-    return run_gemm<Tile<64, 128, 1, 4, 3, true>, kPlain>(p, stream);
-  }
-  if (large) return run_gemm<Large<false>, kPlain>(p, stream);
-  if (split == 16) return run_split<Split<16, 8, 3>, kPlain>(p, stream);
-  if (split == 32) return run_split<Split<32, 8, 3>, kPlain>(p, stream);
-  if (middle) return run_gemm<Tile<128, 128, 2, 2, 2, false>, kPlain>(p, stream);
-  if (low) return run_gemm<Tile<32, 128, 1, 4, 3, false>, kPlain>(p, stream);
-  return run_gemm<Tile<64, 128, 1, 4, 3, false>, kPlain>(p, stream);
+  const GemmTile tile = gemm_tile(p.E, p.N, p.R, epilogue, transposed);
+  if (epilogue == kGated) return run_tile<kGated, false>(tile, p, stream);
+  if (epilogue == kGatedBackward) return run_tile<kGatedBackward, true>(tile, p, stream);
+  return transposed ? run_tile<kPlain, true>(tile, p, stream) : run_tile<kPlain, false>(tile, p, stream);
 }
 
 hipError_t launch_wgrad(const WgradParams &p, bool bf16, hipStream_t stream) {
-  // Large tiles, one for each CU at a time, need a contraction that pays for their start and end, and
-  // enough tiles or enough of it that the last round counts little.  In us, large | small, D binary32:
-  // 16 groups of 384 rows, 4096 x 6144, 477 | 500, of 256 403 | 397; 8 of 1024, 2048 x 2048, 76 | 82, of 512
-  // 54 | 54 (bf16 46 | 41); one of 4096, 4096 x 6144, 207 | 230, of 1024 72 | 65; one of 4096, 2048 x 2048:
-  // 64 tiles, 92 | 53.
-  const int64_t tiles = static_cast<int64_t>(p.E) * ((p.N + 255) / 256) * ((p.K + 255) / 256), mean = p.R / p.E;
-  if (mean >= 384 && tiles >= kCus * 3 / 4 && tiles * mean >= kCus * 2048) {
+  if (wgrad_large(p.E, p.N, p.K, p.R)) {
     using T = Tile<256, 256, 2, 2, 5, true, true, 32>;
     return bf16 ? run_wgrad<T, true>(p, stream) : run_wgrad<T, false>(p, stream);
   }

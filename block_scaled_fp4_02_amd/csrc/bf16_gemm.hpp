@@ -1,12 +1,11 @@
 // Parameters and launchers of the bf16 grouped products (not part of the ABI).
 #pragma once
 
+#include "bf16_tiles.hpp"
 #include "common.hpp"
 
 namespace moe {
 namespace bf16 {
-
-enum Epilogue { kPlain, kGated, kGatedBackward };
 
 struct GemmParams {
   const uint16_t *A;        // [rows_A, K]
