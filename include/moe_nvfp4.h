@@ -540,7 +540,7 @@ moe_status moe_grad_clip_can_implement(const moe_tensor *tensors, int count, uin
  * e = ids[t, j] (ids NULL: k = 1, e = 0, a dense projection):
  *   y[t, j, n] = B_gs[e] * sum_kb sB[e, n, kb] sum_{i<16} x[r, 16kb+i] b[e, n, 16kb+i]
  * with r = t where rows_x == T, and r = t*k + j where rows_x == T*k; products are exact and sums
- * binary32 (a bf16 denormal counts as zero or as its value).  No permutation and no quantisation of the tokens come before it.
+ * binary32 (a bf16 denormal counts as its value).  No permutation and no quantisation of the tokens come before it.
  * Epilogues:
  *   MOE_EPI_NONE      D bf16 [T*k, N]: bf16(y[t, j, n]).
  *   MOE_EPI_SWIGLU    N = 2I, gate columns first: D bf16 [T*k, I]: bf16(silu(g) u), unrounded sums

@@ -240,3 +240,17 @@ def test_offsets_past_32_bits():
     for B in _layouts(W):
         D = moe.gemv_nvfp4_alloc(x, B, ids)
         assert torch.equal(D[0].double(), ref.bf16(want)) and not D[1].any()
+
+
+@pytest.mark.parametrize("T", [1, 3, 7, 16])
+def test_denormals_count(T):
+    """Elements below the least normal number meet weights of 1 and more at their value; sums of eight-bit values are exact."""
+    g = _gen(T)
+    N, K = 64, 256
+    W = moe.NVFP4Tensor(torch.randint(0, 256, (1, N, K // 2), generator=g, device="cuda").to(torch.uint8),
+                        torch.full((1, N, K // 16), 0x38, dtype=torch.uint8, device="cuda"), torch.full((1,), 2.0 ** 100, device="cuda"))
+    x = (torch.randint(-100, 101, (T, K), generator=g, device="cuda").float() * 2.0 ** -133).to(BF16)   # multiples of the least one
+    assert (x.abs() < 2.0 ** -126).all() and x.any()
+    want = x.double() @ ref.nvfp4_values(W.q, W.sf, W.gs)[0].T
+    for B in _layouts(W):
+        assert torch.equal(moe.gemv_nvfp4_alloc(x, B).double(), ref.bf16(want))
