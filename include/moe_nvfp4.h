@@ -442,8 +442,9 @@ moe_status moe_balance_loss_backward(const float *logits, int T, int E, const in
  *   MOE_EPI_NONE    D bf16 [R, N]: D[p, n] = bf16(y[p, n]).
  *   MOE_EPI_SWIGLU  row-major B, N = 2I; columns [0, I) are gate g, [I, 2I) are up u:
  *                   D bf16 [R, I]: D[p, i] = bf16(silu(g) u) of the unrounded sums (hardware exp2
- *                   and reciprocal: a few ulp of binary32); with Z != NULL also Z bf16 [R, 2I] =
- *                   bf16(y), which the backward pass reads.
+ *                   and reciprocal: a few ulp of binary32; a sigmoid below 2^-126, g < -87.3, counts as
+ *                   zero, here and in the backward pass); with Z != NULL also Z bf16 [R, 2I] = bf16(y),
+ *                   which the backward pass reads.
  *   MOE_EPI_SWIGLU_BACKWARD  transposed B (the down projection W2 [E, K = H, N = I], A the gradient
  *                   of its output): y is the gradient of the activations; with g, u of Z bf16
  *                   [R, 2N] and s = 1 / (1 + exp(-g)), D bf16 [R, 2N] receives
@@ -544,7 +545,7 @@ moe_status moe_grad_clip_can_implement(const moe_tensor *tensors, int count, uin
  * Epilogues:
  *   MOE_EPI_NONE      D bf16 [T*k, N]: bf16(y[t, j, n]).
  *   MOE_EPI_SWIGLU    N = 2I, gate columns first: D bf16 [T*k, I]: bf16(silu(g) u), unrounded sums
- *                     (hardware exp2 and reciprocal).
+ *                     (hardware exp2 and reciprocal, as in section 9).
  *   MOE_EPI_FINALIZE  D bf16 [T, N]: bf16(sum_j topk_w[t, j] y[t, j, n]) in binary32; topk_w NULL: 1.
  * An id outside [0, E) is a dropped slot: its row of D is zeros, and it adds nothing to a sum.  A token
  * may name an expert twice.  Tokens that share an expert share the read of its weights, 16 tokens at a time.

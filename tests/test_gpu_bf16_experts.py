@@ -359,3 +359,25 @@ def test_offsets_past_32_bits():
     Wt = _ints(g, 2, 16, C, most=1)   # as the transposed operand: results [R, C]
     moe.moe_grouped_gemm_bf16(moe.make_gemm_bf16_args(x, Wt, off, R, 0, big, B_layout=TR))
     assert torch.equal(big[-40:].double(), ref.bf16(x[-40:].double() @ Wt[1].double()))
+
+
+def test_sigmoids_far_out():
+    """Gates where the sigmoid leaves binary32's normal range, with factors that make it count: below 2^-126 it
+    may be zero, everywhere else it keeps its bound; in every kernel that takes one."""
+    gates = torch.tensor([-80.0, -86.5, -87.0, -87.5, -88.0, -88.5, -89.0, -95.0, -100.0, -104.0, -120.0, 80.0, 87.5, 89.0, 104.0, 120.0], device="cuda")
+    n, I, big = 16, 64, 2.0 ** 100
+    for rows in ([n], [n] * 40):
+        off, R = _offsets(rows), sum(rows)
+        A = torch.zeros(R, 64, dtype=BF16, device="cuda")
+        A[:, 0], A[:, 1] = gates.repeat(len(rows)).to(BF16), 1.0
+        W = torch.zeros(len(rows), 2 * I, 64, dtype=BF16, device="cuda")
+        W[:, :I, 0], W[:, I:, 1] = 1.0, big
+        act, z = moe.gated_ffn_alloc(A, W, off, R)
+        y, _ = ref.product(A, W, off)
+        gate, up = y.chunk(2, 1)
+        assert ref.close(act, ref.swiglu(y), ref.swiglu_error(y) + (gate * up).abs() * 2.0 ** -126)
+        W2 = torch.zeros(len(rows), 64, I, dtype=BF16, device="cuda")
+        W2[:, 1] = 1.0
+        dz = moe.gated_ffn_backward_alloc(A, W2, z, off, R)
+        want, err = ref.swiglu_backward(torch.ones_like(gate), z.double())
+        assert ref.close(dz, want, err + torch.cat([up * (1 + gate.abs()), gate.abs()], 1).abs() * 2.0 ** -126)
