@@ -1030,7 +1030,7 @@ def gemv_nvfp4_alloc(x: torch.Tensor, B, ids=None, topk_w=None, epilogue=MOE_EPI
 class MoETokenPlan:
     """The layer of MoELayerPlan for one or a few tokens: the same weights (NVFP4Tensor or PackedWeights), the
     tokens and activations left in bf16, and three calls: routing, gate/up products with SwiGLU, down products
-    with the weighted sum.  Buffers are allocated once."""
+    with the weighted sum.  Buffers are allocated once.  From about five tokens on MoELayerPlan is faster."""
 
     def __init__(self, T: int, E: int, k: int, H: int, I: int, W1, W2, device="cuda"):
         self.T, self.E, self.k, self.H, self.I = T, E, k, H, I

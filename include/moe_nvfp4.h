@@ -548,7 +548,8 @@ moe_status moe_grad_clip_can_implement(const moe_tensor *tensors, int count, uin
  *                     (hardware exp2 and reciprocal, as in section 9).
  *   MOE_EPI_FINALIZE  D bf16 [T, N]: bf16(sum_j topk_w[t, j] y[t, j, n]) in binary32; topk_w NULL: 1.
  * An id outside [0, E) is a dropped slot: its row of D is zeros, and it adds nothing to a sum.  A token
- * may name an expert twice.  Tokens that share an expert share the read of its weights, 16 tokens at a time.
+ * may name an expert twice.  Tokens that share an expert share the read of its weights, 16 tokens at a time; from
+ * about five tokens on sections 2 to 6 are faster.
  * Supported: 0 <= T <= 4096, 1 <= k <= 32, 1 <= E <= 65536, N % 16 == 0 (SWIGLU: N % 32 == 0), K % 32
  * == 0 (packed: K % 256 == 0), N, K <= 2^20; MOE_ERR_SHAPE or MOE_ERR_UNSUPPORTED otherwise.  No workspace.
  * ------------------------------------------------------------------------- */
